@@ -348,6 +348,133 @@ int spec_commit_accepted_path(void* cache, int32_t B, int32_t n_planes, int32_t 
                               spec_stream_t stream);
 
 /*
+ * Paged key / value caches.  One cache (keys or values of one layer) is device memory
+ * whose element (page, slot, head, d) lies at
+ *   cache + page * page_stride + slot * pos_stride + head * head_stride + d
+ * (strides in elements, so both [pages, slots, heads, d] and [pages, heads, slots, d] fit);
+ * position t of sequence b is slot t % page_size of page page_table[b * max_pages +
+ * t / page_size].  page_size is any number >= 1.  page_table [B, max_pages] is a device
+ * int32 array; a page number outside [0, n_pages) holds nothing: its positions are masked
+ * for attention, not written by an append and not moved by a commit.  Lengths are read on the
+ * device; a negative length counts as 0, a count above N as N.
+ * As in spec_commit_accepted_path, node n of tree b sits at position prefix_len[b] + n.
+ */
+typedef struct {
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  int64_t page_stride, pos_stride, head_stride; /* elements */
+} spec_paged_layout;
+
+/* Strides (elements) of a [B, N, heads, head_dim] array with contiguous head vectors. */
+typedef struct {
+  int64_t batch_stride, node_stride, head_stride;
+} spec_node_layout;
+
+/* Positions one page table row can cover (max_pages * page_size). */
+#define SPEC_MAX_POSITIONS 0x7ffff000
+/* Largest head dimension of spec_tree_attention_paged and of spec_paged_append_rope. */
+#define SPEC_ATTN_MAX_HEAD_DIM 128
+#define SPEC_APPEND_MAX_HEAD_DIM 1024
+
+/* The rotated pairs of a head are (2 i, 2 i + 1) instead of (i, i + rot_dim / 2). */
+#define SPEC_ROPE_INTERLEAVED 1u
+
+/*
+ * Append the keys and values of B x N tokens (the nodes of a draft tree, the next token, a
+ * prompt) to a paged cache, the keys' rotary rotation applied on the way, and rotate the
+ * tokens' queries.  Token (b, n), n < counts[b] (counts NULL: N), is stored at position
+ * prefix_len[b] + n and rotated by r = prefix_len[b] + position_ids[b][n] (NULL: n); with
+ * the depths spec_tree_build writes to out_position_ids an accepted node already carries
+ * the rotation of the position a commit moves it to.
+ *   x'[i] = x[i] cos_r[i] - x[i+h] sin_r[i],  x'[i+h] = x[i+h] cos_r[i] + x[i] sin_r[i],
+ *   h = rot_dim / 2, i < h; elements from rot_dim on pass through; fp32 arithmetic, rounded
+ *   once.  cos_sin [n_positions, rot_dim] float32 (device): row r holds cos_r[0..h), then
+ *   sin_r[0..h).  rot_dim 0: no rotation (cos_sin may be NULL).
+ * q [B, N, n_q_heads, head_dim] (n_q_heads 0: none) -> out_q (may be q itself); k, v
+ *   [B, N, n_kv_heads, head_dim]; all of `dtype`, each with its own strides (views of one
+ *   fused projection, say).
+ * A token with n >= counts[b], or whose r is outside the table, is not stored and its
+ *   rotated queries are 0; a token whose position has no page is not stored.
+ * Bases and strides are multiples of 16 bytes, head_dim of 16 bytes and rot_dim of 32.
+ * The positions written must be distinct.  Asynchronous on `stream`; allocates nothing.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED_DTYPE, SPEC_ERR_MISALIGNED,
+ * SPEC_ERR_TOO_LARGE (head_dim > SPEC_APPEND_MAX_HEAD_DIM, B * N above 2^31 - 1, max_pages *
+ * page_size above SPEC_MAX_POSITIONS), SPEC_ERR_CUDA.
+ */
+int spec_paged_append_rope(const void* q, spec_node_layout q_layout, void* out_q,
+                           spec_node_layout out_q_layout, const void* k,
+                           spec_node_layout k_layout, const void* v, spec_node_layout v_layout,
+                           spec_dtype dtype, int32_t B, int32_t N, int32_t n_q_heads,
+                           void* k_cache, void* v_cache, spec_paged_layout cache,
+                           const int32_t* page_table, int32_t max_pages,
+                           const int32_t* prefix_len, const int32_t* counts,
+                           const int32_t* position_ids, const float* cos_sin,
+                           int32_t n_positions, int32_t rot_dim, uint32_t flags,
+                           spec_stream_t stream);
+
+/*
+ * Attention of B x N query tokens over a paged cache: the target model's attention in a
+ * tree verify step ("LLM speculative decoding: EAGLE", jingming.pro, section 3.4: the whole
+ * candidate tree is verified in one pass under a tree attention mask), and with N = 1 or a
+ * causal mask single-token decoding and prompts.
+ *   out[b][n][h] = sum_t p_t v_t,  p = softmax over the visible t of scale * q . k_t,
+ *   lse[b][n][h] = ln sum_t exp(scale * q . k_t)
+ * Query (b, n), n < counts[b] (NULL: N), sees every position t < prefix_len[b], and position
+ *   prefix_len[b] + j for the j < counts[b] with mask[b][n][j] != 0 (mask [B, N, N] uint8,
+ *   the ancestor mask of spec_tree_build; NULL: j <= n).  Query head h reads key head
+ *   h / (n_q_heads / n_kv_heads).  What a query does not see never reaches its result, whatever
+ *   it holds (NaN and infinities included).  A query that sees nothing, and one with n >=
+ *   counts[b], gives out 0 and lse -inf.
+ * shared_len: the first shared_len positions of every sequence are the same (a system
+ *   prompt): they are read through row 0 of page_table and once for all sequences' queries.
+ *   0 or a multiple of page_size.  A sequence with prefix_len < shared_len sees nothing.
+ * q and out [B, N, n_q_heads, head_dim] of `dtype` (device), lse [B, N, n_q_heads] float32
+ *   (optional).  Scores, softmax statistics and sums are fp32; with SPEC_BF16 the
+ *   exponentials are rounded to bf16 for the product with the values (their sum is not), and
+ *   the result is rounded once.
+ * workspace: device, 256-byte aligned, spec_tree_attention_workspace_size() bytes; not
+ *   initialised by the caller, not preserved between calls.
+ * Bases and strides are multiples of 16 bytes and head_dim of 16 bytes, head_dim <=
+ * SPEC_ATTN_MAX_HEAD_DIM.  Asynchronous on `stream`; allocates nothing.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED_DTYPE, SPEC_ERR_MISALIGNED,
+ * SPEC_ERR_WORKSPACE, SPEC_ERR_TOO_LARGE (head_dim, B * N * n_q_heads >= 2^30, max_pages *
+ * page_size above SPEC_MAX_POSITIONS), SPEC_ERR_CUDA.  The size function returns 0 for
+ * invalid sizes.
+ */
+size_t spec_tree_attention_workspace_size(int32_t B, int32_t N, int32_t n_q_heads,
+                                          int32_t n_kv_heads, int32_t head_dim,
+                                          int32_t shared_len, spec_dtype dtype);
+int spec_tree_attention_paged(const void* q, spec_node_layout q_layout, const void* k_cache,
+                              const void* v_cache, spec_paged_layout cache, spec_dtype dtype,
+                              int32_t B, int32_t N, int32_t n_q_heads,
+                              const int32_t* page_table, int32_t max_pages,
+                              const int32_t* prefix_len, const int32_t* counts,
+                              const uint8_t* mask, int32_t shared_len, float scale, void* out,
+                              spec_node_layout out_layout, float* lse, void* workspace,
+                              size_t workspace_bytes, spec_stream_t stream);
+
+/*
+ * spec_commit_accepted_path on a paged cache: for k = 1 .. accept_len[b], position
+ * prefix_len[b] + k receives the row of position prefix_len[b] + accepted_path[b][k], in
+ * every plane (a layer's K or V) and head.
+ * cache: device bytes; the row of (plane, page, slot, head) is the row_bytes bytes at
+ *   cache + plane * plane_stride + page * page_stride + slot * pos_stride + head * head_stride
+ *   (strides in bytes; heads that lie side by side may be given as one head of wider rows).
+ * A path increases strictly (accepted_path[b][k] >= k), as the verify step writes it.  Moves
+ *   with a source or destination that has no page are skipped, trees with accept_len < 1
+ *   left as they are.
+ * The cache, strides and row_bytes must be multiples of 16 bytes.  Asynchronous on `stream`;
+ *   allocates nothing.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_MISALIGNED, SPEC_ERR_TOO_LARGE, SPEC_ERR_CUDA.
+ */
+int spec_commit_accepted_path_paged(void* cache, int32_t B, int32_t n_planes, int32_t n_heads,
+                                    int32_t n_pages, int32_t page_size, int64_t plane_stride,
+                                    int64_t page_stride, int64_t pos_stride,
+                                    int64_t head_stride, int64_t row_bytes,
+                                    const int32_t* page_table, int32_t max_pages,
+                                    const int32_t* prefix_len, const int32_t* accepted_path,
+                                    const int32_t* accept_len, int32_t W, spec_stream_t stream);
+
+/*
  * Per-request sampling parameters: spec_verify_tree_phases with each tree verified
  * under its own temperature, top-k and top-p (a batch that serves requests with
  * different sampling settings).  temperature [B] (required), top_k [B] and top_p [B]

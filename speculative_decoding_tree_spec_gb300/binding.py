@@ -36,6 +36,10 @@ SPEC_PHASE_ALL_FUSED = 15
 SPEC_MAX_NODES = 4096
 SPEC_MAX_VOCAB = 1 << 21
 SPEC_STATIC_WORKSPACE_BYTES = 1 << 20
+SPEC_ATTN_MAX_HEAD_DIM = 128
+SPEC_APPEND_MAX_HEAD_DIM = 1024
+SPEC_MAX_POSITIONS = 0x7FFFF000
+SPEC_ROPE_INTERLEAVED = 1
 ERRORS = {0: "SPEC_OK", -1: "SPEC_ERR_INVALID_ARG", -2: "SPEC_ERR_UNSUPPORTED_DTYPE",
           -3: "SPEC_ERR_MISALIGNED", -4: "SPEC_ERR_WORKSPACE", -5: "SPEC_ERR_CUDA",
           -6: "SPEC_ERR_TOO_LARGE"}
@@ -57,6 +61,18 @@ class Counters(ctypes.Structure):
                 ("walk_bytes", ctypes.c_uint64), ("residual_passes", ctypes.c_uint64),
                 ("final_draws", ctypes.c_uint64), ("fallback_rows", ctypes.c_uint64),
                 ("reserved", ctypes.c_uint64 * 2)]
+
+
+class PagedLayout(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("pos_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class NodeLayout(ctypes.Structure):
+    _fields_ = [("batch_stride", ctypes.c_int64), ("node_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
 
 
 class SpecError(RuntimeError):
@@ -103,6 +119,19 @@ def lib():
             L.spec_commit_accepted_path.argtypes = [P, i32, i32, i32, i64, i64, i64, i64, P, P, P,
                                                     i32, P]
             L.spec_commit_accepted_path.restype = ctypes.c_int
+            L.spec_paged_append_rope.argtypes = [
+                P, NodeLayout, P, NodeLayout, P, NodeLayout, P, NodeLayout, ctypes.c_int, i32, i32,
+                i32, P, P, PagedLayout, P, i32, P, P, P, P, i32, i32, ctypes.c_uint32, P]
+            L.spec_paged_append_rope.restype = ctypes.c_int
+            L.spec_tree_attention_workspace_size.argtypes = [i32] * 6 + [ctypes.c_int]
+            L.spec_tree_attention_workspace_size.restype = ctypes.c_size_t
+            L.spec_tree_attention_paged.argtypes = [
+                P, NodeLayout, P, P, PagedLayout, ctypes.c_int, i32, i32, i32, P, i32, P, P, P, i32,
+                ctypes.c_float, P, NodeLayout, P, P, ctypes.c_size_t, P]
+            L.spec_tree_attention_paged.restype = ctypes.c_int
+            L.spec_commit_accepted_path_paged.argtypes = [
+                P, i32, i32, i32, i32, i32, i64, i64, i64, i64, i64, P, i32, P, P, P, i32, P]
+            L.spec_commit_accepted_path_paged.restype = ctypes.c_int
             L.spec_verify_tree_per_request.argtypes = [
                 ctypes.c_uint32, P, P, ctypes.c_int, i32, i32, i32, ctypes.c_int64, ctypes.c_int64,
                 P, P, i32, P, P, P, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64,
@@ -403,6 +432,166 @@ def commit_accepted_path(cache: torch.Tensor, prefix_len: torch.Tensor, accepted
         accept_len.data_ptr(), accepted_path.shape[1], _stream_ptr(stream))
     if rc != 0:
         raise SpecError(rc, "spec_commit_accepted_path")
+
+
+def _int32(t, shape, dev, what):
+    """The address of a contiguous int32 device tensor of this shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {dev}")
+    return t.data_ptr()
+
+
+def _paged_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PagedLayout:
+    """The layout of [n_pages, page_size, heads, head_dim] caches (any strides, head vectors
+    contiguous; [n_pages, heads, page_size, head_dim] storage comes as a transposed view)."""
+    st = k_cache.stride()
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or st != v_cache.stride() or \
+            k_cache.dtype != v_cache.dtype or k_cache.device != v_cache.device:
+        raise ValueError("k_cache and v_cache must be 4-d and share shape, strides and dtype")
+    if st[3] != 1 and k_cache.shape[3] > 1:
+        raise ValueError("head vectors must be contiguous")
+    n_pages, page_size, heads, dim = k_cache.shape
+    return PagedLayout(n_pages, page_size, heads, dim, st[0], st[1], st[2])
+
+
+def _nodes(t: torch.Tensor, like: torch.Tensor, B: int, N: int, dim: int, what: str) -> NodeLayout:
+    st = t.stride()
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N or t.shape[3] != dim or \
+            (st[3] != 1 and dim > 1):
+        raise ValueError(f"{what} must be [B, N, heads, head_dim] = [{B}, {N}, heads, {dim}] with "
+                         "contiguous head vectors")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{what} must share the cache's dtype and device")
+    return NodeLayout(st[0], st[1], st[2])
+
+
+def paged_append_rope(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, page_table: torch.Tensor, prefix_len: torch.Tensor,
+                      cos_sin=None, *, position_ids=None, counts=None, interleaved: bool = False,
+                      out_q=None, stream=None):
+    """spec_paged_append_rope: keys and values [B, N, heads, head_dim] of new tokens (views
+    with any strides) into the paged caches [n_pages, page_size, heads, head_dim], in place,
+    at positions prefix_len[b] + n, the keys rotated by prefix_len[b] + position_ids[b][n]
+    (default n; the position_ids of tree_build for a draft tree).  cos_sin [n_positions,
+    rot_dim] float32: the cosines, then the sines (None: no rotation).  counts [B] int32:
+    tokens n >= counts[b] are padding.  Returns the rotated queries (out_q, or a new tensor;
+    None if q is None)."""
+    cache = _paged_cache(k_cache, v_cache)
+    B, N = k.shape[:2]
+    D, dev = cache.head_dim, k_cache.device
+    lk, lv = _nodes(k, k_cache, B, N, D, "k"), _nodes(v, k_cache, B, N, D, "v")
+    if k.shape[2] != cache.n_kv_heads or v.shape[2] != cache.n_kv_heads:
+        raise ValueError("k and v must have the cache's heads")
+    if q is not None:
+        lq = _nodes(q, k_cache, B, N, D, "q")
+        if out_q is None:
+            out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        elif out_q.shape != q.shape:
+            raise ValueError("out_q must have the shape of q")
+        lo = _nodes(out_q, k_cache, B, N, D, "out_q")
+    else:
+        lq = lo = NodeLayout(0, 0, 0)
+    n_positions = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or \
+                cos_sin.device != dev:
+            raise TypeError("cos_sin must be a contiguous float32 [n_positions, rot_dim] tensor")
+        n_positions, rot = cos_sin.shape
+    max_pages = page_table.shape[-1]
+    rc = lib().spec_paged_append_rope(
+        None if q is None else q.data_ptr(), lq, None if q is None else out_q.data_ptr(), lo,
+        k.data_ptr(), lk, v.data_ptr(), lv, _dtype_code(k_cache), B, N,
+        0 if q is None else q.shape[2], k_cache.data_ptr(), v_cache.data_ptr(), cache,
+        _int32(page_table, (B, max_pages), dev, "page_table"), max_pages,
+        _int32(prefix_len, (B,), dev, "prefix_len"), _int32(counts, (B,), dev, "counts"),
+        _int32(position_ids, (B, N), dev, "position_ids"),
+        None if cos_sin is None else cos_sin.data_ptr(), n_positions, rot,
+        SPEC_ROPE_INTERLEAVED if interleaved else 0, _stream_ptr(stream))
+    if rc != 0:
+        raise SpecError(rc, "spec_paged_append_rope")
+    return out_q if q is not None else None
+
+
+def tree_attention_workspace_size(B: int, N: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                  shared_len: int = 0, dtype=torch.bfloat16) -> int:
+    code = SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F32
+    return int(lib().spec_tree_attention_workspace_size(B, N, n_q_heads, n_kv_heads, head_dim,
+                                                        shared_len, code))
+
+
+def tree_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         page_table: torch.Tensor, prefix_len: torch.Tensor, scale=None, *,
+                         mask=None, counts=None, shared_len: int = 0, out=None, lse=None,
+                         workspace=None, stream=None) -> dict:
+    """spec_tree_attention_paged: attention of q [B, N, heads, head_dim] over the paged caches
+    [n_pages, page_size, kv_heads, head_dim]: query (b, n) sees the prefix_len[b] positions
+    before the tree and the drafts j with mask[b, n, j] != 0 (mask [B, N, N] uint8 as tree_build
+    gives it; None: j <= n, which is decoding at N = 1 and a prompt otherwise).  scale defaults
+    to head_dim ** -0.5.  shared_len: positions that all sequences share, read once.  Returns
+    {"out": [B, N, heads, head_dim], "lse": [B, N, heads] float32 natural logarithm}."""
+    cache = _paged_cache(k_cache, v_cache)
+    B, N, H, D = q.shape
+    dev = k_cache.device
+    if D != cache.head_dim:
+        raise ValueError("q and the caches must share head_dim")
+    lq = _nodes(q, k_cache, B, N, D, "q")
+    if out is None:
+        out = torch.empty((B, N, H, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    lo = _nodes(out, k_cache, B, N, D, "out")
+    if lse is None:
+        lse = torch.empty((B, N, H), dtype=torch.float32, device=dev)
+    elif lse.shape != (B, N, H) or lse.dtype != torch.float32 or not lse.is_contiguous() or \
+            lse.device != dev:
+        raise TypeError("lse must be a contiguous float32 [B, N, heads] tensor")
+    if mask is not None and (mask.dtype not in (torch.uint8, torch.bool) or mask.device != dev or
+                             mask.shape != (B, N, N) or not mask.is_contiguous()):
+        raise TypeError("mask must be a contiguous uint8 or bool [B, N, N] tensor")
+    dt = _dtype_code(k_cache)
+    if workspace is None:
+        ws = lib().spec_tree_attention_workspace_size(B, N, H, cache.n_kv_heads, D, shared_len, dt)
+        workspace = torch.empty(max(int(ws), 256), dtype=torch.uint8, device=dev)
+    max_pages = page_table.shape[-1]
+    rc = lib().spec_tree_attention_paged(
+        q.data_ptr(), lq, k_cache.data_ptr(), v_cache.data_ptr(), cache, dt, B, N, H,
+        _int32(page_table, (B, max_pages), dev, "page_table"), max_pages,
+        _int32(prefix_len, (B,), dev, "prefix_len"), _int32(counts, (B,), dev, "counts"),
+        None if mask is None else mask.data_ptr(), int(shared_len),
+        D ** -0.5 if scale is None else float(scale), out.data_ptr(), lo, lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+    if rc != 0:
+        raise SpecError(rc, "spec_tree_attention_paged")
+    return {"out": out, "lse": lse}
+
+
+def commit_accepted_path_paged(cache: torch.Tensor, page_table: torch.Tensor,
+                               prefix_len: torch.Tensor, accepted_path: torch.Tensor,
+                               accept_len: torch.Tensor, stream=None) -> None:
+    """spec_commit_accepted_path_paged on a device cache [planes, n_pages, page_size, heads,
+    head_dim] (or [planes, n_pages, page_size, row]; any dtype and strides, head vectors
+    contiguous), in place: planes are a layer's keys or values."""
+    if cache.dim() == 4:
+        cache = cache.unsqueeze(3)
+    if cache.dim() != 5 or (cache.stride(4) != 1 and cache.shape[4] > 1):
+        raise ValueError("cache must be [planes, n_pages, page_size, heads, head_dim] with "
+                         "contiguous head vectors")
+    P, n_pages, page_size, H, D = cache.shape
+    st, es = cache.stride(), cache.element_size()
+    if st[3] == D:  # heads side by side: one wider row
+        H, D = 1, H * D
+    B, W = accepted_path.shape
+    dev, max_pages = cache.device, page_table.shape[-1]
+    rc = lib().spec_commit_accepted_path_paged(
+        cache.data_ptr(), B, P, H, n_pages, page_size, st[0] * es, st[1] * es, st[2] * es,
+        0 if H == 1 else st[3] * es, D * es, _int32(page_table, (B, max_pages), dev, "page_table"),
+        max_pages, _int32(prefix_len, (B,), dev, "prefix_len"),
+        _int32(accepted_path, (B, W), dev, "accepted_path"),
+        _int32(accept_len, (B,), dev, "accept_len"), W, _stream_ptr(stream))
+    if rc != 0:
+        raise SpecError(rc, "spec_commit_accepted_path_paged")
 
 
 def draft_topk(logits: torch.Tensor, k: int, temperature: float = 1.0, stream=None) -> dict:

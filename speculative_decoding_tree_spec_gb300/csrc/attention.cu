@@ -1,0 +1,750 @@
+// attention.cu -- attention of draft trees, single tokens and prompts over a paged cache:
+// the few-rows kernel, the join of split tiles, and the entry point.
+//
+//   out = sum_t p_t v_t / sum_t p_t,  p_t = 2^(c q.k_t - m),  c = scale log2(e),
+// in one pass over the keys with a running maximum m: when it rises the sum and the output
+// taken so far are scaled by 2^(m_old - m_new).  A part of the keys gives (m, l, o); two
+// parts join as m = max, l = l1 2^(m1 - m) + l2 2^(m2 - m), o likewise.
+#include <cuda_bf16.h>
+
+#include <cfloat>
+#include <cmath>
+
+#include "attention.cuh"
+
+namespace svk {
+
+namespace {
+
+constexpr int kRowsR = 16;       // rows of a tile: one m16 fragment
+constexpr int kRowsWarps = 4;    // each takes every fourth group of keys
+constexpr int kRowsThreads = 32 * kRowsWarps;
+constexpr int kGroup = 16;       // keys of a warp's step
+constexpr int kRowsKB = kGroup * kRowsWarps;
+constexpr int kCombineRows = 16;
+constexpr int kCombineThreads = 128;
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool real) {
+  const int n = real ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "r"(n)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo with both parts tf32: the products hi hi + hi lo + lo hi carry an fp32
+// product to about 2^-21.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(hi) : "f"(x));
+  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+// The same for a value that may be infinite: hi carries it, lo is 0.
+__device__ __forceinline__ void split_tf32_inf(float x, uint32_t& hi, uint32_t& lo) {
+  split_tf32(x, hi, lo);
+  if ((hi & 0x7f800000u) == 0x7f800000u) lo = 0u;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T> __device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ uint16_t from_float<uint16_t>(float x) {
+  return __bfloat16_as_ushort(__float2bfloat16(x));
+}
+
+// Whether a 16-byte unit holds an infinity or a NaN.
+template <typename T> __device__ __forceinline__ bool unit_nonfinite(const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(T) == 4) {
+      bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
+    } else {
+      bad |= (w[i] & 0x7f800000u) == 0x7f800000u || (w[i] & 0x7f80u) == 0x7f80u;
+    }
+  }
+  return bad;
+}
+
+// One row's result: its part (m, l, o[0..n) of columns c0..) joined with the shared
+// positions' result and written, or, in the shared phase, left for that join.
+template <typename T, int C>
+__device__ __forceinline__ void write_row(const AttnJob& job, const AttnTile& t, int head, int r,
+                                          int c0, int DP, float m, float l, float (&o)[C]) {
+  int b, node, g;
+  if (!attn_row(job, t, r, b, node, g)) return;
+  if (job.phase == kShared) {
+    const int64_t row = (int64_t)head * job.B * job.N * job.G + r;
+    const float inv = 1.f / l;  // l > 0: every row of the shared positions sees them
+    float4* dst = reinterpret_cast<float4*>(job.shared_o + row * DP + c0);
+#pragma unroll
+    for (int i = 0; i < C; i += 4)
+      dst[i / 4] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+    if (c0 == 0) job.shared_lse[row] = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+    return;
+  }
+  const bool real = node < t.count;
+  float lse2;
+  if (!real) {
+    lse2 = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = 0.f;
+  } else {
+    float w = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
+    lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+    const float* so = nullptr;
+    if (job.shared_len > 0) {
+      const int64_t row =
+          ((int64_t)head * job.B + b) * job.N * job.G + (int64_t)node * job.G + g;
+      const float s2 = job.shared_lse[row];
+      if (s2 != -CUDART_INF_F) {
+        so = job.shared_o + row * DP + c0;
+        const float top = fmaxf(s2, lse2);
+        const float es = exp2f(s2 - top);
+        const float eo = lse2 == -CUDART_INF_F ? 0.f : exp2f(lse2 - top);
+        ws = es / (es + eo);
+        w = l == 0.f ? 0.f : eo / (es + eo) / l;
+        lse2 = top + log2f(es + eo);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float x = l == 0.f ? 0.f : o[i] * w;
+      if (so) x += so[i] * ws;
+      o[i] = x;
+    }
+  }
+  const int h = head * job.G + g;
+  T* dst = static_cast<T*>(job.out) + b * job.lo.batch_stride + node * job.lo.node_stride +
+           h * job.lo.head_stride;
+  constexpr int E = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < C; i += E) {
+    if (c0 + i < job.D) {
+      T x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = from_float<T>(o[i + e]);
+      *reinterpret_cast<uint4*>(dst + c0 + i) = *reinterpret_cast<const uint4*>(x);
+    }
+  }
+  if (c0 == 0 && job.lse)
+    job.lse[((int64_t)b * job.N + node) * job.Hq + h] = lse2 * 0.693147180559945309f;
+}
+
+// Infinities and NaN among the draft positions' values [from, to) that row (node) sees.  A
+// tile in which some rows do not see a key multiplies it by 0 for them, so such values are
+// taken out of the product (as 0) and added here for the rows that do see them.
+template <typename T, int C>
+__device__ __noinline__ void add_nonfinite(const AttnJob& job, const AttnTile& t, int head,
+                                           int node, int from, int to, int c0, float* o) {
+  const int32_t* row = job.table + (int64_t)t.b * job.max_pages;
+  for (int pos = from; pos < to; ++pos) {
+    if (!attn_sees_draft(job, t, node, pos)) continue;
+    const int64_t off = paged_offset(row, job.max_pages, job.n_pages, job.pd, job.page_stride,
+                                     job.pos_stride, pos);
+    if (off < 0) continue;
+    const T* v = static_cast<const T*>(job.v) + off + head * job.head_stride;
+    for (int i = 0; i < C && c0 + i < job.D; ++i) {
+      const float x = Elt<T>::at(v, c0 + i);
+      if (!(fabsf(x) < CUDART_INF_F)) o[i] += x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Few rows (a tile of 16): what a single token's heads need, and every size or page length
+// the tensor-memory kernel does not take.  Each of the four warps walks its own groups of 16
+// keys with its own copies in flight, its own m, l and o, so no barrier stands in the loop;
+// the four are joined at the end of the tile.  The products are warp-level matrix
+// instructions: at 16 rows the keys' bytes, not the products, set the time.  fp32 inputs are
+// split into two tf32 parts each.
+// ---------------------------------------------------------------------------------------
+template <typename T, int DP>
+struct RowsCfg {
+  static constexpr int kRowBytes = DP * (int)sizeof(T);
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int kStageBytes = 2 * kGroup * kRowBytes;  // keys and values
+  static constexpr int kStages = 3;
+  static constexpr int kQBytes = sizeof(T) == 4 ? kRowsR * DP * 4 : 0;
+  static constexpr int kSmem = kRowsWarps * kStages * kStageBytes + kQBytes;
+  static constexpr int kCtasPerSm = kSmem > 110 * 1024 ? 1 : 2;
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
+  using Cfg = RowsCfg<T, DP>;
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int RB = Cfg::kRowBytes, CH = Cfg::kChunks, S = Cfg::kStages;
+  extern __shared__ __align__(16) unsigned char attn_dyn[];
+  __shared__ int poison;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gr = lane >> 2, tq = lane & 3;  // fragment row, column pair
+  const int cta = blockIdx.x;
+  const AttnRange range = attn_range<kRowsR, kRowsKB, kRowsThreads>(job, cta, gridDim.x);
+  if (threadIdx.x == 0) poison = 0;
+  int4 desc = make_int4(0, 0, 0, kSlotNone);
+  unsigned char* ring = attn_dyn + warp * S * Cfg::kStageBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  float* sq = reinterpret_cast<float*>(attn_dyn + kRowsWarps * S * Cfg::kStageBytes);
+  const float c = job.scale_log2;
+
+  int64_t left = range.units;
+  int head = range.head, entry = range.entry, block = range.block;
+  while (left > 0) {
+    const AttnTile t = attn_tile<kRowsR, kRowsKB>(job, entry);
+    const int nb = (int)min((int64_t)(t.blocks - block), left);
+    const int32_t* table_row = job.table + (int64_t)t.b * job.max_pages;
+    const T* kh = static_cast<const T*>(job.k) + head * job.head_stride;
+    const T* vh = static_cast<const T*>(job.v) + head * job.head_stride;
+    const int seg0 = t.kbeg + block * kRowsKB;
+    const int seg1 = min(seg0 + nb * kRowsKB, t.kend);
+
+    // this thread's two rows
+    int node[2];
+    bool real[2];
+    const T* qrow[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int b, g;
+      real[i] = attn_row(job, t, t.row0 + gr + 8 * i, b, node[i], g);
+      qrow[i] = static_cast<const T*>(job.q) + b * job.lq.batch_stride +
+                node[i] * job.lq.node_stride + (head * job.G + g) * job.lq.head_stride;
+    }
+    // queries: bf16 fragments in registers, fp32 rows in shared memory
+    uint32_t qa[F32 ? 1 : DP / 16][4];
+    if (!F32) {
+#pragma unroll
+      for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = ks * 16 + 2 * tq + 8 * (i >> 1);
+          qa[F32 ? 0 : ks][i] = (real[i & 1] && d < job.D)
+                                    ? *reinterpret_cast<const uint32_t*>(qrow[i & 1] + d)
+                                    : 0u;
+        }
+    } else {
+      for (int i = threadIdx.x; i < kRowsR * DP; i += kRowsThreads) {
+        const int r = i / DP, d = i - r * DP;
+        int b, n, g;
+        float x = 0.f;
+        if (attn_row(job, t, t.row0 + r, b, n, g) && d < job.D)
+          x = Elt<float>::at(static_cast<const float*>(job.q) + b * job.lq.batch_stride +
+                                 n * job.lq.node_stride + (head * job.G + g) * job.lq.head_stride, d);
+        // columns rotated by the row: the fragment reads below touch all banks
+        sq[r * DP + ((d + 4 * r) & (DP - 1))] = x;
+      }
+      __syncthreads();
+    }
+
+    // ---- this warp's groups: keys seg0 + 16 (4 i + warp) .. + 15 ----
+    const int groups = nb;
+    int64_t off_next = -1;  // lane l < 16: offset of key l of the next group to be issued
+    auto lookup = [&](int i) {
+      const int pos = seg0 + (i * kRowsWarps + warp) * kGroup + lane;
+      off_next = (i < groups && lane < kGroup && pos < seg1)
+                     ? paged_offset(table_row, job.max_pages, job.n_pages, job.pd,
+                                    job.page_stride, job.pos_stride, pos)
+                     : (int64_t)-1;
+    };
+    unsigned ok_ring[S];  // per stage: keys that exist
+    auto issue = [&](int i, int stage) {
+      const uint32_t dst = ring_u + stage * Cfg::kStageBytes;
+      const unsigned ok = __ballot_sync(kFull, off_next >= 0);
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s == stage) ok_ring[s] = ok;
+      constexpr int rows_step = CH >= 32 ? 1 : 32 / CH;
+      const int ch0 = lane % CH, r0 = lane / (CH >= 32 ? 32 : CH);
+      if (i < groups) {
+#pragma unroll
+        for (int rr = 0; rr < kGroup; rr += rows_step) {
+          const int r = rr + r0;
+          const int64_t off = __shfl_sync(kFull, off_next, r);
+#pragma unroll
+          for (int cc = 0; cc < CH; cc += 32) {
+            const int ch = ch0 + cc;
+            const bool there = off >= 0 && ch * (16 / (int)sizeof(T)) < job.D;
+            const int64_t at = there ? off + ch * (16 / (int)sizeof(T)) : 0;
+            const uint32_t to = dst + r * RB + ((ch ^ (r & 7)) << 4);
+            cp_async16_or_zero(to, kh + at, there);
+            cp_async16_or_zero(to + kGroup * RB, vh + at, there);
+          }
+        }
+      }
+      cp_async_commit();
+      lookup(i + 1);
+    };
+
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    float o[DP / 8][4];
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+    lookup(0);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) issue(s, s);
+    int stage = 0;
+    for (int i = 0; i < groups; ++i) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      const int pos0 = seg0 + (i * kRowsWarps + warp) * kGroup;
+      unsigned ok = 0;
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s == stage) ok = ok_ring[s];
+      const uint32_t sk = ring_u + stage * Cfg::kStageBytes, sv = sk + kGroup * RB;
+      const unsigned char* sk_p = ring + stage * Cfg::kStageBytes;
+      const unsigned char* sv_p = sk_p + kGroup * RB;
+      const bool whole = ok == 0xffffu && pos0 + kGroup <= t.prefix;
+      if (!whole && pos0 + kGroup > t.prefix) {
+        // drafts among the keys: values that are not finite leave the product
+        bool bad = false;
+        for (int u = lane; u < kGroup * CH; u += 32) {
+          if (pos0 + u / CH < t.prefix) continue;
+          uint4* p = reinterpret_cast<uint4*>(const_cast<unsigned char*>(sv_p)) + u;
+          const uint4 x = *p;
+          if (unit_nonfinite<T>(x)) {
+            bad = true;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int e = 0; e < 4; ++e) {
+              if (F32) {
+                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] = 0u;
+              } else {
+                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+              }
+            }
+            *p = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (bad) poison = 1;
+        __syncwarp();
+      }
+
+      // scores of 16 rows x 16 keys
+      float s[2][4] = {};
+      if (!F32) {
+        // matrices: keys 0-7 / 8-15 x the two halves of a 16-wide step
+        const int krow = (lane & 7) + ((lane >> 4) << 3), khalf = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+          uint32_t kb[4];
+          ldmatrix_x4(kb, sk + krow * RB + (((2 * ks + khalf) ^ (krow & 7)) << 4));
+          mma_bf16(s[0], qa[F32 ? 0 : ks], kb[0], kb[1]);
+          mma_bf16(s[1], qa[F32 ? 0 : ks], kb[2], kb[3]);
+        }
+      } else {
+#pragma unroll 4
+        for (int ks = 0; ks < DP / 8; ++ks) {
+          uint32_t ah[4], al[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = gr + 8 * (e & 1), d = ks * 8 + tq + 4 * (e >> 1);
+            split_tf32_inf(sq[r * DP + ((d + 4 * r) & (DP - 1))], ah[e], al[e]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const int key = nt * 8 + gr;
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x = *reinterpret_cast<const float*>(
+                  sk_p + key * RB + (((2 * ks + e) ^ (key & 7)) << 4) + tq * 4);
+              split_tf32_inf(x, bh[e], bl[e]);
+            }
+            mma_tf32(s[nt], al, bh[0], bh[1]);
+            mma_tf32(s[nt], ah, bl[0], bl[1]);
+            mma_tf32(s[nt], ah, bh[0], bh[1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] *= c;
+      if (!whole) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = nt * 8 + 2 * tq + (e & 1), pos = pos0 + key;
+            bool sees = (ok >> key) & 1u;
+            if (sees && pos >= t.prefix) sees = attn_sees_draft(job, t, node[e >> 1], pos);
+            if (!sees) s[nt][e] = -CUDART_INF_F;
+          }
+      }
+      // running maximum and sum of the two rows
+      float mu[2];
+#pragma unroll
+      for (int i2 = 0; i2 < 2; ++i2) {
+        float x = fmaxf(fmaxf(s[0][2 * i2], s[0][2 * i2 + 1]), fmaxf(s[1][2 * i2], s[1][2 * i2 + 1]));
+        x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+        const float mn = fmaxf(m[i2], x);
+        mu[i2] = mn == -CUDART_INF_F ? 0.f : mn;
+        if (__any_sync(kFull, mn > m[i2])) {
+          const float a = exp2f(m[i2] - mu[i2]);
+          l[i2] *= a;
+#pragma unroll
+          for (int dt = 0; dt < DP / 8; ++dt) {
+            o[dt][2 * i2] *= a;
+            o[dt][2 * i2 + 1] *= a;
+          }
+        }
+        m[i2] = mn;
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[nt][e] = exp2f(s[nt][e] - mu[e >> 1]);
+          l[e >> 1] += s[nt][e];
+        }
+      if (!F32) {
+        uint32_t pa[4];
+        pa[0] = pack_bf16(s[0][0], s[0][1]);
+        pa[1] = pack_bf16(s[0][2], s[0][3]);
+        pa[2] = pack_bf16(s[1][0], s[1][1]);
+        pa[3] = pack_bf16(s[1][2], s[1][3]);
+        const int vrow = lane & 15, vhalf = lane >> 4;
+#pragma unroll
+        for (int ds = 0; ds < DP / 16; ++ds) {
+          uint32_t vb[4];
+          ldmatrix_x4_trans(vb, sv + vrow * RB + (((2 * ds + vhalf) ^ (vrow & 7)) << 4));
+          mma_bf16(o[2 * ds], pa, vb[0], vb[1]);
+          mma_bf16(o[2 * ds + 1], pa, vb[2], vb[3]);
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          // the score fragment's columns 2 t, 2 t + 1 serve as k = t, t + 4
+          uint32_t ah[4], al[4];
+          const int pick[4] = {0, 2, 1, 3};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_tf32(s[nt][pick[e]], ah[e], al[e]);
+#pragma unroll
+          for (int dt = 0; dt < DP / 8; ++dt) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = nt * 8 + 2 * tq + e, d = dt * 8 + gr;
+              const float x = *reinterpret_cast<const float*>(
+                  sv_p + key * RB + (((d >> 2) ^ (key & 7)) << 4) + (d & 3) * 4);
+              split_tf32_inf(x, bh[e], bl[e]);
+            }
+            mma_tf32(o[dt], al, bh[0], bh[1]);
+            mma_tf32(o[dt], ah, bl[0], bl[1]);
+            mma_tf32(o[dt], ah, bh[0], bh[1]);
+          }
+        }
+      }
+      __syncwarp();
+      issue(i + S - 1, stage == 0 ? S - 1 : stage - 1);
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+    // a row's sum over the four threads that hold its columns
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(kFull, l[i], 1);
+      l[i] += __shfl_xor_sync(kFull, l[i], 2);
+    }
+    __syncthreads();
+    // ---- join the four warps through shared memory (the rings are drained) ----
+    constexpr int OP = DP + 4;  // padded output pitch
+    float* so = reinterpret_cast<float*>(attn_dyn);            // [warp][16][OP]
+    float* sm = so + kRowsWarps * kRowsR * OP;                 // [warp][16] m, then l
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = gr + 8 * i;
+      if (tq == 0) {
+        sm[warp * kRowsR + r] = m[i];
+        sm[(kRowsWarps + warp) * kRowsR + r] = l[i];
+      }
+#pragma unroll
+      for (int dt = 0; dt < DP / 8; ++dt)
+        *reinterpret_cast<float2*>(so + (warp * kRowsR + r) * OP + dt * 8 + 2 * tq) =
+            make_float2(o[dt][2 * i], o[dt][2 * i + 1]);
+    }
+    __syncthreads();
+    constexpr int C = kRowsR * DP / kRowsThreads;  // columns of a thread
+    const int r = threadIdx.x / (DP / C), c0 = (threadIdx.x % (DP / C)) * C;
+    float mt = -CUDART_INF_F, lt = 0.f, ot[C];
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) mt = fmaxf(mt, sm[w * kRowsR + r]);
+    const float mbase = mt == -CUDART_INF_F ? 0.f : mt;
+#pragma unroll
+    for (int i = 0; i < C; ++i) ot[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) {
+      const float mw = sm[w * kRowsR + r];
+      const float a = exp2f(mw - mbase);
+      lt += a * sm[(kRowsWarps + w) * kRowsR + r];
+#pragma unroll
+      for (int i = 0; i < C; ++i) ot[i] += a * so[(w * kRowsR + r) * OP + c0 + i];
+    }
+    if (poison) {
+      int b, n, g;
+      if (attn_row(job, t, t.row0 + r, b, n, g))
+        add_nonfinite<T, C>(job, t, head, n, max(t.prefix, seg0), seg1, c0, ot);
+    }
+    if (nb == t.blocks) {
+      write_row<T, C>(job, t, head, t.row0 + r, c0, DP, mt, lt, ot);
+    } else {
+      const int slot = 2 * cta + (block == 0 ? 1 : 0);
+      if (c0 == 0) {
+        job.part_ms[(slot * 2) * kRowsR + r] = mt;
+        job.part_ms[(slot * 2 + 1) * kRowsR + r] = lt;
+      }
+      float4* dst = reinterpret_cast<float4*>(job.part_o + ((int64_t)slot * kRowsR + r) * DP + c0);
+#pragma unroll
+      for (int i = 0; i < C; i += 4)
+        dst[i / 4] = make_float4(ot[i], ot[i + 1], ot[i + 2], ot[i + 3]);
+      if (block == 0) {
+        desc.x = 1;
+        desc.y = head;
+        desc.z = entry;
+      } else {
+        desc.w = block + nb == t.blocks ? kSlotEnd : kSlotMiddle;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) poison = 0;
+    left -= nb;
+    block = 0;
+    if (++entry == job.entries) {
+      entry = 0;
+      ++head;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) job.part_desc[cta] = desc;
+}
+
+// ---------------------------------------------------------------------------------------
+// Join of the tiles cut between CTAs.  Block (j, y) looks whether CTA j left a tile open and
+// joins rows 16 y .. + 15 of its parts: CTA j's second slot, then the first slots of the
+// CTAs after it until the one that holds the tile's end.
+// ---------------------------------------------------------------------------------------
+template <typename T, int DP, int R, int KB>
+__global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(AttnJob job, int ctas) {
+  const int j = blockIdx.x;
+  const int4 desc = job.part_desc[j];
+  if (!desc.x) return;
+  constexpr int C = kCombineRows * DP / kCombineThreads;
+  const int r = blockIdx.y * kCombineRows + threadIdx.x / (DP / C);
+  const int c0 = (threadIdx.x % (DP / C)) * C;
+  const AttnTile t = attn_tile<R, KB>(job, desc.z);
+  float m = -CUDART_INF_F, l = 0.f, o[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = 0.f;
+  auto join = [&](int slot) {
+    const float ms = job.part_ms[(slot * 2) * R + r];
+    const float ls = job.part_ms[(slot * 2 + 1) * R + r];
+    const float4* src = reinterpret_cast<const float4*>(job.part_o + ((int64_t)slot * R + r) * DP + c0);
+    float4 x[C / 4];
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) x[i] = src[i];
+    if (ms == -CUDART_INF_F && ls == 0.f) return;  // sees none of these keys (NaN goes on)
+    const float mn = fmaxf(m, ms);
+    const float a = m == -CUDART_INF_F ? 0.f : exp2f(m - mn), b = exp2f(ms - mn);
+    l = l * a + ls * b;
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) {
+      o[4 * i] = o[4 * i] * a + x[i].x * b;
+      o[4 * i + 1] = o[4 * i + 1] * a + x[i].y * b;
+      o[4 * i + 2] = o[4 * i + 2] * a + x[i].z * b;
+      o[4 * i + 3] = o[4 * i + 3] * a + x[i].w * b;
+    }
+    m = mn;
+  };
+  join(2 * j + 1);
+  for (int i = j + 1; i < ctas; ++i) {
+    const int what = job.part_desc[i].w;
+    if (what == kSlotNone) continue;  // a CTA without work
+    join(2 * i);
+    if (what == kSlotEnd) break;
+  }
+  write_row<T, C>(job, t, desc.y, t.row0 + r, c0, DP, m, l, o);
+}
+
+template <typename T, int DP>
+cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
+  using Cfg = RowsCfg<T, DP>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    e = cudaFuncSetAttribute(attn_rows_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  const int rows = job.phase == kShared ? job.B * job.N * job.G : job.N * job.G;
+  job.row_tiles = (rows + kRowsR - 1) / kRowsR;
+  job.entries = job.phase == kShared ? job.row_tiles : job.row_tiles * job.B;
+  const int grid = min(device_sm_count() * Cfg::kCtasPerSm, kAttnMaxCtas);
+  attn_rows_kernel<T, DP><<<grid, kRowsThreads, Cfg::kSmem, s>>>(job);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  attn_combine_kernel<T, DP, kRowsR, kRowsKB>
+      <<<dim3(grid, kRowsR / kCombineRows), kCombineThreads, 0, s>>>(job, grid);
+  return cudaGetLastError();
+}
+
+struct AttnWs {
+  size_t desc, ms, o, shared_lse, shared_o, total;
+};
+
+int padded_dim(int d) { return d <= 64 ? 64 : 128; }
+
+AttnWs attn_ws(int64_t rows, int Hq, int D, int shared_len) {
+  AttnWs w{};
+  const size_t DP = padded_dim(D);
+  size_t off = 256;  // the error word
+  w.desc = off;
+  off = align_up(off + kAttnMaxCtas * sizeof(int4), 256);
+  w.ms = off;
+  off = align_up(off + (size_t)kAttnMaxCtas * 2 * 2 * kAttnMaxRows * 4, 256);
+  w.o = off;
+  off = align_up(off + (size_t)kAttnMaxCtas * 2 * kAttnMaxRows * DP * 4, 256);
+  w.shared_lse = off;
+  w.shared_o = off;
+  if (shared_len > 0) {
+    off = align_up(off + (size_t)rows * Hq * 4, 256);
+    w.shared_o = off;
+    off = align_up(off + (size_t)rows * Hq * DP * 4, 256);
+  }
+  w.total = off;
+  return w;
+}
+
+bool attn_sizes_ok(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t shared_len) {
+  return B >= 0 && N >= 0 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && D >= 1 && shared_len >= 0;
+}
+
+}  // namespace
+
+}  // namespace svk
+
+using namespace svk;
+
+extern "C" size_t spec_tree_attention_workspace_size(int32_t B, int32_t N, int32_t n_q_heads,
+                                                     int32_t n_kv_heads, int32_t head_dim,
+                                                     int32_t shared_len, spec_dtype dtype) {
+  if (!attn_sizes_ok(B, N, n_q_heads, n_kv_heads, head_dim, shared_len)) return 0;
+  if (head_dim > SPEC_ATTN_MAX_HEAD_DIM || (int64_t)B * N * n_q_heads > 0x3fffffff) return 0;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return 0;
+  return attn_ws((int64_t)B * N, n_q_heads, head_dim, shared_len).total;
+}
+
+extern "C" int spec_tree_attention_paged(
+    const void* q, spec_node_layout q_layout, const void* k_cache, const void* v_cache,
+    spec_paged_layout cache, spec_dtype dtype, int32_t B, int32_t N, int32_t n_q_heads,
+    const int32_t* page_table, int32_t max_pages, const int32_t* prefix_len,
+    const int32_t* counts, const uint8_t* mask, int32_t shared_len, float scale, void* out,
+    spec_node_layout out_layout, float* lse, void* workspace, size_t workspace_bytes,
+    spec_stream_t stream) {
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  int rc = check_paged_layout(cache, max_pages);
+  if (rc != SPEC_OK) return rc;
+  if (!attn_sizes_ok(B, N, n_q_heads, cache.n_kv_heads, cache.head_dim, shared_len) ||
+      shared_len % cache.page_size != 0 || !(fabsf(scale) <= FLT_MAX))
+    return SPEC_ERR_INVALID_ARG;
+  if (cache.head_dim > SPEC_ATTN_MAX_HEAD_DIM || (int64_t)B * N * n_q_heads > 0x3fffffff)
+    return SPEC_ERR_TOO_LARGE;
+  if (B == 0 || N == 0) return SPEC_OK;
+  if (!q || !k_cache || !v_cache || !page_table || !prefix_len || !out || !workspace)
+    return SPEC_ERR_INVALID_ARG;
+  const int64_t es = dtype == SPEC_F32 ? 4 : 2;
+  const int64_t strides[] = {q_layout.batch_stride,   q_layout.node_stride,
+                             q_layout.head_stride,    out_layout.batch_stride,
+                             out_layout.node_stride,  out_layout.head_stride,
+                             cache.page_stride,       cache.pos_stride,
+                             cache.head_stride,       cache.head_dim};
+  for (int64_t x : strides)
+    if ((x * es) % 16 != 0) return SPEC_ERR_MISALIGNED;
+  const void* bases[] = {q, k_cache, v_cache, out};
+  for (const void* p : bases)
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return SPEC_ERR_MISALIGNED;
+  const AttnWs w = attn_ws((int64_t)B * N, n_q_heads, cache.head_dim, shared_len);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < w.total)
+    return SPEC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  AttnJob job{};
+  job.q = q;
+  job.k = k_cache;
+  job.v = v_cache;
+  job.out = out;
+  job.lse = lse;
+  job.lq = q_layout;
+  job.lo = out_layout;
+  job.page_stride = cache.page_stride;
+  job.pos_stride = cache.pos_stride;
+  job.head_stride = cache.head_stride;
+  job.table = page_table;
+  job.prefix = prefix_len;
+  job.counts = counts;
+  job.mask = mask;
+  job.B = B;
+  job.N = N;
+  job.Hq = n_q_heads;
+  job.Hkv = cache.n_kv_heads;
+  job.G = n_q_heads / cache.n_kv_heads;
+  job.D = cache.head_dim;
+  job.n_pages = cache.n_pages;
+  job.max_pages = max_pages;
+  job.shared_len = shared_len;
+  job.pd = PageDiv::make(cache.page_size);
+  job.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  job.err = reinterpret_cast<int*>(ws);
+  job.part_desc = reinterpret_cast<int4*>(ws + w.desc);
+  job.part_ms = reinterpret_cast<float*>(ws + w.ms);
+  job.part_o = reinterpret_cast<float*>(ws + w.o);
+  job.shared_lse = reinterpret_cast<float*>(ws + w.shared_lse);
+  job.shared_o = reinterpret_cast<float*>(ws + w.shared_o);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool narrow = padded_dim(job.D) == 64;
+  for (int phase = shared_len > 0 ? kShared : kOwn; phase >= kOwn; --phase) {
+    job.phase = phase;
+    cudaError_t e;
+    if (dtype == SPEC_BF16)
+      e = narrow ? launch_rows<uint16_t, 64>(job, s) : launch_rows<uint16_t, 128>(job, s);
+    else
+      e = narrow ? launch_rows<float, 64>(job, s) : launch_rows<float, 128>(job, s);
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
+  }
+  return SPEC_OK;
+}

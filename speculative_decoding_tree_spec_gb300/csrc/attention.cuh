@@ -1,0 +1,168 @@
+// attention.cuh -- the work list of the paged tree attention, shared by its kernels.
+//
+// Rows: the query heads that read one key head are taken together, row r = node * G + g of
+// sequence b (G = query heads per key head), in tiles of R rows.  A tile's keys are cut into
+// blocks of KB positions; a tile holds max(1, blocks) units of work, numbered key head by
+// key head and tile by tile.  CTA j of n takes the units [U j / n, U (j + 1) / n): every CTA
+// does the same number of blocks however the lengths differ.  A tile that lies in one CTA is
+// finished there; of a tile cut between CTAs each CTA leaves its part (running maximum, sum,
+// unnormalised output) in one of its two slots and attn_combine_kernel joins the parts in
+// the order of the keys.  The split depends on the lengths and the grid alone, so a call is
+// reproducible bit for bit.
+//
+// Two phases: kOwn takes each sequence's own positions (from shared_len on) and writes the
+// call's outputs; kShared takes the positions all sequences share, for the rows of all
+// sequences at once (row r = (b * N + node) * G + g), and writes a normalised result that
+// kOwn joins with its own.
+#pragma once
+
+#include "paged.cuh"
+
+namespace svk {
+
+constexpr int kAttnMaxCtas = 512;  // grid limit: two slots per CTA in the workspace
+constexpr int kAttnMaxRows = 16;   // rows of the largest tile
+
+enum AttnPhase { kOwn = 0, kShared = 1 };
+
+struct AttnJob {
+  const void *q, *k, *v;
+  void* out;
+  float* lse;
+  spec_node_layout lq, lo;                       // elements
+  int64_t page_stride, pos_stride, head_stride;  // elements
+  const int32_t *table, *prefix, *counts;
+  const uint8_t* mask;
+  int B, N, Hq, Hkv, G, D, n_pages, max_pages, shared_len;
+  int row_tiles;   // tiles per sequence (kOwn) or in all (kShared)
+  int entries;     // tiles of one key head
+  PageDiv pd;
+  float scale_log2;  // scale * log2(e)
+  int phase;
+  // result of the shared positions, [Hkv][B * N * G] rows: normalised output (row pitch DP)
+  // and its log2-sum-exp2
+  float* shared_o;
+  float* shared_lse;
+  // two slots per CTA: [slot][R] maximum and sum, [slot][R][DP] output
+  float* part_ms;
+  float* part_o;
+  int4* part_desc;  // per CTA: {a tile is left open, key head, tile, what slot 0 holds}
+  int* err;
+};
+
+// What slot 0 of a CTA holds: nothing, the middle of a tile, the end of one.
+enum { kSlotNone = 0, kSlotMiddle = 1, kSlotEnd = 2 };
+
+// One tile's rows and keys.
+struct AttnTile {
+  int b;            // sequence (0 for the shared positions)
+  int row0;         // first row
+  int prefix, count;
+  int kbeg, kend;   // positions its rows can see at most
+  int blocks;       // units
+};
+
+template <int R, int KB>
+__device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry) {
+  AttnTile t;
+  const int cap = job.max_pages * job.pd.size;
+  if (job.phase == kShared) {
+    t.b = 0;
+    t.row0 = entry * R;
+    t.prefix = job.shared_len;
+    t.count = job.N;
+    t.kbeg = 0;
+    t.kend = min(job.shared_len, cap);
+  } else {
+    t.b = entry / job.row_tiles;
+    t.row0 = (entry - t.b * job.row_tiles) * R;
+    t.prefix = max(job.prefix[t.b], 0);
+    t.count = job.counts ? min(max(job.counts[t.b], 0), job.N) : job.N;
+    if (t.prefix < job.shared_len) t.count = 0;  // not a sequence behind the shared prefix
+    t.kbeg = job.shared_len;
+    const int first = t.row0 / job.G, last = (min(t.row0 + R, job.N * job.G) - 1) / job.G;
+    int64_t end = (int64_t)t.prefix + (job.mask ? t.count : min(t.count, last + 1));
+    if (first >= t.count) end = t.kbeg;  // only padding rows
+    t.kend = (int)max((int64_t)t.kbeg, min(end, (int64_t)cap));
+  }
+  t.blocks = max(1, (t.kend - t.kbeg + KB - 1) / KB);
+  return t;
+}
+
+// This CTA's units and where the first one lies: key head, tile, block in it.
+struct AttnRange {
+  int64_t units;
+  int head, entry, block;
+};
+
+// All NT threads of the block call this.  Thread i sums the units of a run of tiles; a scan
+// over the threads gives a key head's units and the run that holds the first one.
+template <int R, int KB, int NT>
+__device__ __forceinline__ AttnRange attn_range(const AttnJob& job, int cta, int ctas) {
+  __shared__ int64_t warp_sum[NT / 32];
+  __shared__ int found[2];
+  const int run = (job.entries + NT - 1) / NT;
+  const int e0 = (int)threadIdx.x * run, e1 = min(e0 + run, job.entries);
+  int64_t mine = 0;
+  for (int e = e0; e < e1; ++e) mine += attn_tile<R, KB>(job, e).blocks;
+  int64_t inc = mine;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(kFull, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, per_head = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    per_head += warp_sum[w];
+  }
+  const int64_t total = per_head * job.Hkv;
+  const int64_t u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
+  AttnRange r;
+  r.units = u1 - u0;
+  r.head = (int)(u0 / per_head);
+  int64_t rest = u0 - r.head * per_head - (before + inc - mine);
+  if (rest >= 0 && rest < mine) {
+    int e = e0;
+    for (;; ++e) {
+      const int n = attn_tile<R, KB>(job, e).blocks;
+      if (rest < n) break;
+      rest -= n;
+    }
+    found[0] = e;
+    found[1] = (int)rest;
+  }
+  __syncthreads();
+  r.entry = found[0];
+  r.block = found[1];
+  return r;
+}
+
+// Whether row r of the tile is a query (not padding), and its node.
+__device__ __forceinline__ bool attn_row(const AttnJob& job, const AttnTile& t, int r, int& b,
+                                         int& node, int& g) {
+  if (job.phase == kShared) {
+    const int ng = job.N * job.G;
+    b = r / ng;
+    r -= b * ng;
+  } else {
+    b = t.b;
+  }
+  node = r / job.G;
+  g = r - node * job.G;
+  return job.phase == kShared ? b < job.B : node < job.N;
+}
+
+// Whether node n of the tile's sequence sees position t >= prefix (t below kend).
+__device__ __forceinline__ bool attn_sees_draft(const AttnJob& job, const AttnTile& t, int n,
+                                                int pos) {
+  const int j = pos - t.prefix;
+  if (j >= t.count || n >= t.count) return false;
+  return job.mask ? job.mask[((int64_t)t.b * job.N + n) * job.N + j] != 0 : j <= n;
+}
+
+}  // namespace svk

@@ -9,7 +9,7 @@
 // place).  A path increases strictly (parents precede children), so path[b][k] >= k;
 // one thread owns each 16-byte column of a (plane, tree) and no other thread touches
 // its bytes.
-#include "common.cuh"
+#include "paged.cuh"
 
 namespace svk {
 
@@ -69,11 +69,121 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitJob job) {
   }
 }
 
+// The same in a paged cache: a position's row is found through the sequence's page table,
+// and a row may be split over heads that lie apart.
+struct PagedCommitJob {
+  unsigned char* cache;
+  int B, n_planes, n_heads, n_pages, max_pages, W;
+  int64_t plane_stride, page_stride, pos_stride, head_stride;  // bytes
+  int64_t row_bytes;                                           // multiple of 16
+  PageDiv pd;
+  const int32_t* table;
+  const int32_t* prefix_len;
+  const int32_t* path;
+  const int32_t* accept_len;
+};
+
+// One thread per (plane, tree, head, 16-byte column) item, grid-stride, moves in batches
+// as above: all addresses of a batch, then all loads, then all stores.
+__global__ void __launch_bounds__(kCommitThreads) paged_commit_kernel(PagedCommitJob job) {
+  const int64_t nvec = job.row_bytes / 16, per_tree = nvec * job.n_heads;
+  const int64_t total = (int64_t)job.B * job.n_planes * per_tree;
+  for (int64_t item = (int64_t)blockIdx.x * kCommitThreads + threadIdx.x; item < total;
+       item += (int64_t)gridDim.x * kCommitThreads) {
+    const int64_t pair = item / per_tree, in_tree = item - pair * per_tree;
+    const int64_t head = in_tree / nvec, v = in_tree - head * nvec;
+    const int b = (int)(pair % job.B);
+    const int64_t plane = pair / job.B;
+    const int a = min(job.accept_len[b], job.W - 1);
+    if (a <= 0) continue;
+    const int base = job.prefix_len[b];
+    const int32_t* path = job.path + (int64_t)b * job.W;
+    const int32_t* row = job.table + (int64_t)b * job.max_pages;
+    unsigned char* col = job.cache + plane * job.plane_stride + head * job.head_stride + v * 16;
+    auto at = [&](int node) {  // node 0 is at `base`; overflowing sums have no page
+      const int64_t t = (int64_t)base + node;
+      return t >= 0 && t <= 0x7fffffff
+                 ? paged_offset(row, job.max_pages, job.n_pages, job.pd, job.page_stride,
+                                job.pos_stride, (int)t)
+                 : (int64_t)-1;
+    };
+    for (int k0 = 1; k0 <= a; k0 += kBatchMoves) {
+      uint4 x[kBatchMoves];
+      int64_t src[kBatchMoves], dst[kBatchMoves];
+#pragma unroll
+      for (int i = 0; i < kBatchMoves; ++i) {
+        const int k = k0 + i;
+        src[i] = dst[i] = -1;
+        if (k <= a) {
+          const int node = path[k];
+          if (node != k) {
+            src[i] = at(node);
+            dst[i] = at(k);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatchMoves; ++i)
+        if (src[i] >= 0 && dst[i] >= 0) x[i] = *reinterpret_cast<const uint4*>(col + src[i]);
+#pragma unroll
+      for (int i = 0; i < kBatchMoves; ++i)
+        if (src[i] >= 0 && dst[i] >= 0) *reinterpret_cast<uint4*>(col + dst[i]) = x[i];
+    }
+  }
+}
+
 }  // namespace
 
 }  // namespace svk
 
 using namespace svk;
+
+extern "C" int spec_commit_accepted_path_paged(
+    void* cache, int32_t B, int32_t n_planes, int32_t n_heads, int32_t n_pages,
+    int32_t page_size, int64_t plane_stride, int64_t page_stride, int64_t pos_stride,
+    int64_t head_stride, int64_t row_bytes, const int32_t* page_table, int32_t max_pages,
+    const int32_t* prefix_len, const int32_t* accepted_path, const int32_t* accept_len, int32_t W,
+    spec_stream_t stream) {
+  if (B < 0 || n_planes < 0 || n_heads < 0 || row_bytes < 0 || W < 1 || plane_stride < 0)
+    return SPEC_ERR_INVALID_ARG;
+  const spec_paged_layout l{n_pages, page_size, 1, 1, page_stride, pos_stride, head_stride};
+  const int rc = check_paged_layout(l, max_pages);
+  if (rc != SPEC_OK) return rc;
+  if (B == 0 || n_planes == 0 || n_heads == 0 || row_bytes == 0) return SPEC_OK;
+  if (!cache || !page_table || !prefix_len || !accepted_path || !accept_len)
+    return SPEC_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(cache) & 15u) ||
+      ((plane_stride | page_stride | pos_stride | head_stride | row_bytes) & 15))
+    return SPEC_ERR_MISALIGNED;
+  if (row_bytes > pos_stride && page_size > 1) return SPEC_ERR_INVALID_ARG;  // rows may not overlap
+  const int64_t pairs = (int64_t)B * n_planes;
+  if (pairs > 0x7fffffff) return SPEC_ERR_TOO_LARGE;
+  PagedCommitJob job{};
+  job.cache = static_cast<unsigned char*>(cache);
+  job.B = B;
+  job.n_planes = n_planes;
+  job.n_heads = n_heads;
+  job.n_pages = n_pages;
+  job.max_pages = max_pages;
+  job.W = W;
+  job.plane_stride = plane_stride;
+  job.page_stride = page_stride;
+  job.pos_stride = pos_stride;
+  job.head_stride = head_stride;
+  job.row_bytes = row_bytes;
+  job.pd = PageDiv::make(page_size);
+  job.table = page_table;
+  job.prefix_len = prefix_len;
+  job.path = accepted_path;
+  job.accept_len = accept_len;
+  const int64_t items = pairs * n_heads * (row_bytes / 16);
+  int64_t blocks = (items + kCommitThreads - 1) / kCommitThreads;
+  const int64_t cap = (int64_t)device_sm_count() * 16;  // grid-stride beyond this
+  if (blocks > cap) blocks = cap;
+  paged_commit_kernel<<<(unsigned)blocks, kCommitThreads, 0,
+                        reinterpret_cast<cudaStream_t>(stream)>>>(job);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
 
 extern "C" int spec_commit_accepted_path(void* cache, int32_t B, int32_t n_planes, int32_t n_pos,
                                          int64_t plane_stride, int64_t batch_stride,
