@@ -16,7 +16,7 @@ namespace svk {
 
 namespace {
 
-constexpr int kRowsR = 16;       // rows of a tile: one m16 fragment
+constexpr int kRowsR = kAttnRowsTile;  // rows of a tile: one m16 fragment
 constexpr int kRowsWarps = 4;    // each takes every fourth group of keys
 constexpr int kRowsThreads = 32 * kRowsWarps;
 constexpr int kGroup = 16;       // keys of a warp's step
@@ -66,118 +66,6 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 __device__ __forceinline__ void split_tf32_inf(float x, uint32_t& hi, uint32_t& lo) {
   split_tf32(x, hi, lo);
   if ((hi & 0x7f800000u) == 0x7f800000u) lo = 0u;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-template <typename T> __device__ __forceinline__ T from_float(float x);
-template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <> __device__ __forceinline__ uint16_t from_float<uint16_t>(float x) {
-  return __bfloat16_as_ushort(__float2bfloat16(x));
-}
-
-// Whether a 16-byte unit holds an infinity or a NaN.
-template <typename T> __device__ __forceinline__ bool unit_nonfinite(const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (sizeof(T) == 4) {
-      bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
-    } else {
-      bad |= (w[i] & 0x7f800000u) == 0x7f800000u || (w[i] & 0x7f80u) == 0x7f80u;
-    }
-  }
-  return bad;
-}
-
-// One row's result: its part (m, l, o[0..n) of columns c0..) joined with the shared
-// positions' result and written, or, in the shared phase, left for that join.
-template <typename T, int C>
-__device__ __forceinline__ void write_row(const AttnJob& job, const AttnTile& t, int head, int r,
-                                          int c0, int DP, float m, float l, float (&o)[C]) {
-  int b, node, g;
-  if (!attn_row(job, t, r, b, node, g)) return;
-  if (job.phase == kShared) {
-    const int64_t row = (int64_t)head * job.B * job.N * job.G + r;
-    const float inv = 1.f / l;  // l > 0: every row of the shared positions sees them
-    float4* dst = reinterpret_cast<float4*>(job.shared_o + row * DP + c0);
-#pragma unroll
-    for (int i = 0; i < C; i += 4)
-      dst[i / 4] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                            : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-    if (c0 == 0) job.shared_lse[row] = l == 0.f ? -CUDART_INF_F : m + log2f(l);
-    return;
-  }
-  const bool real = node < t.count;
-  float lse2;
-  if (!real) {
-    lse2 = -CUDART_INF_F;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
-  } else {
-    float w = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
-    lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
-    const float* so = nullptr;
-    if (job.shared_len > 0) {
-      const int64_t row =
-          ((int64_t)head * job.B + b) * job.N * job.G + (int64_t)node * job.G + g;
-      const float s2 = job.shared_lse[row];
-      if (s2 != -CUDART_INF_F) {
-        so = job.shared_o + row * DP + c0;
-        const float top = fmaxf(s2, lse2);
-        const float es = exp2f(s2 - top);
-        const float eo = lse2 == -CUDART_INF_F ? 0.f : exp2f(lse2 - top);
-        ws = es / (es + eo);
-        w = l == 0.f ? 0.f : eo / (es + eo) / l;
-        lse2 = top + log2f(es + eo);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float x = l == 0.f ? 0.f : o[i] * w;
-      if (so) x += so[i] * ws;
-      o[i] = x;
-    }
-  }
-  const int h = head * job.G + g;
-  T* dst = static_cast<T*>(job.out) + b * job.lo.batch_stride + node * job.lo.node_stride +
-           h * job.lo.head_stride;
-  constexpr int E = 16 / (int)sizeof(T);
-#pragma unroll
-  for (int i = 0; i < C; i += E) {
-    if (c0 + i < job.D) {
-      T x[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = from_float<T>(o[i + e]);
-      *reinterpret_cast<uint4*>(dst + c0 + i) = *reinterpret_cast<const uint4*>(x);
-    }
-  }
-  if (c0 == 0 && job.lse)
-    job.lse[((int64_t)b * job.N + node) * job.Hq + h] = lse2 * 0.693147180559945309f;
-}
-
-// Infinities and NaN among the draft positions' values [from, to) that row (node) sees.  A
-// tile in which some rows do not see a key multiplies it by 0 for them, so such values are
-// taken out of the product (as 0) and added here for the rows that do see them.
-template <typename T, int C>
-__device__ __noinline__ void add_nonfinite(const AttnJob& job, const AttnTile& t, int head,
-                                           int node, int from, int to, int c0, float* o) {
-  const int32_t* row = job.table + (int64_t)t.b * job.max_pages;
-  for (int pos = from; pos < to; ++pos) {
-    if (!attn_sees_draft(job, t, node, pos)) continue;
-    const int64_t off = paged_offset(row, job.max_pages, job.n_pages, job.pd, job.page_stride,
-                                     job.pos_stride, pos);
-    if (off < 0) continue;
-    const T* v = static_cast<const T*>(job.v) + off + head * job.head_stride;
-    for (int i = 0; i < C && c0 + i < job.D; ++i) {
-      const float x = Elt<T>::at(v, c0 + i);
-      if (!(fabsf(x) < CUDART_INF_F)) o[i] += x;
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -624,6 +512,13 @@ cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+constexpr int kTcRows = 256, kTcKeys = 128;
+
+// rows of all slots of a launch, whichever kernel it is
+constexpr size_t kAttnSlotRows =
+    2 * (size_t)(kAttnTcCtas * kTcRows > kAttnMaxCtas * kRowsR ? kAttnTcCtas * kTcRows
+                                                               : kAttnMaxCtas * kRowsR);
+
 struct AttnWs {
   size_t desc, ms, o, shared_lse, shared_o, total;
 };
@@ -633,13 +528,13 @@ int padded_dim(int d) { return d <= 64 ? 64 : 128; }
 AttnWs attn_ws(int64_t rows, int Hq, int D, int shared_len) {
   AttnWs w{};
   const size_t DP = padded_dim(D);
-  size_t off = 256;  // the error word
+  size_t off = 0;
   w.desc = off;
   off = align_up(off + kAttnMaxCtas * sizeof(int4), 256);
   w.ms = off;
-  off = align_up(off + (size_t)kAttnMaxCtas * 2 * 2 * kAttnMaxRows * 4, 256);
+  off = align_up(off + kAttnSlotRows * 2 * 4, 256);
   w.o = off;
-  off = align_up(off + (size_t)kAttnMaxCtas * 2 * kAttnMaxRows * DP * 4, 256);
+  off = align_up(off + kAttnSlotRows * DP * 4, 256);
   w.shared_lse = off;
   w.shared_o = off;
   if (shared_len > 0) {
@@ -650,6 +545,21 @@ AttnWs attn_ws(int64_t rows, int Hq, int D, int shared_len) {
   w.total = off;
   return w;
 }
+
+}  // namespace
+
+cudaError_t launch_attn_combine(const AttnJob& job, int DP, int R, int KB, int ctas,
+                                cudaStream_t s) {
+  if (R != kTcRows || KB != kTcKeys) return cudaErrorInvalidValue;
+  const dim3 grid(ctas, kTcRows / kCombineRows);
+  if (DP == 64)
+    attn_combine_kernel<uint16_t, 64, kTcRows, kTcKeys><<<grid, kCombineThreads, 0, s>>>(job, ctas);
+  else
+    attn_combine_kernel<uint16_t, 128, kTcRows, kTcKeys><<<grid, kCombineThreads, 0, s>>>(job, ctas);
+  return cudaGetLastError();
+}
+
+namespace {
 
 bool attn_sizes_ok(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t shared_len) {
   return B >= 0 && N >= 0 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && D >= 1 && shared_len >= 0;
@@ -729,7 +639,6 @@ extern "C" int spec_tree_attention_paged(
   job.shared_len = shared_len;
   job.pd = PageDiv::make(cache.page_size);
   job.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  job.err = reinterpret_cast<int*>(ws);
   job.part_desc = reinterpret_cast<int4*>(ws + w.desc);
   job.part_ms = reinterpret_cast<float*>(ws + w.ms);
   job.part_o = reinterpret_cast<float*>(ws + w.o);
@@ -739,7 +648,11 @@ extern "C" int spec_tree_attention_paged(
   const bool narrow = padded_dim(job.D) == 64;
   for (int phase = shared_len > 0 ? kShared : kOwn; phase >= kOwn; --phase) {
     job.phase = phase;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
+    bool taken = false;
+    if (attn_tc_fits(job, dtype)) e = launch_attn_tc(job, s, &taken);
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
+    if (taken) continue;
     if (dtype == SPEC_BF16)
       e = narrow ? launch_rows<uint16_t, 64>(job, s) : launch_rows<uint16_t, 128>(job, s);
     else

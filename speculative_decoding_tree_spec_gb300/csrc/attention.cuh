@@ -16,16 +16,19 @@
 // kOwn joins with its own.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "paged.cuh"
 
 namespace svk {
 
 constexpr int kAttnMaxCtas = 512;  // grid limit: two slots per CTA in the workspace
-constexpr int kAttnMaxRows = 16;   // rows of the largest tile
+constexpr int kAttnTcCtas = 256;   // grid limit of the 256-row tiles
+constexpr int kAttnRowsTile = 16;  // rows of the few-rows kernel's tile
 
 enum AttnPhase { kOwn = 0, kShared = 1 };
 
-struct AttnJob {
+struct AttnJob {  // (the kernels' argument)
   const void *q, *k, *v;
   void* out;
   float* lse;
@@ -47,8 +50,14 @@ struct AttnJob {
   float* part_ms;
   float* part_o;
   int4* part_desc;  // per CTA: {a tile is left open, key head, tile, what slot 0 holds}
-  int* err;
 };
+
+bool attn_tc_fits(const AttnJob& job, spec_dtype dtype);
+// The tensor-memory kernel and its join; *taken = false where the cache's strides make no
+// tensor map (nothing was launched).
+cudaError_t launch_attn_tc(const AttnJob& job, cudaStream_t s, bool* taken);
+cudaError_t launch_attn_combine(const AttnJob& job, int DP, int R, int KB, int ctas,
+                                cudaStream_t s);
 
 // What slot 0 of a CTA holds: nothing, the middle of a tile, the end of one.
 enum { kSlotNone = 0, kSlotMiddle = 1, kSlotEnd = 2 };
@@ -76,7 +85,7 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry) {
   } else {
     t.b = entry / job.row_tiles;
     t.row0 = (entry - t.b * job.row_tiles) * R;
-    t.prefix = max(job.prefix[t.b], 0);
+    t.prefix = min(max(job.prefix[t.b], 0), cap);  // no position beyond the table exists
     t.count = job.counts ? min(max(job.counts[t.b], 0), job.N) : job.N;
     if (t.prefix < job.shared_len) t.count = 0;  // not a sequence behind the shared prefix
     t.kbeg = job.shared_len;
@@ -163,6 +172,118 @@ __device__ __forceinline__ bool attn_sees_draft(const AttnJob& job, const AttnTi
   const int j = pos - t.prefix;
   if (j >= t.count || n >= t.count) return false;
   return job.mask ? job.mask[((int64_t)t.b * job.N + n) * job.N + j] != 0 : j <= n;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T> __device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ uint16_t from_float<uint16_t>(float x) {
+  return __bfloat16_as_ushort(__float2bfloat16(x));
+}
+
+// Whether a 16-byte unit holds an infinity or a NaN.
+template <typename T> __device__ __forceinline__ bool unit_nonfinite(const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(T) == 4) {
+      bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
+    } else {
+      bad |= (w[i] & 0x7f800000u) == 0x7f800000u || (w[i] & 0x7f80u) == 0x7f80u;
+    }
+  }
+  return bad;
+}
+
+// One row's result: its part (m, l, o[0..n) of columns c0..) joined with the shared
+// positions' result and written, or, in the shared phase, left for that join.
+template <typename T, int C>
+__device__ __forceinline__ void write_row(const AttnJob& job, const AttnTile& t, int head, int r,
+                                          int c0, int DP, float m, float l, float (&o)[C]) {
+  int b, node, g;
+  if (!attn_row(job, t, r, b, node, g)) return;
+  if (job.phase == kShared) {
+    const int64_t row = (int64_t)head * job.B * job.N * job.G + r;
+    const float inv = 1.f / l;  // l > 0: every row of the shared positions sees them
+    float4* dst = reinterpret_cast<float4*>(job.shared_o + row * DP + c0);
+#pragma unroll
+    for (int i = 0; i < C; i += 4)
+      dst[i / 4] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+    if (c0 == 0) job.shared_lse[row] = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+    return;
+  }
+  const bool real = node < t.count;
+  float lse2;
+  if (!real) {
+    lse2 = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = 0.f;
+  } else {
+    float w = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
+    lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+    const float* so = nullptr;
+    if (job.shared_len > 0) {
+      const int64_t row =
+          ((int64_t)head * job.B + b) * job.N * job.G + (int64_t)node * job.G + g;
+      const float s2 = job.shared_lse[row];
+      if (s2 != -CUDART_INF_F) {
+        so = job.shared_o + row * DP + c0;
+        const float top = fmaxf(s2, lse2);
+        const float es = exp2f(s2 - top);
+        const float eo = lse2 == -CUDART_INF_F ? 0.f : exp2f(lse2 - top);
+        ws = es / (es + eo);
+        w = l == 0.f ? 0.f : eo / (es + eo) / l;
+        lse2 = top + log2f(es + eo);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float x = l == 0.f ? 0.f : o[i] * w;
+      if (so) x += so[i] * ws;
+      o[i] = x;
+    }
+  }
+  const int h = head * job.G + g;
+  T* dst = static_cast<T*>(job.out) + b * job.lo.batch_stride + node * job.lo.node_stride +
+           h * job.lo.head_stride;
+  constexpr int E = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < C; i += E) {
+    if (c0 + i < job.D) {
+      T x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = from_float<T>(o[i + e]);
+      *reinterpret_cast<uint4*>(dst + c0 + i) = *reinterpret_cast<const uint4*>(x);
+    }
+  }
+  if (c0 == 0 && job.lse)
+    job.lse[((int64_t)b * job.N + node) * job.Hq + h] = lse2 * 0.693147180559945309f;
+}
+
+// Infinities and NaN among the draft positions' values [from, to) that row (node) sees.  A
+// tile in which some rows do not see a key multiplies it by 0 for them, so such values are
+// taken out of the product (as 0) and added here for the rows that do see them.
+template <typename T, int C>
+static __device__ __noinline__ void add_nonfinite(const AttnJob& job, const AttnTile& t, int head,
+                                           int node, int from, int to, int c0, float* o) {
+  const int32_t* row = job.table + (int64_t)t.b * job.max_pages;
+  for (int pos = from; pos < to; ++pos) {
+    if (!attn_sees_draft(job, t, node, pos)) continue;
+    const int64_t off = paged_offset(row, job.max_pages, job.n_pages, job.pd, job.page_stride,
+                                     job.pos_stride, pos);
+    if (off < 0) continue;
+    const T* v = static_cast<const T*>(job.v) + off + head * job.head_stride;
+    for (int i = 0; i < C && c0 + i < job.D; ++i) {
+      const float x = Elt<T>::at(v, c0 + i);
+      if (!(fabsf(x) < CUDART_INF_F)) o[i] += x;
+    }
+  }
 }
 
 }  // namespace svk
