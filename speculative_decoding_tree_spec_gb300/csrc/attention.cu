@@ -21,8 +21,7 @@ constexpr int kRowsWarps = 4;    // each takes every fourth group of keys
 constexpr int kRowsThreads = 32 * kRowsWarps;
 constexpr int kGroup = 16;       // keys of a warp's step
 constexpr int kRowsKB = kGroup * kRowsWarps;
-constexpr int kCombineRows = 16;
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 512;
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool real) {
   const int n = real ? 16 : 0;
@@ -57,7 +56,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // x = hi + lo with both parts tf32: the products hi hi + hi lo + lo hi carry an fp32
-// product to about 2^-21.
+// product to about 2^-21.  The tensor cores' own sum cuts bits off where an fp32 add rounds, so
+// each step of 8 starts from 0 and is added to the running sums in fp32.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(hi) : "f"(x));
   asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, tq = lane & 3;  // fragment row, column pair
   const int cta = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may line up
   const AttnRange range = attn_range<kRowsR, kRowsKB, kRowsThreads>(job, cta, gridDim.x);
   if (threadIdx.x == 0) poison = 0;
   int4 desc = make_int4(0, 0, 0, kSlotNone);
@@ -214,12 +215,12 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
       const uint32_t sk = ring_u + stage * Cfg::kStageBytes, sv = sk + kGroup * RB;
       const unsigned char* sk_p = ring + stage * Cfg::kStageBytes;
       const unsigned char* sv_p = sk_p + kGroup * RB;
-      const bool whole = ok == 0xffffu && pos0 + kGroup <= t.prefix;
-      if (!whole && pos0 + kGroup > t.prefix) {
+      const bool whole = ok == 0xffffu && pos0 + kGroup <= t.clear;
+      if (pos0 + kGroup > t.clear) {
         // drafts among the keys: values that are not finite leave the product
         bool bad = false;
         for (int u = lane; u < kGroup * CH; u += 32) {
-          if (pos0 + u / CH < t.prefix) continue;
+          if (pos0 + u / CH < t.clear) continue;
           uint4* p = reinterpret_cast<uint4*>(const_cast<unsigned char*>(sv_p)) + u;
           const uint4 x = *p;
           if (unit_nonfinite<T>(x)) {
@@ -271,9 +272,12 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
                   sk_p + key * RB + (((2 * ks + e) ^ (key & 7)) << 4) + tq * 4);
               split_tf32_inf(x, bh[e], bl[e]);
             }
-            mma_tf32(s[nt], al, bh[0], bh[1]);
-            mma_tf32(s[nt], ah, bl[0], bl[1]);
-            mma_tf32(s[nt], ah, bh[0], bh[1]);
+            float part[4] = {};
+            mma_tf32(part, al, bh[0], bh[1]);
+            mma_tf32(part, ah, bl[0], bl[1]);
+            mma_tf32(part, ah, bh[0], bh[1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] += part[e];
           }
         }
       }
@@ -351,9 +355,12 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
                   sv_p + key * RB + (((d >> 2) ^ (key & 7)) << 4) + (d & 3) * 4);
               split_tf32_inf(x, bh[e], bl[e]);
             }
-            mma_tf32(o[dt], al, bh[0], bh[1]);
-            mma_tf32(o[dt], ah, bl[0], bl[1]);
-            mma_tf32(o[dt], ah, bh[0], bh[1]);
+            float part[4] = {};
+            mma_tf32(part, al, bh[0], bh[1]);
+            mma_tf32(part, ah, bl[0], bl[1]);
+            mma_tf32(part, ah, bh[0], bh[1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[dt][e] += part[e];
           }
         }
       }
@@ -405,7 +412,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
     if (poison) {
       int b, n, g;
       if (attn_row(job, t, t.row0 + r, b, n, g))
-        add_nonfinite<T, C>(job, t, head, n, max(t.prefix, seg0), seg1, c0, ot);
+        add_nonfinite<T, C>(job, t, head, n, max(t.clear, seg0), seg1, c0, ot);
     }
     if (nb == t.blocks) {
       write_row<T, C>(job, t, head, t.row0 + r, c0, DP, mt, lt, ot);
@@ -442,49 +449,115 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
 
 // ---------------------------------------------------------------------------------------
 // Join of the tiles cut between CTAs.  Block (j, y) looks whether CTA j left a tile open and
-// joins rows 16 y .. + 15 of its parts: CTA j's second slot, then the first slots of the
-// CTAs after it until the one that holds the tile's end.
+// joins some rows of its parts: CTA j's second slot, then the first slots of the CTAs after
+// it until the one that holds the tile's end.  A few rows of one long sequence leave a part in
+// every CTA: with GROUPS > 1 the parts are dealt to that many groups of threads, each joining
+// its own in the order of the keys, and the groups are joined through shared memory.
 // ---------------------------------------------------------------------------------------
+
+// Joins (ms, ls, x) to (m, l, o).
+template <int C>
+__device__ __forceinline__ void join_part(float& m, float& l, float (&o)[C], float ms, float ls,
+                                          const float (&x)[C]) {
+  if (ms == -CUDART_INF_F && ls == 0.f) return;  // sees none of these keys (NaN goes on)
+  const float mn = fmaxf(m, ms);
+  const float a = m == -CUDART_INF_F ? 0.f : exp2f(m - mn), b = exp2f(ms - mn);
+  l = l * a + ls * b;
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = o[i] * a + x[i] * b;
+  m = mn;
+}
+
+template <int DP, int R>
+struct CombineCfg {
+  static constexpr int kGroups = R == kRowsR ? 4 : 1;
+  static constexpr int kGroupThreads = kCombineThreads / kGroups;
+  static constexpr int kC = DP / 8;                 // columns of a thread
+  static constexpr int kRows = kGroupThreads / 8;   // rows of a block
+};
+
 template <typename T, int DP, int R, int KB>
 __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(AttnJob job, int ctas) {
+  using Cfg = CombineCfg<DP, R>;
+  constexpr int GROUPS = Cfg::kGroups, GT = Cfg::kGroupThreads, C = Cfg::kC, BR = Cfg::kRows;
+  constexpr int XG = GROUPS > 1 ? GROUPS - 1 : 1, XR = GROUPS > 1 ? BR : 1;
+  __shared__ float s_ms[XG][XR][2];
+  __shared__ float s_o[XG][XR][DP + 4];
+  __shared__ int s_end;
   const int j = blockIdx.x;
+  if (threadIdx.x == 0) s_end = ctas;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 desc = job.part_desc[j];
   if (!desc.x) return;
-  constexpr int C = kCombineRows * DP / kCombineThreads;
-  const int r = blockIdx.y * kCombineRows + threadIdx.x / (DP / C);
-  const int c0 = (threadIdx.x % (DP / C)) * C;
+  __syncthreads();
+  for (int i = j + 1 + threadIdx.x; i < ctas; i += kCombineThreads)
+    if (job.part_desc[i].w == kSlotEnd) {
+      atomicMin(&s_end, i);
+      break;
+    }
   const AttnTile t = attn_tile<R, KB>(job, desc.z);
+  const int grp = threadIdx.x / GT, tg = threadIdx.x % GT;
+  const int rr = tg / 8, r = blockIdx.y * BR + rr, c0 = (tg % 8) * C;
+  __syncthreads();
+  const int last = min(s_end, ctas - 1);  // its first slot holds the tile's end
   float m = -CUDART_INF_F, l = 0.f, o[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = 0.f;
-  auto join = [&](int slot) {
-    const float ms = job.part_ms[(slot * 2) * R + r];
-    const float ls = job.part_ms[(slot * 2 + 1) * R + r];
-    const float4* src = reinterpret_cast<const float4*>(job.part_o + ((int64_t)slot * R + r) * DP + c0);
-    float4 x[C / 4];
+#pragma unroll 2
+  for (int i = j + grp; i <= last; i += GROUPS) {
+    const bool none = i > j && job.part_desc[i].w == kSlotNone;  // a CTA without work
+    const int slot = i == j ? 2 * j + 1 : 2 * i;
+    const float ms = none ? -CUDART_INF_F : job.part_ms[(slot * 2) * R + r];
+    const float ls = none ? 0.f : job.part_ms[(slot * 2 + 1) * R + r];
+    const float4* src =
+        reinterpret_cast<const float4*>(job.part_o + ((int64_t)slot * R + r) * DP + c0);
+    float x[C];
 #pragma unroll
-    for (int i = 0; i < C / 4; ++i) x[i] = src[i];
-    if (ms == -CUDART_INF_F && ls == 0.f) return;  // sees none of these keys (NaN goes on)
-    const float mn = fmaxf(m, ms);
-    const float a = m == -CUDART_INF_F ? 0.f : exp2f(m - mn), b = exp2f(ms - mn);
-    l = l * a + ls * b;
-#pragma unroll
-    for (int i = 0; i < C / 4; ++i) {
-      o[4 * i] = o[4 * i] * a + x[i].x * b;
-      o[4 * i + 1] = o[4 * i + 1] * a + x[i].y * b;
-      o[4 * i + 2] = o[4 * i + 2] * a + x[i].z * b;
-      o[4 * i + 3] = o[4 * i + 3] * a + x[i].w * b;
+    for (int k = 0; k < C / 4; ++k) {
+      const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f) : src[k];
+      x[4 * k] = v.x;
+      x[4 * k + 1] = v.y;
+      x[4 * k + 2] = v.z;
+      x[4 * k + 3] = v.w;
     }
-    m = mn;
-  };
-  join(2 * j + 1);
-  for (int i = j + 1; i < ctas; ++i) {
-    const int what = job.part_desc[i].w;
-    if (what == kSlotNone) continue;  // a CTA without work
-    join(2 * i);
-    if (what == kSlotEnd) break;
+    join_part<C>(m, l, o, ms, ls, x);
+  }
+  if (GROUPS > 1) {
+    if (grp > 0) {
+      if (c0 == 0) {
+        s_ms[grp - 1][rr][0] = m;
+        s_ms[grp - 1][rr][1] = l;
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) s_o[grp - 1][rr][c0 + i] = o[i];
+    }
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int g = 0; g < GROUPS - 1; ++g) {
+      float x[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) x[i] = s_o[g][rr][c0 + i];
+      join_part<C>(m, l, o, s_ms[g][rr][0], s_ms[g][rr][1], x);
+    }
   }
   write_row<T, C>(job, t, desc.y, t.row0 + r, c0, DP, m, l, o);
+}
+
+// The join starts while the attention kernel's last CTAs still run and waits for them
+// (programmatic stream serialization).
+template <typename T, int DP, int R, int KB>
+cudaError_t launch_combine(const AttnJob& job, int ctas, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, R / CombineCfg<DP, R>::kRows);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, DP, R, KB>, job, ctas);
 }
 
 template <typename T, int DP>
@@ -507,17 +580,12 @@ cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
   attn_rows_kernel<T, DP><<<grid, kRowsThreads, Cfg::kSmem, s>>>(job);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_combine_kernel<T, DP, kRowsR, kRowsKB>
-      <<<dim3(grid, kRowsR / kCombineRows), kCombineThreads, 0, s>>>(job, grid);
-  return cudaGetLastError();
+  return launch_combine<T, DP, kRowsR, kRowsKB>(job, grid, s);
 }
-
-constexpr int kTcRows = 256, kTcKeys = 128;
 
 // rows of all slots of a launch, whichever kernel it is
 constexpr size_t kAttnSlotRows =
-    2 * (size_t)(kAttnTcCtas * kTcRows > kAttnMaxCtas * kRowsR ? kAttnTcCtas * kTcRows
-                                                               : kAttnMaxCtas * kRowsR);
+    2 * (size_t)(kAttnTcSlots > kAttnMaxCtas * kRowsR ? kAttnTcSlots : kAttnMaxCtas * kRowsR);
 
 struct AttnWs {
   size_t desc, ms, o, shared_lse, shared_o, total;
@@ -548,15 +616,12 @@ AttnWs attn_ws(int64_t rows, int Hq, int D, int shared_len) {
 
 }  // namespace
 
-cudaError_t launch_attn_combine(const AttnJob& job, int DP, int R, int KB, int ctas,
-                                cudaStream_t s) {
-  if (R != kTcRows || KB != kTcKeys) return cudaErrorInvalidValue;
-  const dim3 grid(ctas, kTcRows / kCombineRows);
-  if (DP == 64)
-    attn_combine_kernel<uint16_t, 64, kTcRows, kTcKeys><<<grid, kCombineThreads, 0, s>>>(job, ctas);
-  else
-    attn_combine_kernel<uint16_t, 128, kTcRows, kTcKeys><<<grid, kCombineThreads, 0, s>>>(job, ctas);
-  return cudaGetLastError();
+cudaError_t launch_attn_combine(const AttnJob& job, int DP, int R, int ctas, cudaStream_t s) {
+  if (R == 256)
+    return DP == 64 ? launch_combine<uint16_t, 64, 256, kAttnTcKeys>(job, ctas, s)
+                    : launch_combine<uint16_t, 128, 256, kAttnTcKeys>(job, ctas, s);
+  return DP == 64 ? launch_combine<uint16_t, 64, 128, kAttnTcKeys>(job, ctas, s)
+                  : launch_combine<uint16_t, 128, 128, kAttnTcKeys>(job, ctas, s);
 }
 
 namespace {
@@ -638,6 +703,8 @@ extern "C" int spec_tree_attention_paged(
   job.max_pages = max_pages;
   job.shared_len = shared_len;
   job.pd = PageDiv::make(cache.page_size);
+  job.by_g = FastDiv::make(job.G);
+  job.by_ng = FastDiv::make(N * job.G);
   job.scale_log2 = (float)((double)scale * 1.4426950408889634);
   job.part_desc = reinterpret_cast<int4*>(ws + w.desc);
   job.part_ms = reinterpret_cast<float*>(ws + w.ms);

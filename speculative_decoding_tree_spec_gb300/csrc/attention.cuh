@@ -23,10 +23,23 @@
 namespace svk {
 
 constexpr int kAttnMaxCtas = 512;  // grid limit: two slots per CTA in the workspace
-constexpr int kAttnTcCtas = 256;   // grid limit of the 256-row tiles
+constexpr int kAttnTcSlots = 256 * 256;  // tensor-memory kernel: limit of CTAs * rows of a tile
+constexpr int kAttnTcKeys = 128;  // keys of the tensor-memory kernel's block
 constexpr int kAttnRowsTile = 16;  // rows of the few-rows kernel's tile
 
 enum AttnPhase { kOwn = 0, kShared = 1 };
+
+// x / d by a multiplication: the high half of x * ceil(2^64 / d) is exact for x below 2^32.
+struct FastDiv {
+  uint64_t magic;
+  int d;
+  __host__ static FastDiv make(int d) {
+    return FastDiv{d > 1 ? ~0ull / (uint64_t)d + 1u : 0u, d};
+  }
+  __device__ __forceinline__ int div(int x) const {
+    return d == 1 ? x : (int)__umul64hi((uint64_t)(uint32_t)x, magic);
+  }
+};
 
 struct AttnJob {  // (the kernels' argument)
   const void *q, *k, *v;
@@ -40,6 +53,7 @@ struct AttnJob {  // (the kernels' argument)
   int row_tiles;   // tiles per sequence (kOwn) or in all (kShared)
   int entries;     // tiles of one key head
   PageDiv pd;
+  FastDiv by_g, by_ng;  // G, N * G
   float scale_log2;  // scale * log2(e)
   int phase;
   // result of the shared positions, [Hkv][B * N * G] rows: normalised output (row pitch DP)
@@ -56,8 +70,7 @@ bool attn_tc_fits(const AttnJob& job, spec_dtype dtype);
 // The tensor-memory kernel and its join; *taken = false where the cache's strides make no
 // tensor map (nothing was launched).
 cudaError_t launch_attn_tc(const AttnJob& job, cudaStream_t s, bool* taken);
-cudaError_t launch_attn_combine(const AttnJob& job, int DP, int R, int KB, int ctas,
-                                cudaStream_t s);
+cudaError_t launch_attn_combine(const AttnJob& job, int DP, int R, int ctas, cudaStream_t s);
 
 // What slot 0 of a CTA holds: nothing, the middle of a tile, the end of one.
 enum { kSlotNone = 0, kSlotMiddle = 1, kSlotEnd = 2 };
@@ -68,11 +81,26 @@ struct AttnTile {
   int row0;         // first row
   int prefix, count;
   int kbeg, kend;   // positions its rows can see at most
+  int clear;        // positions below it are seen by every query of the tile
   int blocks;       // units
 };
 
+// The lengths a tile needs from memory, read ahead of its use.
+struct AttnLens {
+  int prefix, count;
+};
+__device__ __forceinline__ AttnLens attn_lens(const AttnJob& job, int entry) {
+  AttnLens x{0, 0};
+  if (job.phase == kOwn && entry < job.entries) {
+    const int b = entry / job.row_tiles;
+    x.prefix = job.prefix[b];
+    x.count = job.counts ? job.counts[b] : job.N;
+  }
+  return x;
+}
+
 template <int R, int KB>
-__device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry) {
+__device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry, const AttnLens& lens) {
   AttnTile t;
   const int cap = job.max_pages * job.pd.size;
   if (job.phase == kShared) {
@@ -81,21 +109,29 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry) {
     t.prefix = job.shared_len;
     t.count = job.N;
     t.kbeg = 0;
-    t.kend = min(job.shared_len, cap);
+    t.kend = t.clear = min(job.shared_len, cap);
   } else {
     t.b = entry / job.row_tiles;
     t.row0 = (entry - t.b * job.row_tiles) * R;
-    t.prefix = min(max(job.prefix[t.b], 0), cap);  // no position beyond the table exists
-    t.count = job.counts ? min(max(job.counts[t.b], 0), job.N) : job.N;
+    t.prefix = min(max(lens.prefix, 0), cap);  // no position beyond the table exists
+    t.count = min(max(lens.count, 0), job.N);
     if (t.prefix < job.shared_len) t.count = 0;  // not a sequence behind the shared prefix
     t.kbeg = job.shared_len;
-    const int first = t.row0 / job.G, last = (min(t.row0 + R, job.N * job.G) - 1) / job.G;
+    const int first = job.by_g.div(t.row0);
+    const int last = job.by_g.div(min(t.row0 + R, job.N * job.G) - 1);
     int64_t end = (int64_t)t.prefix + (job.mask ? t.count : min(t.count, last + 1));
     if (first >= t.count) end = t.kbeg;  // only padding rows
     t.kend = (int)max((int64_t)t.kbeg, min(end, (int64_t)cap));
+    t.clear = min(t.kend, t.prefix);
+    if (!job.mask && first < t.count)
+      t.clear = (int)min((int64_t)t.kend, (int64_t)t.prefix + first + 1);
   }
   t.blocks = max(1, (t.kend - t.kbeg + KB - 1) / KB);
   return t;
+}
+template <int R, int KB>
+__device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry) {
+  return attn_tile<R, KB>(job, entry, attn_lens(job, entry));
 }
 
 // This CTA's units and where the first one lies: key head, tile, block in it.
@@ -155,13 +191,12 @@ __device__ __forceinline__ AttnRange attn_range(const AttnJob& job, int cta, int
 __device__ __forceinline__ bool attn_row(const AttnJob& job, const AttnTile& t, int r, int& b,
                                          int& node, int& g) {
   if (job.phase == kShared) {
-    const int ng = job.N * job.G;
-    b = r / ng;
-    r -= b * ng;
+    b = job.by_ng.div(r);
+    r -= b * job.by_ng.d;
   } else {
     b = t.b;
   }
-  node = r / job.G;
+  node = job.by_g.div(r);
   g = r - node * job.G;
   return job.phase == kShared ? b < job.B : node < job.N;
 }
@@ -245,8 +280,17 @@ __device__ __forceinline__ void write_row(const AttnJob& job, const AttnTile& t,
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float x = l == 0.f ? 0.f : o[i] * w;
-      if (so) x += so[i] * ws;
       o[i] = x;
+    }
+    if (so) {
+#pragma unroll
+      for (int i = 0; i < C; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(so + i);
+        o[i] += x.x * ws;
+        o[i + 1] += x.y * ws;
+        o[i + 2] += x.z * ws;
+        o[i + 3] += x.w * ws;
+      }
     }
   }
   const int h = head * job.G + g;

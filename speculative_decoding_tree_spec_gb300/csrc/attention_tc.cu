@@ -1,20 +1,27 @@
 // attention_tc.cu -- the many-rows kernel of the paged tree attention: bf16, tiles of 256
 // rows on the fifth-generation tensor cores.
 //
-// A CTA holds the queries of two halves of 128 rows in shared memory and walks its tile's
-// keys in blocks of 128:
+// A CTA holds the queries of one or two halves of 128 rows in shared memory and walks its
+// tile's keys in blocks of 128:
 //   warp 0      TMA producer: a block's keys and values, page by page (boxes of up to 128
 //               rows that never cross a page), with the 128-byte swizzle into a ring
 //   warp 1      MMA issuer: S_w = Q_w K^T (128 x 128, fp32 in tensor memory), then
 //               O_w += P_w V with P_w read from tensor memory and V as it lies (its rows are
 //               the product's inner direction)
-//   warps 4-7   softmax of half 0, one row per thread: the row of S into registers, running
-//   warps 8-11  maximum, exponentials, their sum, P back over S as bf16; half 1 likewise
+//   warps 2-5   softmax of half 0, one row per thread: the row of S into registers, running
+//   warps 6-9   maximum, exponentials, their sum, P back over S as bf16; half 1 likewise
 // The halves take turns on the tensor cores: while one half's exponentials are formed the
-// other half's products run.  The output stays in tensor memory and is scaled only when a
-// row's maximum has risen by more than 2^8 since it was last scaled (the exponentials then
-// stay below 2^8, far inside bf16's and fp32's range, and the quotient by their sum is the
-// same), so the read-modify-write of the output is rare.
+// other half's products run.  P goes out in two parts of 64 keys, so that the first part's
+// product runs while the second part's exponentials are formed.
+// The 128 scores of a row are read once for the maximum; the upper 64 stay in registers and
+// P goes over their place, so that the lower 64 can be read a second time and no thread needs
+// more than about 128 registers for them.
+// (Blocks of 64 keys with two score buffers per half, which take the scores off that chain,
+// were slower: a 128 x 64 product takes the tensor cores as long as a 128 x 128 one.)
+// The output stays in tensor memory and is scaled only when a row's maximum has risen by more
+// than 2^8 since it was last scaled (the exponentials then stay below 2^8, far inside bf16's
+// and fp32's range, and the quotient by their sum is the same), so the read-modify-write of
+// the output is rare.
 //
 // Every wait is bounded; one that gives up sets a flag, all later waits return at once, the
 // control flow runs to its end and the CTA's results become NaN.
@@ -25,23 +32,35 @@ namespace svk {
 
 namespace {
 
-constexpr int kTcR = 256, kTcHalf = 128, kTcKB = 128;
-constexpr int kTcThreads = 384;
-constexpr uint32_t kTcTmemCols = 512;
-constexpr float kTcLazy = 8.f;  // log2 of the rise that makes the output scaled
+constexpr int kTcHalf = 128, kTcKB = kAttnTcKeys;
+constexpr uint32_t kTcP = 64;      // P's column within a half's scores
+constexpr int kTcStagePitch = 80;  // bytes of a staged row: 64 and a pad against bank conflicts
+constexpr int kTcCheck = 4;        // blocks whose page numbers are checked at once
+constexpr uint64_t kTcLimitNs = 2000000000ull;  // of a wait
+constexpr float kTcLazy = 8.f;     // log2 of the rise that makes the output scaled
 
-template <int DP>
+// H halves of 128 rows in a tile.  H = 2: one CTA per SM.  H = 1 (tiles of at most 128 rows):
+// two CTAs per SM, each with half of the tensor memory, whose loads, products and epilogues
+// overlap each other's.
+template <int DP, int H>
 struct TcCfg {
-  static constexpr int kChunks = DP / 64;                  // 128-byte columns of a row
-  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kR = kTcHalf * H;
+  static constexpr int kThreads = 64 + kTcHalf * H;
+  static constexpr uint32_t kTmemCols = 256 * H;            // per half: scores, output
+  static constexpr int kChunks = DP / 64;                   // 128-byte columns of a row
+  static constexpr int kQChunkBytes = kTcHalf * 128;
+  static constexpr int kQHalfBytes = kChunks * kQChunkBytes;
+  static constexpr int kQBytes = H * kQHalfBytes;
+  static constexpr int kChunkBytes = kTcKB * 128;
   static constexpr int kStageBytes = kChunks * kChunkBytes; // 128 keys (or values)
-  static constexpr int kQBytes = 2 * kStageBytes;
-  static constexpr int kStages = DP == 64 ? 8 : 4;
-  static constexpr int kSmem = 1024 + kQBytes + kStages * kStageBytes;
+  static constexpr int kStages = (DP == 64 ? 4 : 2) * H;
+  static constexpr int kStaging = 4 * H * kTcStagePitch * 32;  // a warp's 32 rows of 64 bytes
+  static constexpr int kSmem = 1024 + kQBytes + kStages * kStageBytes + kStaging;
 };
 
 struct TcShared {
-  uint64_t full[8], empty[8], q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint64_t full[8], empty[8];  // ring entries: key and value blocks in turn
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], done;
   uint32_t tmem;
   int abort;
   int poison;
@@ -49,28 +68,32 @@ struct TcShared {
 
 struct TcWait {
   int* abort;
+  __device__ __forceinline__ bool aborted() const { return *((volatile int*)abort) != 0; }
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
-    if (mbar_try(bar, parity)) return;
-    const uint64_t t0 = global_ns();
-    for (;;) {
-      for (int k = 0; k < 32; ++k)
-        if (mbar_try(bar, parity)) return;
-      if (*((volatile int*)abort)) return;
-      if (global_ns() - t0 > 2000000000ull) {
-        *((volatile int*)abort) = 1;
-        return;
+    // the clock is read after many tries only: a read takes longer than most waits
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1;; ++tries) {
+      if (mbar_try(bar, parity)) return;
+      if ((tries & 1023u) == 0) {
+        if (aborted()) return;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kTcLimitNs) {
+          *((volatile int*)abort) = 1;
+          return;
+        }
       }
     }
   }
 };
 
-
-template <int DP>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int DP, int H>
+__global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnJob job,
                    int box_rows) {
-  using Cfg = TcCfg<DP>;
+  using Cfg = TcCfg<DP, H>;
+  constexpr int kTcR = Cfg::kR;
   constexpr int NST = Cfg::kStages;
   __shared__ TcShared sh;
   extern __shared__ unsigned char tc_dyn[];
@@ -85,9 +108,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sh.empty[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&sh.q_full[w], kTcHalf);
+      mbar_init(&sh.q_full[w], 4);
       mbar_init(&sh.s_full[w], 1);
-      mbar_init(&sh.p_full[w], kTcHalf);
+      mbar_init(&sh.p_full[w][0], 4);
+      mbar_init(&sh.p_full[w][1], 4);
       mbar_init(&sh.o_full[w], 1);
     }
     mbar_init(&sh.done, 1);
@@ -95,8 +119,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     sh.poison = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tc05_alloc(&sh.tmem, kTcTmemCols);
-  const AttnRange range = attn_range<kTcR, kTcKB, kTcThreads>(job, cta, gridDim.x);
+  if (warp == 1) tc05_alloc(&sh.tmem, Cfg::kTmemCols);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may line up
+  const AttnRange range = attn_range<kTcR, kTcKB, Cfg::kThreads>(job, cta, gridDim.x);
   tc05_fence_before();
   __syncthreads();
   tc05_fence_after();
@@ -108,41 +133,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int head = range.head, entry = range.entry, block = range.block;
   uint32_t ent = 0;  // ring entries so far: key and value blocks in turn
 
+  AttnLens lens = attn_lens(job, entry);  // read a tile ahead from here on
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     const int boxes = kTcKB / box_rows;
     while (left > 0) {
-      const AttnTile t = attn_tile<kTcR, kTcKB>(job, entry);
+      const AttnTile t = attn_tile<kTcR, kTcKB>(job, entry, lens);
+      lens = attn_lens(job, entry + 1 == job.entries ? 0 : entry + 1);
       const int nb = (int)min((int64_t)(t.blocks - block), left);
       const int32_t* table_row = job.table + (int64_t)t.b * job.max_pages;
-      for (int i = 0; i < nb; ++i) {
-        // a box with no page, or past the last visible key, is read outside the cache: zeros
-        int page = job.n_pages, slot = 0;
+      const int pos0 = t.kbeg + block * kTcKB + lane * box_rows;  // this lane's box of block 0
+      auto page_of = [&](int i) {
+        const int pos = pos0 + i * kTcKB;
+        return lane < boxes && i < nb && pos < t.kend ? table_row[job.pd.div(pos)] : -1;
+      };
+      // one box of each 64 columns; a box with no page, or past the last visible key, is read
+      // outside the cache: zeros
+      auto issue = [&](const CUtensorMap* tm, int page, int i) {
+        const int s = (int)(ent % NST);
+        wait(&sh.empty[s], ((ent / NST) & 1u) ^ 1u);
+        if (__any_sync(kFull, wait.aborted())) return;  // the stage may still be in use
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], Cfg::kStageBytes);
+        __syncwarp();
         if (lane < boxes) {
-          const int pos = t.kbeg + (block + i) * kTcKB + lane * box_rows;
-          const int at = job.pd.div(pos);
-          if (pos < t.kend && at < job.max_pages) {
-            const int p = table_row[at];
-            if ((unsigned)p < (unsigned)job.n_pages) {
-              page = p;
-              slot = pos - at * job.pd.size;
-            }
-          }
-        }
+          const int pos = pos0 + i * kTcKB;
+          const bool there = (unsigned)page < (unsigned)job.n_pages;
+          const int slot = there ? pos - job.pd.div(pos) * job.pd.size : 0;
+          const uint32_t dst = ring + s * Cfg::kStageBytes + lane * box_rows * 128;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++ent) {
-          const int s = (int)(ent % NST);
-          wait(&sh.empty[s], ((ent / NST) & 1u) ^ 1u);
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], Cfg::kStageBytes);
-          __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = ring + s * Cfg::kStageBytes + lane * box_rows * 128;
-#pragma unroll
-            for (int c = 0; c < Cfg::kChunks; ++c)
-              tma_load_4d(dst + c * Cfg::kChunkBytes, kv ? &tm_v : &tm_k, c * 64, head, slot, page,
-                          &sh.full[s]);
-          }
+          for (int c = 0; c < Cfg::kChunks; ++c)
+            tma_load_4d(dst + c * Cfg::kChunkBytes, tm, c * 64, head, slot,
+                        there ? page : job.n_pages, &sh.full[s]);
         }
+        ++ent;
+      };
+      int page = page_of(0);
+      for (int i = 0; i < nb; ++i) {
+        const int next = page_of(i + 1);
+        issue(&tm_k, page, i);
+        issue(&tm_v, page, i);
+        page = next;
       }
       left -= nb;
       block = 0;
@@ -153,149 +183,199 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     // no copy may still be landing when the CTA exits
     const uint32_t first = ent > (uint32_t)NST ? ent - NST : 0u;
-    for (uint32_t e = first; e < ent; ++e) wait(&sh.full[e % NST], (e / NST) & 1u);
+    for (uint32_t e = first; e < ent; ++e)
+      mbar_wait(&sh.full[e % NST], (e / NST) & 1u, kTcLimitNs);
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = bf16_idesc(kTcKB, false), idesc_o = bf16_idesc(DP, true);
-      uint32_t seg[2] = {0, 0}, blk[2] = {0, 0};
-      auto scores = [&](int w, uint32_t e) {
-        const uint64_t a = sw128_tile(sq + w * Cfg::kStageBytes, 16);
-        const uint64_t b = sw128_tile(ring + (e % NST) * Cfg::kStageBytes, 16);
+    constexpr uint32_t idesc_s = bf16_idesc(kTcKB, false), idesc_o = bf16_idesc(DP, true);
+    uint32_t seg[H] = {}, blk[H] = {};
+    auto scores = [&](int w, uint32_t stage) {
+      const uint64_t a = sw128_tile(sq + w * Cfg::kQHalfBytes, 16);
+      const uint64_t b = sw128_tile(ring + stage * Cfg::kStageBytes, 16);
+      if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) {
-          const uint64_t off = (uint64_t)(((ks >> 2) * Cfg::kChunkBytes + (ks & 3) * 32) >> 4);
-          tc05_mma_ss(tmem + w * 128, a + off, b + off, idesc_s, ks > 0);
-        }
-      };
-      while (left > 0) {
-        const AttnTile t = attn_tile<kTcR, kTcKB>(job, entry);
-        const int nb = (int)min((int64_t)(t.blocks - block), left);
-        const int halves = rows_all - t.row0 > kTcHalf ? 2 : 1;
-        for (int w = 0; w < halves; ++w) wait(&sh.q_full[w], seg[w]++ & 1u);
-        wait(&sh.full[ent % NST], (ent / NST) & 1u);
-        tc05_fence_after();
-        for (int w = 0; w < halves; ++w) {
-          scores(w, ent);
-          tc05_commit(&sh.s_full[w]);
-        }
-        tc05_commit(&sh.empty[ent % NST]);
-        for (int i = 0; i < nb; ++i) {
-          const uint32_t ev = ent + 2 * i + 1, ek = ev + 1;
-          wait(&sh.full[ev % NST], (ev / NST) & 1u);
-          for (int w = 0; w < halves; ++w) {
-            wait(&sh.p_full[w], blk[w]++ & 1u);
+        for (int ks = 0; ks < DP / 16; ++ks)
+          tc05_mma_ss(tmem + w * 256,
+                      a + (uint64_t)(((ks >> 2) * Cfg::kQChunkBytes + (ks & 3) * 32) >> 4),
+                      b + (uint64_t)(((ks >> 2) * Cfg::kChunkBytes + (ks & 3) * 32) >> 4), idesc_s,
+                      ks > 0);
+        tc05_commit(&sh.s_full[w]);
+      }
+      __syncwarp();
+    };
+    auto release = [&](uint32_t stage) {
+      if (elect_one()) tc05_commit(&sh.empty[stage]);
+      __syncwarp();
+    };
+    // the ring's position: stage of the next entry and its barrier's parity
+    uint32_t st = 0, par = 0;
+    auto advance = [&]() {
+      if (++st == (uint32_t)NST) {
+        st = 0;
+        par ^= 1u;
+      }
+    };
+    // (after a wait that gave up the products run on whatever the buffers hold, within their
+    // bounds)
+    while (left > 0) {
+      const AttnTile t = attn_tile<kTcR, kTcKB>(job, entry, lens);
+      lens = attn_lens(job, entry + 1 == job.entries ? 0 : entry + 1);
+      const int nb = uniform((int)min((int64_t)(t.blocks - block), left));
+      const int halves = uniform(H == 2 && rows_all - t.row0 > kTcHalf ? 2 : 1);
+#pragma unroll
+      for (int w = 0; w < H; ++w)
+        if (w < halves) wait(&sh.q_full[w], seg[w]++ & 1u);
+      wait(&sh.full[st], par);
+      tc05_fence_after();
+#pragma unroll
+      for (int w = 0; w < H; ++w)
+        if (w < halves) scores(w, st);
+      release(st);
+      advance();
+      for (int i = 0; i < nb; ++i) {
+        const bool more = i + 1 < nb;
+        const uint32_t sv = st, pv = par;  // V_i; K_{i+1} follows it
+        advance();
+        const uint32_t sk = st, pk = par;
+        if (more) advance();
+        wait(&sh.full[sv], pv);
+#pragma unroll
+        for (int w = 0; w < H; ++w) {
+          if (w >= halves) break;
+          const uint32_t parity = blk[w]++ & 1u;
+          const uint64_t b = sw128_tile(ring + sv * Cfg::kStageBytes, Cfg::kChunkBytes);
+          // keys 64 .. 127 first: their exponentials are
+#pragma unroll
+          for (int part = 1; part >= 0; --part) {
+            wait(&sh.p_full[w][part], parity);
             tc05_fence_after();
-            const uint64_t b = sw128_tile(ring + (ev % NST) * Cfg::kStageBytes, Cfg::kChunkBytes);
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < kTcKB / 16; ++ks)
-              tc05_mma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8,
-                          b + (uint64_t)((ks * 2048) >> 4), idesc_o, i > 0 || ks > 0);
-            if (w == halves - 1) tc05_commit(&sh.empty[ev % NST]);
-            if (i + 1 < nb) {
-              if (w == 0) {
-                wait(&sh.full[ek % NST], (ek / NST) & 1u);
-                tc05_fence_after();
-              }
-              scores(w, ek);
-              tc05_commit(&sh.s_full[w]);
-              if (w == halves - 1) tc05_commit(&sh.empty[ek % NST]);
-            } else {
-              tc05_commit(&sh.o_full[w]);
+              for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+                tc05_mma_ts(tmem + w * 256 + 128, tmem + w * 256 + kTcP + ks * 8,
+                            b + (uint64_t)((ks * 2048) >> 4), idesc_o,
+                            i > 0 || part == 0 || ks > 4);
+              if (part == 0 && !more) tc05_commit(&sh.o_full[w]);
             }
+            __syncwarp();
+          }
+          if (w == halves - 1) release(sv);
+          if (more) {
+            if (w == 0) {
+              wait(&sh.full[sk], pk);
+              tc05_fence_after();
+            }
+            scores(w, sk);
+            if (w == halves - 1) release(sk);
           }
         }
-        ent += 2 * nb;
-        left -= nb;
-        block = 0;
-        if (++entry == job.entries) {
-          entry = 0;
-          ++head;
-        }
       }
-      tc05_commit(&sh.done);
-      wait(&sh.done, 0u);
+      left -= nb;
+      block = 0;
+      if (++entry == job.entries) {
+        entry = 0;
+        ++head;
+      }
     }
+    // every product issued has finished before the tensor memory is freed
+    if (elect_one()) tc05_commit(&sh.done);
     __syncwarp();
-  } else if (warp >= 4) {
+    mbar_wait(&sh.done, 0u, kTcLimitNs);
+    __syncwarp();
+  } else {
     // ---------------- softmax and epilogue of one half ----------------
-    const int w = (warp - 4) >> 2;
-    const int tid = (int)threadIdx.x - 128 - w * 128;  // 0 .. 127: the row within the half
+    // A warp's tensor-memory lanes are 32 (warp % 4) .. + 31: rows of the half by that number.
+    const int w = (warp - 2) >> 2;
+    const int tid = (warp & 3) * 32 + lane;  // 0 .. 127: the row within the half
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = lanes + w * 128, t_o = lanes + 256 + w * 128;
+    const uint32_t t_s = lanes + w * 256, t_o = t_s + 128;
     const float c = fabsf(job.scale_log2);
     const uint32_t flip = job.scale_log2 < 0.f ? 0x80008000u : 0u;  // the maximum wants c >= 0
     const int boxes = kTcKB / box_rows, box_shift = 31 - __clz(box_rows);
-    uint32_t seg = 0, blk = 0;
+    uint32_t blk = 0, seg = 0;  // blocks and segments of this half so far
 
-    // the half's queries into shared memory (K-major, 128-byte swizzle)
-    auto load_q = [&](int hd, int en) {
-      const AttnTile t = attn_tile<kTcR, kTcKB>(job, en);
-      if (w == 1 && rows_all - t.row0 <= kTcHalf) return;
-      constexpr int CPR = DP / 8;  // 16-byte units of a row
-      const int u = tid % CPR;
-      unsigned char* dst = base_p + w * Cfg::kStageBytes + (u >> 3) * Cfg::kChunkBytes;
-      constexpr int kBatch = 8;
-      for (int r0 = tid / CPR; r0 < kTcHalf; r0 += kBatch * (kTcHalf / CPR)) {
-        uint4 x[kBatch];
+    // the half's queries into shared memory (K-major, 128-byte swizzle): each warp its 32 rows,
+    // a few rows to a load, all loads in flight
+    auto load_q = [&](int hd, const AttnTile& t) {
+      if (H == 2 && w == 1 && rows_all - t.row0 <= kTcHalf) return;
+      int b, node, g;
+      const bool real = attn_row(job, t, t.row0 + w * kTcHalf + tid, b, node, g);
+      const int64_t mine = real ? b * job.lq.batch_stride + node * job.lq.node_stride +
+                                      (hd * job.G + g) * job.lq.head_stride
+                                : (int64_t)-1;
+      constexpr int CPR = DP / 8, STEP = 32 / CPR;  // 16-byte units of a row; rows of a step
+      const int u = lane % CPR, r0 = lane / CPR;
+      unsigned char* dst = base_p + w * Cfg::kQHalfBytes + (u >> 3) * Cfg::kQChunkBytes;
+      uint4 x[CPR];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + i * (kTcHalf / CPR);
-          x[i] = make_uint4(0, 0, 0, 0);
-          int b, node, g;
-          if (r < kTcHalf && attn_row(job, t, t.row0 + w * kTcHalf + r, b, node, g) &&
-              u * 8 < job.D)
-            x[i] = *reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(job.q) + b * job.lq.batch_stride +
-                node * job.lq.node_stride + (hd * job.G + g) * job.lq.head_stride + u * 8);
-        }
+      for (int i = 0; i < CPR; ++i) {
+        const int64_t at = __shfl_sync(kFull, mine, r0 + i * STEP);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (at >= 0 && u * 8 < job.D)
+          x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(job.q) + at + u * 8);
+      }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = r0 + i * (kTcHalf / CPR);
-          if (r >= kTcHalf) break;
-          x[i].x ^= flip;
-          x[i].y ^= flip;
-          x[i].z ^= flip;
-          x[i].w ^= flip;
-          *reinterpret_cast<uint4*>(dst + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[i];
-        }
+      for (int i = 0; i < CPR; ++i) {
+        const int r = (warp & 3) * 32 + r0 + i * STEP;
+        x[i].x ^= flip;
+        x[i].y ^= flip;
+        x[i].z ^= flip;
+        x[i].w ^= flip;
+        *reinterpret_cast<uint4*>(dst + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[i];
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sh.q_full[w]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[w]);
     };
-    if (left > 0) load_q(head, entry);
+    AttnTile t = attn_tile<kTcR, kTcKB>(job, entry, lens);
+    if (left > 0) load_q(head, t);
     int4 desc = make_int4(0, 0, 0, kSlotNone);
     while (left > 0) {
-      const AttnTile t = attn_tile<kTcR, kTcKB>(job, entry);
       const int nb = (int)min((int64_t)(t.blocks - block), left);
-      const int halves = rows_all - t.row0 > kTcHalf ? 2 : 1;
+      const int halves = H == 2 && rows_all - t.row0 > kTcHalf ? 2 : 1;
       int next_head = head, next_entry = entry + 1;
       if (next_entry == job.entries) {
         next_entry = 0;
         ++next_head;
       }
+      lens = attn_lens(job, next_entry);
       const int seg0 = t.kbeg + block * kTcKB;
+      if (nb != t.blocks) {
+        if (block == 0) {
+          desc.x = 1;
+          desc.y = head;
+          desc.z = entry;
+        } else {
+          desc.w = block + nb == t.blocks ? kSlotEnd : kSlotMiddle;
+        }
+      }
       if (w < halves) {
         const int r = t.row0 + w * kTcHalf + tid;
         int rb, node, g;
         const bool real = attn_row(job, t, r, rb, node, g);
         const int32_t* table_row = job.table + (int64_t)t.b * job.max_pages;
         float m = -CUDART_INF_F, l = 0.f;
-        // page of this lane's box of the next block
-        auto box_ok = [&](int i) {
-          const int pos = seg0 + i * kTcKB + lane * box_rows;
-          if (lane >= boxes || pos >= t.kend) return true;  // past the end: masked there
-          const int at = job.pd.div(pos);
-          return at < job.max_pages && (unsigned)table_row[at] < (unsigned)job.n_pages;
+        // Page numbers of the next kTcCheck blocks, two boxes of each lane, read ahead (0 past
+        // the last visible key: masked there).  Only where one is no page are the keys of the
+        // blocks looked at one by one.
+        auto page_at = [&](int i, int box) {
+          const int pos = seg0 + i * kTcKB + box * box_rows;
+          if (i >= nb || box >= kTcCheck * boxes || pos >= t.kend) return 0;
+          return table_row[job.pd.div(pos)];  // kend lies within the table
         };
-        bool ok_next = box_ok(0);
+        int ahead_a = page_at(0, lane), ahead_b = page_at(0, lane + 32);
+        bool bad = false;
         for (int i = 0; i < nb; ++i) {
           const int pos0 = seg0 + i * kTcKB;
-          const unsigned ok = __ballot_sync(kFull, ok_next);
-          if (i + 1 < nb) ok_next = box_ok(i + 1);
-          const bool drafts = pos0 + kTcKB > min(t.prefix, t.kend);  // rows may differ in what they see
+          if (i % kTcCheck == 0) {
+            bad = __any_sync(kFull, (unsigned)ahead_a >= (unsigned)job.n_pages ||
+                                        (unsigned)ahead_b >= (unsigned)job.n_pages);
+            ahead_a = page_at(i + kTcCheck, lane);
+            ahead_b = page_at(i + kTcCheck, lane + 32);
+          }
+          const bool drafts = pos0 + kTcKB > t.clear;  // rows may differ in what they see
           uint32_t sees[4];
-          if (drafts || ok != kFull) {
+          if (drafts || bad) {
             // bit k of word j: this row sees key 32 j + k of the block
             const int lim = min(t.prefix, t.kend) - pos0;
 #pragma unroll
@@ -303,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int n = min(max(lim - 32 * j, 0), 32);
               sees[j] = n == 32 ? kFull : (1u << n) - 1u;
             }
-            if (drafts && job.phase == kOwn && real && node < t.count) {
+            if (drafts && job.phase == kOwn) {
               const int from = max(pos0, t.prefix), to = min(pos0 + kTcKB, t.kend);
               if (!job.mask) {
                 const int end = min(to - t.prefix, node + 1) + (t.prefix - pos0);
@@ -313,16 +393,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   sees[j] = n == 32 ? kFull : (1u << n) - 1u;
                 }
               } else {
-                const uint8_t* mrow = job.mask + ((int64_t)t.b * job.N + node) * job.N - t.prefix;
+                // the warp reads its nodes' mask rows together, 32 keys of a node at a time
+                const int n0 = __shfl_sync(kFull, node, 0);
+                const int n1 = min(__shfl_sync(kFull, node, 31), t.count - 1);
+                const uint8_t* mrow = job.mask + ((int64_t)t.b * job.N + n0) * job.N - t.prefix;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  const int lo = max(from, pos0 + 32 * j), hi = min(to, pos0 + 32 * j + 32);
-                  for (int p = lo; p < hi; ++p)
-                    if (mrow[p]) sees[j] |= 1u << (p - pos0 - 32 * j);
+                  const int p = pos0 + 32 * j + lane;
+                  if (p - lane >= to || p - lane + 32 <= from) continue;
+                  const bool in = p >= from && p < to;
+                  for (int n = n0; n <= n1; n += 8) {
+                    uint8_t x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                      x[e] = in && n + e <= n1 ? mrow[(int64_t)(n + e - n0) * job.N + p] : (uint8_t)0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                      const unsigned bits = __ballot_sync(kFull, x[e] != 0);
+                      if (node == n + e) sees[j] |= bits;
+                    }
+                  }
                 }
               }
             }
-            if (ok != kFull) {
+            if (bad) {
+              const int mine = page_at(i, lane);
+              const unsigned ok = __ballot_sync(
+                  kFull, lane >= boxes || (unsigned)mine < (unsigned)job.n_pages);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 for (int k = 0; k < 32; k += 8)
@@ -333,7 +430,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ++blk;
           __syncwarp();
           tc05_fence_after();
-          uint32_t s[128];
+          uint32_t s[kTcKB];
           tc05_ld32(t_s, s);
           tc05_ld32(t_s + 32, s + 32);
           tc05_ld32(t_s + 64, s + 64);
@@ -343,14 +440,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc05_landed(s + 32);
           tc05_landed(s + 64);
           tc05_landed(s + 96);
-          if (drafts || ok != kFull) {
+          if (drafts || bad) {
 #pragma unroll
-            for (int k = 0; k < 128; ++k)
+            for (int k = 0; k < kTcKB; ++k)
               if (!((sees[k >> 5] >> (k & 31)) & 1u)) s[k] = 0xff800000u;  // -inf
           }
           float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int k = 0; k < 128; k += 8)
+          for (int k = 0; k < kTcKB; k += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1])));
@@ -359,7 +456,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (__any_sync(kFull, rise)) {
             const float a = (rise && m != -CUDART_INF_F) ? ex2_approx((m - mn) * c)
                             : (rise ? 0.f : 1.f);
-            if (i > 0) {
+            if (i > 0) {  // (these scores were issued after the last product of the output)
 #pragma unroll 1
               for (int ch = 0; ch < DP; ch += 16) {
                 uint32_t o[16];
@@ -374,34 +471,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             l *= a;
             if (rise) m = mn;
           }
-          const float mc = m == -CUDART_INF_F ? 0.f : m * c;
-          const float2 c2 = make_float2(c, c), n2 = make_float2(-mc, -mc);
-          float2 sum = make_float2(0.f, 0.f), sum2 = sum;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t p[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const int e = 64 * half + 2 * k;
-              float2 x = fma_f32x2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
-                                   c2, n2);
-              x.x = ex2_approx(x.x);
-              x.y = ex2_approx(x.y);
-              if (k & 1) sum = add_f32x2(sum, x);
-              else sum2 = add_f32x2(sum2, x);
-              p[k] = pack_bf16(x.x, x.y);
-            }
-            tc05_st32(t_s + 32 * half, p);
-          }
-          sum = add_f32x2(sum, sum2);
-          l += sum.x + sum.y;
           if (drafts) {
             // values past the last visible key leave the product, and so do infinities and
             // NaN among the drafts (a row that does not see them has weight 0 for them)
             const uint32_t ev = ent + 2 * i + 1;
             wait(&sh.full[ev % NST], (ev / NST) & 1u);
             constexpr int CPR = DP / 8;
-            const int k0 = max(t.prefix - pos0, 0), kn = t.kend - pos0;
+            const int k0 = max(t.clear - pos0, 0), kn = t.kend - pos0;
             unsigned char* vb = base_p + Cfg::kQBytes + (ev % NST) * Cfg::kStageBytes;
             for (int x = k0 * CPR + w * kTcHalf + tid; x < kTcKB * CPR; x += halves * kTcHalf) {
               const int key = x / CPR, u = x % CPR;
@@ -425,23 +501,139 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_proxy_async_smem();
             asm volatile("bar.sync 2, %0;\n" ::"r"(halves * kTcHalf) : "memory");
           }
-          __syncwarp();
-          tc05_wait_st();
-          tc05_fence_before();
-          mbar_arrive(&sh.p_full[w]);
+          const float mc = m == -CUDART_INF_F ? 0.f : m * c;
+          const float2 c2 = make_float2(c, c), n2 = make_float2(-mc, -mc);
+          float2 sum = make_float2(0.f, 0.f), sum2 = sum;
+          uint32_t* z = s + 64;
+#pragma unroll
+          for (int part = 1; part >= 0; --part) {
+            if (part == 0) {
+              tc05_ld32(t_s, z);
+              tc05_ld32(t_s + 32, z + 32);
+              tc05_wait_ld();
+              tc05_landed(z);
+              tc05_landed(z + 32);
+              if (drafts || bad) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                  if (!((sees[k >> 5] >> (k & 31)) & 1u)) z[k] = 0xff800000u;
+              }
+            }
+            uint32_t p[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float2 x = fma_f32x2(make_float2(__uint_as_float(z[2 * k]),
+                                               __uint_as_float(z[2 * k + 1])), c2, n2);
+              x.x = ex2_approx(x.x);
+              x.y = ex2_approx(x.y);
+              if (k & 1) sum = add_f32x2(sum, x);
+              else sum2 = add_f32x2(sum2, x);
+              p[k] = pack_bf16(x.x, x.y);
+            }
+            tc05_st32(t_s + kTcP + 32 * part, p);
+            tc05_wait_st();
+            tc05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[w][part]);
+          }
+          sum = add_f32x2(sum, sum2);
+          l += sum.x + sum.y;
         }
         // the last scores are read: the half's queries may be replaced
-        if (left > nb) load_q(next_head, next_entry);
+        const AttnTile t_next = attn_tile<kTcR, kTcKB>(job, next_entry, lens);
+        if (left > nb) load_q(next_head, t_next);
+
+        // ---- epilogue.  Each thread scales its row; the rows leave through the warp's staging
+        // area, four lanes to the 64 bytes of a row, so that a store fills whole sectors. ----
+        const bool whole = nb == t.blocks;
+        const bool wide = !whole || job.phase == kShared;  // fp32 rows
+        const int slot = 2 * cta + (block == 0 ? 1 : 0);
+        const int rr = w * kTcHalf + tid;
+        const int64_t shared_row = job.phase == kShared
+            ? (int64_t)head * job.B * job.N * job.G + r
+            : ((int64_t)head * job.B + rb) * job.N * job.G + r;
+        const bool prior = whole && job.phase == kOwn && job.shared_len > 0;
+        int64_t to = -1;  // this row's destination
+        if (!whole) to = ((int64_t)slot * kTcR + rr) * DP;
+        else if (real) to = job.phase == kShared ? shared_row * DP
+                                                 : rb * job.lo.batch_stride +
+                                                       node * job.lo.node_stride +
+                                                       (head * job.G + g) * job.lo.head_stride;
+        // this lane's part of the rows lane / 4 + 8 i of the warp
+        const int sub = lane & 3;
+        int64_t dst[4], src[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dst[i] = __shfl_sync(kFull, to, (lane >> 2) + 8 * i);
+          src[i] = __shfl_sync(kFull, real ? shared_row * DP : (int64_t)-1, (lane >> 2) + 8 * i);
+        }
+        unsigned char* stage = base_p + Cfg::kQBytes + NST * Cfg::kStageBytes +
+                               (w * 4 + (warp & 3)) * 32 * kTcStagePitch;
+        unsigned char* stage_row = stage + lane * kTcStagePitch;
+        unsigned char* stage_out = stage + (lane >> 2) * kTcStagePitch + sub * 16;
+        float4 ahead[4];  // the shared positions' result, 16 columns ahead
+        auto fetch = [&](int col) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ahead[i] = src[i] >= 0 ? *reinterpret_cast<const float4*>(job.shared_o + src[i] + col +
+                                                                      sub * 4)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        if (prior) fetch(0);
+        const float s2 = prior && real ? job.shared_lse[shared_row] : -CUDART_INF_F;
         wait(&sh.o_full[w], seg & 1u);
         ++seg;
         __syncwarp();
         tc05_fence_after();
         if (*((volatile int*)&sh.abort)) l = __int_as_float(0x7fc00000);
+        if (*((volatile int*)&sh.poison) && job.phase == kOwn) {
+          const int seg1 = min(seg0 + nb * kTcKB, t.kend);
+#pragma unroll 1
+          for (int ch = 0; ch < DP; ch += 16) {
+            uint32_t o[16];
+            __syncwarp();
+            tc05_ld16(t_o + ch, o);
+            tc05_wait_ld();
+            tc05_landed16(o);
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]);
+            if (real)
+              add_nonfinite<uint16_t, 16>(job, t, head, node, max(t.clear, seg0), seg1, ch, x);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(x[k]);
+            __syncwarp();
+            tc05_st16(t_o + ch, o);
+          }
+          tc05_wait_st();
+        }
         const float m2 = m == -CUDART_INF_F ? m : m * c;
-        const bool whole = nb == t.blocks;
-        const int slot = 2 * cta + (block == 0 ? 1 : 0);
-        const int seg1 = min(seg0 + nb * kTcKB, t.kend);
-        const bool poisoned = *((volatile int*)&sh.poison) != 0;
+        // the row's weight, and the shared positions' where they are joined
+        bool some = l != 0.f;
+        float wo = 1.f, ws = 0.f;
+        if (!whole) {
+          job.part_ms[(slot * 2) * kTcR + rr] = m2;
+          job.part_ms[(slot * 2 + 1) * kTcR + rr] = l;
+          some = true;
+        } else if (job.phase == kShared) {
+          wo = 1.f / l;
+          if (real) job.shared_lse[shared_row] = some ? m2 + log2f(l) : -CUDART_INF_F;
+        } else {
+          const bool query = real && node < t.count;
+          some = some && query;
+          float lse2 = some ? m2 + log2f(l) : -CUDART_INF_F;
+          wo = 1.f / l;
+          if (query && s2 != -CUDART_INF_F) {
+            const float top = fmaxf(s2, lse2);
+            const float es = exp2f(s2 - top), eo = some ? exp2f(lse2 - top) : 0.f;
+            ws = es / (es + eo);
+            wo = eo / (es + eo) / l;
+            lse2 = top + log2f(es + eo);
+          }
+          if (real && job.lse)
+            job.lse[((int64_t)rb * job.N + node) * job.Hq + head * job.G + g] =
+                lse2 * 0.693147180559945309f;
+        }
 #pragma unroll 1
         for (int ch = 0; ch < DP; ch += 32) {
           uint32_t o[32];
@@ -451,36 +643,63 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc05_landed(o);
           float of[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) of[k] = __uint_as_float(o[k]);
-          if (poisoned && job.phase == kOwn && real)
-            add_nonfinite<uint16_t, 32>(job, t, head, node, max(t.prefix, seg0), seg1, ch, of);
-          if (whole) {
-            write_row<uint16_t, 32>(job, t, head, r, ch, DP, m2, l, of);
-          } else {
-            const int rr = r - t.row0;
-            float4* dst =
-                reinterpret_cast<float4*>(job.part_o + ((int64_t)slot * kTcR + rr) * DP + ch);
+          for (int k = 0; k < 32; ++k) of[k] = some ? __uint_as_float(o[k]) * wo : 0.f;
+          if (prior) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              dst[k / 4] = make_float4(of[k], of[k + 1], of[k + 2], of[k + 3]);
-            if (ch == 0) {
-              job.part_ms[(slot * 2) * kTcR + rr] = m2;
-              job.part_ms[(slot * 2 + 1) * kTcR + rr] = l;
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(stage_out + 8 * i * kTcStagePitch) = ahead[i];
+              if (ch + 16 * part + 16 < DP) fetch(ch + 16 * part + 16);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(stage_row + k * 4);
+                of[16 * part + k] += ws == 0.f ? 0.f : x.x * ws;
+                of[16 * part + k + 1] += ws == 0.f ? 0.f : x.y * ws;
+                of[16 * part + k + 2] += ws == 0.f ? 0.f : x.z * ws;
+                of[16 * part + k + 3] += ws == 0.f ? 0.f : x.w * ws;
+              }
+              __syncwarp();
             }
+          }
+          if (wide) {
+            float* out = job.phase == kShared && whole ? job.shared_o : job.part_o;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 4)
+                *reinterpret_cast<float4*>(stage_row + k * 4) =
+                    make_float4(of[16 * part + k], of[16 * part + k + 1], of[16 * part + k + 2],
+                                of[16 * part + k + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (dst[i] >= 0)
+                  *reinterpret_cast<float4*>(out + dst[i] + ch + 16 * part + sub * 4) =
+                      *reinterpret_cast<const float4*>(stage_out + 8 * i * kTcStagePitch);
+              __syncwarp();
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(stage_row + k * 2) =
+                  make_uint4(pack_bf16(of[k], of[k + 1]), pack_bf16(of[k + 2], of[k + 3]),
+                             pack_bf16(of[k + 4], of[k + 5]), pack_bf16(of[k + 6], of[k + 7]));
+            __syncwarp();
+            uint16_t* out = static_cast<uint16_t*>(job.out);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (dst[i] >= 0 && ch + sub * 8 < job.D)
+                *reinterpret_cast<uint4*>(out + dst[i] + ch + sub * 8) =
+                    *reinterpret_cast<const uint4*>(stage_out + 8 * i * kTcStagePitch);
           }
         }
         tc05_fence_before();
-      } else if (left > nb) {
-        load_q(next_head, next_entry);  // this half idles in this tile
-      }
-      if (nb != t.blocks) {
-        if (block == 0) {
-          desc.x = 1;
-          desc.y = head;
-          desc.z = entry;
-        } else {
-          desc.w = block + nb == t.blocks ? kSlotEnd : kSlotMiddle;
-        }
+        t = t_next;
+      } else {
+        t = attn_tile<kTcR, kTcKB>(job, next_entry, lens);  // this half idles in this tile
+        if (left > nb) load_q(next_head, t);
       }
       ent += 2 * nb;
       left -= nb;
@@ -488,12 +707,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       head = next_head;
       entry = next_entry;
     }
-    if (threadIdx.x == 128) job.part_desc[cta] = desc;
+    if (threadIdx.x == 64) job.part_desc[cta] = desc;
   }
   tc05_fence_before();
   __syncthreads();
   tc05_fence_after();
-  if (warp == 1) tc05_dealloc(tmem, kTcTmemCols);
+  if (warp == 1) tc05_dealloc(tmem, Cfg::kTmemCols);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -535,9 +754,9 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, const AttnJob& job, int b
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP>
-cudaError_t launch_tc(AttnJob job, cudaStream_t s, bool* taken) {
-  using Cfg = TcCfg<DP>;
+template <int DP, int H>
+cudaError_t launch_tc(AttnJob job, int rows, cudaStream_t s, bool* taken) {
+  using Cfg = TcCfg<DP, H>;
   const int box = tc_box_rows(job.pd.size);
   CUtensorMap tm_k, tm_v;
   *taken = make_cache_map(&tm_k, job.k, job, box) && make_cache_map(&tm_v, job.v, job, box);
@@ -547,20 +766,23 @@ cudaError_t launch_tc(AttnJob job, cudaStream_t s, bool* taken) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(attn_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_tc_kernel<DP, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Cfg::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  const int rows = job.phase == kShared ? job.B * job.N * job.G : job.N * job.G;
-  job.row_tiles = (rows + kTcR - 1) / kTcR;
+  job.row_tiles = (rows + Cfg::kR - 1) / Cfg::kR;
   job.entries = job.phase == kShared ? job.row_tiles : job.row_tiles * job.B;
-  const int sms = device_sm_count();
-  const int grid = sms < kAttnTcCtas ? sms : kAttnTcCtas;
-  attn_tc_kernel<DP><<<grid, kTcThreads, Cfg::kSmem, s>>>(tm_k, tm_v, job, box);
+  const int most = kAttnTcSlots / Cfg::kR, sms = device_sm_count() * (3 - H);
+  const int grid = sms < most ? sms : most;
+  attn_tc_kernel<DP, H><<<grid, Cfg::kThreads, Cfg::kSmem, s>>>(tm_k, tm_v, job, box);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_attn_combine(job, DP, kTcR, kTcKB, grid, s);
+  return launch_attn_combine(job, DP, Cfg::kR, grid, s);
+}
+
+int64_t tc_rows(const AttnJob& job) {
+  return job.phase == kShared ? (int64_t)job.B * job.N * job.G : (int64_t)job.N * job.G;
 }
 
 }  // namespace
@@ -568,12 +790,15 @@ cudaError_t launch_tc(AttnJob job, cudaStream_t s, bool* taken) {
 // Few rows do not pay for 128-row products, and a box of fewer than 8 rows does not fill a
 // swizzle group.
 bool attn_tc_fits(const AttnJob& job, spec_dtype dtype) {
-  const int64_t rows = job.phase == kShared ? (int64_t)job.B * job.N * job.G : (int64_t)job.N * job.G;
-  return dtype == SPEC_BF16 && job.pd.size % 8 == 0 && job.n_pages > 0 && rows > kAttnRowsTile;
+  return dtype == SPEC_BF16 && job.pd.size % 8 == 0 && job.n_pages > 0 &&
+         tc_rows(job) > kAttnRowsTile;
 }
 
 cudaError_t launch_attn_tc(const AttnJob& job, cudaStream_t s, bool* taken) {
-  return job.D <= 64 ? launch_tc<64>(job, s, taken) : launch_tc<128>(job, s, taken);
+  const int rows = (int)tc_rows(job);
+  if (rows <= kTcHalf)
+    return job.D <= 64 ? launch_tc<64, 1>(job, rows, s, taken) : launch_tc<128, 1>(job, rows, s, taken);
+  return job.D <= 64 ? launch_tc<64, 2>(job, rows, s, taken) : launch_tc<128, 2>(job, rows, s, taken);
 }
 
 }  // namespace svk

@@ -245,6 +245,17 @@ def test_long_context_is_cut_and_joined_reproducibly():
     c.check(a)
 
 
+@pytest.mark.parametrize("B,N,hq,hkv,d", [(1, 70, 4, 1, 128), (3, 40, 2, 1, 128), (2, 33, 8, 2, 64),
+                                          (1, 300, 2, 2, 96)])
+def test_many_blocks_of_many_rows(B, N, hq, hkv, d):
+    """Long runs of key blocks in one tile, rising and falling scores."""
+    c = Case([4000 + 777 * b for b in range(B)], N, hq, hkv, d, 16, seed=N, mask="tree")
+    ramp = torch.linspace(0.1, 2.5, c.k.shape[0])[torch.randperm(c.k.shape[0],
+                                                               generator=torch.Generator().manual_seed(1))]
+    c.k = (c.k.float() * ramp[:, None, None, None]).to(BF)
+    c.check()
+
+
 def test_large_scores_and_flat_rows():
     Case([90, 300], 20, 4, 2, 64, 16, mask="tree", spread=60.0).check()
     Case([90, 300], 20, 4, 2, 64, 16, mask="tree", spread=0.0).check()
