@@ -21,13 +21,8 @@ constexpr int kRowsWarps = 4;    // each takes every fourth group of keys
 constexpr int kRowsThreads = 32 * kRowsWarps;
 constexpr int kGroup = 16;       // keys of a warp's step
 constexpr int kRowsKB = kGroup * kRowsWarps;
+constexpr int kRowsC = 2;        // a tile's fixed costs in blocks
 constexpr int kCombineThreads = 512;
-
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool real) {
-  const int n = real ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "r"(n)
-               : "memory");
-}
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -98,7 +93,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
   const int gr = lane >> 2, tq = lane & 3;  // fragment row, column pair
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may line up
-  const AttnRange range = attn_range<kRowsR, kRowsKB, kRowsThreads>(job, cta, gridDim.x);
+  const AttnRange range = attn_range<kRowsR, kRowsKB, kRowsC, kRowsThreads>(job, cta, gridDim.x);
   if (threadIdx.x == 0) poison = 0;
   int4 desc = make_int4(0, 0, 0, kSlotNone);
   unsigned char* ring = attn_dyn + warp * S * Cfg::kStageBytes;
@@ -106,11 +101,11 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
   float* sq = reinterpret_cast<float*>(attn_dyn + kRowsWarps * S * Cfg::kStageBytes);
   const float c = job.scale_log2;
 
-  int64_t left = range.units;
-  int head = range.head, entry = range.entry, block = range.block;
-  while (left > 0) {
-    const AttnTile t = attn_tile<kRowsR, kRowsKB>(job, entry);
-    const int nb = (int)min((int64_t)(t.blocks - block), left);
+  for (AttnWalk<kRowsC> walk(range); walk.left > 0; walk.next(job)) {
+    const AttnTile t = attn_tile<kRowsR, kRowsKB>(job, walk.entry);
+    const int head = walk.head, entry = walk.entry;
+    walk.take(t.blocks);
+    const int block = walk.first, nb = walk.blocks;
     const int32_t* table_row = job.table + (int64_t)t.b * job.max_pages;
     const T* kh = static_cast<const T*>(job.k) + head * job.head_stride;
     const T* vh = static_cast<const T*>(job.v) + head * job.head_stride;
@@ -436,12 +431,6 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
     }
     __syncthreads();
     if (threadIdx.x == 0) poison = 0;
-    left -= nb;
-    block = 0;
-    if (++entry == job.entries) {
-      entry = 0;
-      ++head;
-    }
     __syncthreads();
   }
   if (threadIdx.x == 0) job.part_desc[cta] = desc;

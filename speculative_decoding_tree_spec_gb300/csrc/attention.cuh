@@ -2,9 +2,9 @@
 //
 // Rows: the query heads that read one key head are taken together, row r = node * G + g of
 // sequence b (G = query heads per key head), in tiles of R rows.  A tile's keys are cut into
-// blocks of KB positions; a tile holds max(1, blocks) units of work, numbered key head by
-// key head and tile by tile.  CTA j of n takes the units [U j / n, U (j + 1) / n): every CTA
-// does the same number of blocks however the lengths differ.  A tile that lies in one CTA is
+// blocks of KB positions; a tile is max(1, blocks) + C units of work, C standing for its fixed
+// costs (queries, epilogue), numbered key head by key head and tile by tile.  CTA j of n takes the units [U j / n, U (j + 1) / n): every CTA
+// does the same amount of work however the lengths differ.  A tile that lies in one CTA is
 // finished there; of a tile cut between CTAs each CTA leaves its part (running maximum, sum,
 // unnormalised output) in one of its two slots and attn_combine_kernel joins the parts in
 // the order of the keys.  The split depends on the lengths and the grid alone, so a call is
@@ -134,22 +134,50 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry) {
   return attn_tile<R, KB>(job, entry, attn_lens(job, entry));
 }
 
-// This CTA's units and where the first one lies: key head, tile, block in it.
+// This CTA's units and where the first one lies: key head, tile, unit in it.
 struct AttnRange {
   int64_t units;
-  int head, entry, block;
+  int head, entry, unit;
+};
+
+// A walk over the units of a CTA, tile by tile.  The blocks of a tile are its first units.
+template <int C>
+struct AttnWalk {
+  int64_t left;
+  int head, entry, unit;  // the next tile to take, and the unit to start at
+  int first, blocks;      // taken: first block and number of blocks
+
+  __device__ __forceinline__ explicit AttnWalk(const AttnRange& r)
+      : left(r.units), head(r.head), entry(r.entry), unit(r.unit), first(0), blocks(0) {}
+  // Takes the units of a tile of `tile_blocks` blocks.
+  __device__ __forceinline__ void take(int tile_blocks) {
+    const int n = (int)min((int64_t)(tile_blocks + C - unit), left);
+    first = min(unit, tile_blocks);
+    blocks = min(unit + n, tile_blocks) - first;
+    left -= n;
+  }
+  __device__ __forceinline__ int next_entry(const AttnJob& job) const {
+    return entry + 1 == job.entries ? 0 : entry + 1;
+  }
+  __device__ __forceinline__ void next(const AttnJob& job) {
+    unit = 0;
+    if (++entry == job.entries) {
+      entry = 0;
+      ++head;
+    }
+  }
 };
 
 // All NT threads of the block call this.  Thread i sums the units of a run of tiles; a scan
 // over the threads gives a key head's units and the run that holds the first one.
-template <int R, int KB, int NT>
+template <int R, int KB, int C, int NT>
 __device__ __forceinline__ AttnRange attn_range(const AttnJob& job, int cta, int ctas) {
   __shared__ int64_t warp_sum[NT / 32];
-  __shared__ int found[2];
+  __shared__ int found[3];
   const int run = (job.entries + NT - 1) / NT;
   const int e0 = (int)threadIdx.x * run, e1 = min(e0 + run, job.entries);
   int64_t mine = 0;
-  for (int e = e0; e < e1; ++e) mine += attn_tile<R, KB>(job, e).blocks;
+  for (int e = e0; e < e1; ++e) mine += attn_tile<R, KB>(job, e).blocks + C;
   int64_t inc = mine;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -172,18 +200,26 @@ __device__ __forceinline__ AttnRange attn_range(const AttnJob& job, int cta, int
   r.head = (int)(u0 / per_head);
   int64_t rest = u0 - r.head * per_head - (before + inc - mine);
   if (rest >= 0 && rest < mine) {
-    int e = e0;
+    int e = e0, n;
     for (;; ++e) {
-      const int n = attn_tile<R, KB>(job, e).blocks;
+      n = attn_tile<R, KB>(job, e).blocks + C;
       if (rest < n) break;
       rest -= n;
     }
-    found[0] = e;
-    found[1] = (int)rest;
+    // a CTA that would start behind the tile's blocks starts with the next tile
+    const bool behind = rest >= n - C;
+    found[0] = behind ? e + 1 : e;
+    found[1] = behind ? 0 : (int)rest;
+    found[2] = behind ? (int)(n - rest) : 0;
   }
   __syncthreads();
   r.entry = found[0];
-  r.block = found[1];
+  r.unit = found[1];
+  if (r.units > 0) r.units -= min((int64_t)found[2], r.units);
+  if (r.entry == job.entries) {
+    r.entry = 0;
+    ++r.head;
+  }
   return r;
 }
 
@@ -207,6 +243,12 @@ __device__ __forceinline__ bool attn_sees_draft(const AttnJob& job, const AttnTi
   const int j = pos - t.prefix;
   if (j >= t.count || n >= t.count) return false;
   return job.mask ? job.mask[((int64_t)t.b * job.N + n) * job.N + j] != 0 : j <= n;
+}
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool real) {
+  const int n = real ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "r"(n)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {

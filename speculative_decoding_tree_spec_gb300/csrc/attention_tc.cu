@@ -33,6 +33,7 @@ namespace svk {
 namespace {
 
 constexpr int kTcHalf = 128, kTcKB = kAttnTcKeys;
+constexpr int kTcC = 4;            // a tile's fixed costs in blocks
 constexpr uint32_t kTcP = 64;      // P's column within a half's scores
 constexpr int kTcStagePitch = 80;  // bytes of a staged row: 64 and a pad against bank conflicts
 constexpr int kTcCheck = 4;        // blocks whose page numbers are checked at once
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
   }
   if (warp == 1) tc05_alloc(&sh.tmem, Cfg::kTmemCols);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may line up
-  const AttnRange range = attn_range<kTcR, kTcKB, Cfg::kThreads>(job, cta, gridDim.x);
+  const AttnRange range = attn_range<kTcR, kTcKB, kTcC, Cfg::kThreads>(job, cta, gridDim.x);
   tc05_fence_before();
   __syncthreads();
   tc05_fence_after();
@@ -129,20 +130,20 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
   const TcWait wait{&sh.abort};
   const int rows_all = job.phase == kShared ? job.B * job.N * job.G : job.N * job.G;
 
-  int64_t left = range.units;
-  int head = range.head, entry = range.entry, block = range.block;
+  AttnWalk<kTcC> walk(range);
   uint32_t ent = 0;  // ring entries so far: key and value blocks in turn
 
-  AttnLens lens = attn_lens(job, entry);  // read a tile ahead from here on
+  AttnLens lens = attn_lens(job, walk.entry);  // read a tile ahead from here on
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     const int boxes = kTcKB / box_rows;
-    while (left > 0) {
-      const AttnTile t = attn_tile<kTcR, kTcKB>(job, entry, lens);
-      lens = attn_lens(job, entry + 1 == job.entries ? 0 : entry + 1);
-      const int nb = (int)min((int64_t)(t.blocks - block), left);
+    for (; walk.left > 0; walk.next(job)) {
+      const AttnTile t = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);
+      lens = attn_lens(job, walk.next_entry(job));
+      walk.take(t.blocks);
+      const int nb = walk.blocks, head = walk.head;
       const int32_t* table_row = job.table + (int64_t)t.b * job.max_pages;
-      const int pos0 = t.kbeg + block * kTcKB + lane * box_rows;  // this lane's box of block 0
+      const int pos0 = t.kbeg + walk.first * kTcKB + lane * box_rows;  // this lane's box of block 0
       auto page_of = [&](int i) {
         const int pos = pos0 + i * kTcKB;
         return lane < boxes && i < nb && pos < t.kend ? table_row[job.pd.div(pos)] : -1;
@@ -173,12 +174,6 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
         issue(&tm_k, page, i);
         issue(&tm_v, page, i);
         page = next;
-      }
-      left -= nb;
-      block = 0;
-      if (++entry == job.entries) {
-        entry = 0;
-        ++head;
       }
     }
     // no copy may still be landing when the CTA exits
@@ -217,10 +212,11 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     };
     // (after a wait that gave up the products run on whatever the buffers hold, within their
     // bounds)
-    while (left > 0) {
-      const AttnTile t = attn_tile<kTcR, kTcKB>(job, entry, lens);
-      lens = attn_lens(job, entry + 1 == job.entries ? 0 : entry + 1);
-      const int nb = uniform((int)min((int64_t)(t.blocks - block), left));
+    for (; walk.left > 0; walk.next(job)) {
+      const AttnTile t = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);
+      lens = attn_lens(job, walk.next_entry(job));
+      walk.take(t.blocks);
+      const int nb = uniform(walk.blocks);
       const int halves = uniform(H == 2 && rows_all - t.row0 > kTcHalf ? 2 : 1);
 #pragma unroll
       for (int w = 0; w < H; ++w)
@@ -270,12 +266,6 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
           }
         }
       }
-      left -= nb;
-      block = 0;
-      if (++entry == job.entries) {
-        entry = 0;
-        ++head;
-      }
     }
     // every product issued has finished before the tensor memory is freed
     if (elect_one()) tc05_commit(&sh.done);
@@ -289,13 +279,12 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     const int tid = (warp & 3) * 32 + lane;  // 0 .. 127: the row within the half
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + w * 256, t_o = t_s + 128;
-    const float c = fabsf(job.scale_log2);
-    const uint32_t flip = job.scale_log2 < 0.f ? 0x80008000u : 0u;  // the maximum wants c >= 0
+    const float c = job.scale_log2;  // >= 0: the maximum is taken before the scaling
     const int boxes = kTcKB / box_rows, box_shift = 31 - __clz(box_rows);
     uint32_t blk = 0, seg = 0;  // blocks and segments of this half so far
 
     // the half's queries into shared memory (K-major, 128-byte swizzle): each warp its 32 rows,
-    // a few rows to a load, all loads in flight
+    // a few rows to a copy; landed_q, later, hands them to the products
     auto load_q = [&](int hd, const AttnTile& t) {
       if (H == 2 && w == 1 && rows_all - t.row0 <= kTcHalf) return;
       int b, node, g;
@@ -305,40 +294,56 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
                                 : (int64_t)-1;
       constexpr int CPR = DP / 8, STEP = 32 / CPR;  // 16-byte units of a row; rows of a step
       const int u = lane % CPR, r0 = lane / CPR;
-      unsigned char* dst = base_p + w * Cfg::kQHalfBytes + (u >> 3) * Cfg::kQChunkBytes;
-      uint4 x[CPR];
-#pragma unroll
+      const uint32_t dst = sq + w * Cfg::kQHalfBytes + (u >> 3) * Cfg::kQChunkBytes;
+#pragma unroll 4
       for (int i = 0; i < CPR; ++i) {
         const int64_t at = __shfl_sync(kFull, mine, r0 + i * STEP);
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (at >= 0 && u * 8 < job.D)
-          x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(job.q) + at + u * 8);
-      }
-#pragma unroll
-      for (int i = 0; i < CPR; ++i) {
         const int r = (warp & 3) * 32 + r0 + i * STEP;
-        x[i].x ^= flip;
-        x[i].y ^= flip;
-        x[i].z ^= flip;
-        x[i].w ^= flip;
-        *reinterpret_cast<uint4*>(dst + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[i];
+        const bool there = at >= 0 && u * 8 < job.D;
+        cp_async16_or_zero(dst + r * 128 + (((u & 7) ^ (r & 7)) << 4),
+                           static_cast<const uint16_t*>(job.q) + (there ? at + u * 8 : 0), there);
       }
+    };
+    auto landed_q = [&](const AttnTile& t) {
+      if (H == 2 && w == 1 && rows_all - t.row0 <= kTcHalf) return;
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[w]);
     };
-    AttnTile t = attn_tile<kTcR, kTcKB>(job, entry, lens);
-    if (left > 0) load_q(head, t);
-    int4 desc = make_int4(0, 0, 0, kSlotNone);
-    while (left > 0) {
-      const int nb = (int)min((int64_t)(t.blocks - block), left);
-      const int halves = H == 2 && rows_all - t.row0 > kTcHalf ? 2 : 1;
-      int next_head = head, next_entry = entry + 1;
-      if (next_entry == job.entries) {
-        next_entry = 0;
-        ++next_head;
+    // a later tile's rows on their way into the L2: queries, mask, the shared positions' result
+    auto prefetch_rows = [&](int hd, int en) {
+      AttnTile t;
+      t.b = job.phase == kShared ? 0 : en / job.row_tiles;
+      t.row0 = (en - t.b * job.row_tiles) * kTcR;
+      int b, node, g;
+      if (!attn_row(job, t, t.row0 + w * kTcHalf + tid, b, node, g)) return;
+      const uint16_t* q = static_cast<const uint16_t*>(job.q) + b * job.lq.batch_stride +
+                          node * job.lq.node_stride + (hd * job.G + g) * job.lq.head_stride;
+      for (int d = 0; d < job.D; d += 64) prefetch_l2(q + d);
+      if (job.phase == kShared) return;
+      if (job.mask) prefetch_l2(job.mask + ((int64_t)b * job.N + node) * job.N);
+      if (job.shared_len > 0) {
+        const float* so = job.shared_o + (((int64_t)hd * job.B + b) * job.by_ng.d +
+                                          t.row0 + w * kTcHalf + tid) * DP;
+#pragma unroll
+        for (int d = 0; d < DP; d += 32) prefetch_l2(so + d);
       }
-      lens = attn_lens(job, next_entry);
+    };
+    AttnTile t = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);
+    if (walk.left > 0) {
+      load_q(walk.head, t);
+      landed_q(t);
+    }
+    int4 desc = make_int4(0, 0, 0, kSlotNone);
+    while (walk.left > 0) {
+      walk.take(t.blocks);
+      const int head = walk.head, entry = walk.entry, block = walk.first, nb = walk.blocks;
+      walk.next(job);
+      const bool more = walk.left > 0;
+      lens = attn_lens(job, walk.entry);
+      if (more) prefetch_rows(walk.head, walk.entry);
+      const int halves = H == 2 && rows_all - t.row0 > kTcHalf ? 2 : 1;
       const int seg0 = t.kbeg + block * kTcKB;
       if (nb != t.blocks) {
         if (block == 0) {
@@ -477,27 +482,33 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
             const uint32_t ev = ent + 2 * i + 1;
             wait(&sh.full[ev % NST], (ev / NST) & 1u);
             constexpr int CPR = DP / 8;
-            const int k0 = max(t.clear - pos0, 0), kn = t.kend - pos0;
+            const int k0 = max(t.clear - pos0, 0), kn = min(t.kend - pos0, kTcKB);
             unsigned char* vb = base_p + Cfg::kQBytes + (ev % NST) * Cfg::kStageBytes;
-            for (int x = k0 * CPR + w * kTcHalf + tid; x < kTcKB * CPR; x += halves * kTcHalf) {
+            auto unit_at = [&](int x) {
               const int key = x / CPR, u = x % CPR;
-              uint4* at = reinterpret_cast<uint4*>(vb + (u >> 3) * Cfg::kChunkBytes + key * 128 +
-                                                   (((u & 7) ^ (key & 7)) << 4));
-              if (key >= kn) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else {
-                const uint4 v = *at;
-                if (unit_nonfinite<uint16_t>(v)) {
-                  uint32_t z[4] = {v.x, v.y, v.z, v.w};
-                  for (int e = 0; e < 4; ++e) {
-                    if ((z[e] & 0x7f800000u) == 0x7f800000u) z[e] &= 0xffffu;
-                    if ((z[e] & 0x7f80u) == 0x7f80u) z[e] &= 0xffff0000u;
+              return reinterpret_cast<uint4*>(vb + (u >> 3) * Cfg::kChunkBytes + key * 128 +
+                                              (((u & 7) ^ (key & 7)) << 4));
+            };
+            const int step = halves * kTcHalf, first = w * kTcHalf + tid;
+            for (int x = k0 * CPR + first; x < kn * CPR; x += 4 * step) {
+              uint4 v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = x + e * step < kn * CPR ? *unit_at(x + e * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (unit_nonfinite<uint16_t>(v[e])) {
+                  uint32_t z[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+                  for (int q = 0; q < 4; ++q) {
+                    if ((z[q] & 0x7f800000u) == 0x7f800000u) z[q] &= 0xffffu;
+                    if ((z[q] & 0x7f80u) == 0x7f80u) z[q] &= 0xffff0000u;
                   }
-                  *at = make_uint4(z[0], z[1], z[2], z[3]);
+                  *unit_at(x + e * step) = make_uint4(z[0], z[1], z[2], z[3]);
                   *((volatile int*)&sh.poison) = 1;
                 }
-              }
             }
+            for (int x = max(kn, 0) * CPR + first; x < kTcKB * CPR; x += step)
+              *unit_at(x) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             asm volatile("bar.sync 2, %0;\n" ::"r"(halves * kTcHalf) : "memory");
           }
@@ -540,8 +551,8 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
           l += sum.x + sum.y;
         }
         // the last scores are read: the half's queries may be replaced
-        const AttnTile t_next = attn_tile<kTcR, kTcKB>(job, next_entry, lens);
-        if (left > nb) load_q(next_head, t_next);
+        const AttnTile t_next = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);
+        if (more) load_q(walk.head, t_next);
 
         // ---- epilogue.  Each thread scales its row; the rows leave through the warp's staging
         // area, four lanes to the 64 bytes of a row, so that a store fills whole sectors. ----
@@ -571,18 +582,20 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
                                (w * 4 + (warp & 3)) * 32 * kTcStagePitch;
         unsigned char* stage_row = stage + lane * kTcStagePitch;
         unsigned char* stage_out = stage + (lane >> 2) * kTcStagePitch + sub * 16;
-        float4 ahead[4];  // the shared positions' result, 16 columns ahead
+        float4 ahead[8];  // the shared positions' result, 32 columns ahead
         auto fetch = [&](int col) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            ahead[i] = src[i] >= 0 ? *reinterpret_cast<const float4*>(job.shared_o + src[i] + col +
-                                                                      sub * 4)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < 8; ++i)
+            ahead[i] = src[i & 3] >= 0
+                           ? *reinterpret_cast<const float4*>(job.shared_o + src[i & 3] + col +
+                                                              (i >> 2) * 16 + sub * 4)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
         };
         if (prior) fetch(0);
         const float s2 = prior && real ? job.shared_lse[shared_row] : -CUDART_INF_F;
         wait(&sh.o_full[w], seg & 1u);
         ++seg;
+        if (more) landed_q(t_next);
         __syncwarp();
         tc05_fence_after();
         if (*((volatile int*)&sh.abort)) l = __int_as_float(0x7fc00000);
@@ -645,22 +658,26 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
 #pragma unroll
           for (int k = 0; k < 32; ++k) of[k] = some ? __uint_as_float(o[k]) * wo : 0.f;
           if (prior) {
+            float4 x[8];
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(stage_out + 8 * i * kTcStagePitch) = ahead[i];
-              if (ch + 16 * part + 16 < DP) fetch(ch + 16 * part + 16);
+                *reinterpret_cast<float4*>(stage_out + 8 * i * kTcStagePitch) = ahead[4 * part + i];
               __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 16; k += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(stage_row + k * 4);
-                of[16 * part + k] += ws == 0.f ? 0.f : x.x * ws;
-                of[16 * part + k + 1] += ws == 0.f ? 0.f : x.y * ws;
-                of[16 * part + k + 2] += ws == 0.f ? 0.f : x.z * ws;
-                of[16 * part + k + 3] += ws == 0.f ? 0.f : x.w * ws;
-              }
+              for (int k = 0; k < 4; ++k)
+                x[4 * part + k] = *reinterpret_cast<const float4*>(stage_row + k * 16);
               __syncwarp();
+            }
+            if (ch + 32 < DP) fetch(ch + 32);
+            const bool joined = ws != 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              of[4 * k] += joined ? x[k].x * ws : 0.f;
+              of[4 * k + 1] += joined ? x[k].y * ws : 0.f;
+              of[4 * k + 2] += joined ? x[k].z * ws : 0.f;
+              of[4 * k + 3] += joined ? x[k].w * ws : 0.f;
             }
           }
           if (wide) {
@@ -698,14 +715,13 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
         tc05_fence_before();
         t = t_next;
       } else {
-        t = attn_tile<kTcR, kTcKB>(job, next_entry, lens);  // this half idles in this tile
-        if (left > nb) load_q(next_head, t);
+        t = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);  // this half idles in this tile
+        if (more) {
+          load_q(walk.head, t);
+          landed_q(t);
+        }
       }
       ent += 2 * nb;
-      left -= nb;
-      block = 0;
-      head = next_head;
-      entry = next_entry;
     }
     if (threadIdx.x == 64) job.part_desc[cta] = desc;
   }
@@ -787,10 +803,10 @@ int64_t tc_rows(const AttnJob& job) {
 
 }  // namespace
 
-// Few rows do not pay for 128-row products, and a box of fewer than 8 rows does not fill a
-// swizzle group.
+// Few rows do not pay for 128-row products, a box of fewer than 8 rows does not fill a swizzle
+// group, and the maximum is taken before the scaling.
 bool attn_tc_fits(const AttnJob& job, spec_dtype dtype) {
-  return dtype == SPEC_BF16 && job.pd.size % 8 == 0 && job.n_pages > 0 &&
+  return dtype == SPEC_BF16 && job.scale_log2 >= 0.f && job.pd.size % 8 == 0 && job.n_pages > 0 &&
          tc_rows(job) > kAttnRowsTile;
 }
 
