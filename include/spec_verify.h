@@ -462,8 +462,8 @@ int spec_tree_attention_paged(const void* q, spec_node_layout q_layout, const vo
  * A path increases strictly (accepted_path[b][k] >= k), as the verify step writes it.  Moves
  *   with a source or destination that has no page are skipped, trees with accept_len < 1
  *   left as they are.
- * The cache, strides and row_bytes must be multiples of 16 bytes.  Asynchronous on `stream`;
- *   allocates nothing.
+ * The cache, strides and row_bytes must be multiples of 16 bytes; n_planes * n_heads *
+ *   row_bytes < 2^34.  Asynchronous on `stream`; allocates nothing.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_MISALIGNED, SPEC_ERR_TOO_LARGE, SPEC_ERR_CUDA.
  */
 int spec_commit_accepted_path_paged(void* cache, int32_t B, int32_t n_planes, int32_t n_heads,

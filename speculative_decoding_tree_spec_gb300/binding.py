@@ -434,37 +434,58 @@ def commit_accepted_path(cache: torch.Tensor, prefix_len: torch.Tensor, accepted
         raise SpecError(rc, "spec_commit_accepted_path")
 
 
-def _int32(t, shape, dev, what):
-    """The address of a contiguous int32 device tensor of this shape (None: NULL)."""
+# The paged-cache calls sit in every layer of a decoding step: their checks keep to a few
+# attribute reads per tensor.
+def _int32(t, shape, dev: int, what):
+    """The address of a contiguous int32 tensor of this shape on device `dev` (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise TypeError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {dev}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or \
+            not t.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on the "
+                        "cache's device")
     return t.data_ptr()
 
 
-def _paged_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PagedLayout:
-    """The layout of [n_pages, page_size, heads, head_dim] caches (any strides, head vectors
-    contiguous; [n_pages, heads, page_size, head_dim] storage comes as a transposed view)."""
-    st = k_cache.stride()
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or st != v_cache.stride() or \
-            k_cache.dtype != v_cache.dtype or k_cache.device != v_cache.device:
+def _paged_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+
+
+def _paged_cache(k_cache: torch.Tensor, v_cache: torch.Tensor):
+    """(layout, dtype, device number) of [n_pages, page_size, heads, head_dim] caches (any
+    strides, head vectors contiguous; [n_pages, heads, page_size, head_dim] storage comes as a
+    transposed view)."""
+    st, shape, dtype, dev = k_cache.stride(), k_cache.shape, k_cache.dtype, k_cache.get_device()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st or \
+            v_cache.dtype is not dtype or v_cache.get_device() != dev:
         raise ValueError("k_cache and v_cache must be 4-d and share shape, strides and dtype")
-    if st[3] != 1 and k_cache.shape[3] > 1:
+    if st[3] != 1 and shape[3] > 1:
         raise ValueError("head vectors must be contiguous")
-    n_pages, page_size, heads, dim = k_cache.shape
-    return PagedLayout(n_pages, page_size, heads, dim, st[0], st[1], st[2])
+    if dev < 0:
+        raise ValueError("the caches must be on a CUDA device")
+    return PagedLayout(*shape, st[0], st[1], st[2]), dtype, dev
 
 
-def _nodes(t: torch.Tensor, like: torch.Tensor, B: int, N: int, dim: int, what: str) -> NodeLayout:
-    st = t.stride()
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N or t.shape[3] != dim or \
+def _nodes(t: torch.Tensor, dtype, dev: int, B: int, N: int, dim: int, what: str):
+    """(layout, heads) of a [B, N, heads, dim] array."""
+    st, shape = t.stride(), t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != N or shape[3] != dim or \
             (st[3] != 1 and dim > 1):
         raise ValueError(f"{what} must be [B, N, heads, head_dim] = [{B}, {N}, heads, {dim}] with "
                          "contiguous head vectors")
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype is not dtype or t.get_device() != dev:
         raise TypeError(f"{what} must share the cache's dtype and device")
-    return NodeLayout(st[0], st[1], st[2])
+    return NodeLayout(st[0], st[1], st[2]), shape[2]
+
+
+_PAGED_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
+
+
+def _paged_dtype(dtype) -> int:
+    code = _PAGED_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"paged caches must be float32 or bfloat16, got {dtype}")
+    return code
 
 
 def paged_append_rope(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -478,40 +499,44 @@ def paged_append_rope(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
     rot_dim] float32: the cosines, then the sines (None: no rotation).  counts [B] int32:
     tokens n >= counts[b] are padding.  Returns the rotated queries (out_q, or a new tensor;
     None if q is None)."""
-    cache = _paged_cache(k_cache, v_cache)
+    cache, dtype, dev = _paged_cache(k_cache, v_cache)
     B, N = k.shape[:2]
-    D, dev = cache.head_dim, k_cache.device
-    lk, lv = _nodes(k, k_cache, B, N, D, "k"), _nodes(v, k_cache, B, N, D, "v")
-    if k.shape[2] != cache.n_kv_heads or v.shape[2] != cache.n_kv_heads:
+    D = cache.head_dim
+    lk, hk = _nodes(k, dtype, dev, B, N, D, "k")
+    lv, hv = _nodes(v, dtype, dev, B, N, D, "v")
+    if hk != cache.n_kv_heads or hv != hk:
         raise ValueError("k and v must have the cache's heads")
     if q is not None:
-        lq = _nodes(q, k_cache, B, N, D, "q")
+        lq, hq = _nodes(q, dtype, dev, B, N, D, "q")
         if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif out_q.shape != q.shape:
-            raise ValueError("out_q must have the shape of q")
-        lo = _nodes(out_q, k_cache, B, N, D, "out_q")
+            out_q = torch.empty(q.shape, dtype=dtype, device=q.device)
+            lo = NodeLayout(N * hq * D, hq * D, D)
+        else:
+            lo, ho = _nodes(out_q, dtype, dev, B, N, D, "out_q")
+            if ho != hq:
+                raise ValueError("out_q must have the shape of q")
+        q_ptr, out_ptr = q.data_ptr(), out_q.data_ptr()
     else:
         lq = lo = NodeLayout(0, 0, 0)
+        hq, q_ptr, out_ptr, out_q = 0, None, None, None
     n_positions = rot = 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or \
-                cos_sin.device != dev:
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or \
+                not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
             raise TypeError("cos_sin must be a contiguous float32 [n_positions, rot_dim] tensor")
         n_positions, rot = cos_sin.shape
     max_pages = page_table.shape[-1]
-    rc = lib().spec_paged_append_rope(
-        None if q is None else q.data_ptr(), lq, None if q is None else out_q.data_ptr(), lo,
-        k.data_ptr(), lk, v.data_ptr(), lv, _dtype_code(k_cache), B, N,
-        0 if q is None else q.shape[2], k_cache.data_ptr(), v_cache.data_ptr(), cache,
+    rc = (_lib or lib()).spec_paged_append_rope(
+        q_ptr, lq, out_ptr, lo, k.data_ptr(), lk, v.data_ptr(), lv, _paged_dtype(dtype), B, N, hq,
+        k_cache.data_ptr(), v_cache.data_ptr(), cache,
         _int32(page_table, (B, max_pages), dev, "page_table"), max_pages,
         _int32(prefix_len, (B,), dev, "prefix_len"), _int32(counts, (B,), dev, "counts"),
         _int32(position_ids, (B, N), dev, "position_ids"),
         None if cos_sin is None else cos_sin.data_ptr(), n_positions, rot,
-        SPEC_ROPE_INTERLEAVED if interleaved else 0, _stream_ptr(stream))
+        SPEC_ROPE_INTERLEAVED if interleaved else 0, _paged_stream(stream, dev))
     if rc != 0:
         raise SpecError(rc, "spec_paged_append_rope")
-    return out_q if q is not None else None
+    return out_q
 
 
 def tree_attention_workspace_size(B: int, N: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
@@ -531,37 +556,40 @@ def tree_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     gives it; None: j <= n, which is decoding at N = 1 and a prompt otherwise).  scale defaults
     to head_dim ** -0.5.  shared_len: positions that all sequences share, read once.  Returns
     {"out": [B, N, heads, head_dim], "lse": [B, N, heads] float32 natural logarithm}."""
-    cache = _paged_cache(k_cache, v_cache)
+    cache, dtype, dev = _paged_cache(k_cache, v_cache)
     B, N, H, D = q.shape
-    dev = k_cache.device
     if D != cache.head_dim:
         raise ValueError("q and the caches must share head_dim")
-    lq = _nodes(q, k_cache, B, N, D, "q")
+    lq = _nodes(q, dtype, dev, B, N, D, "q")[0]
+    device = q.device
     if out is None:
-        out = torch.empty((B, N, H, D), dtype=q.dtype, device=dev)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    lo = _nodes(out, k_cache, B, N, D, "out")
+        out = torch.empty((B, N, H, D), dtype=dtype, device=device)
+        lo = NodeLayout(N * H * D, H * D, D)
+    else:
+        lo, ho = _nodes(out, dtype, dev, B, N, D, "out")
+        if ho != H:
+            raise ValueError("out must have the shape of q")
     if lse is None:
-        lse = torch.empty((B, N, H), dtype=torch.float32, device=dev)
-    elif lse.shape != (B, N, H) or lse.dtype != torch.float32 or not lse.is_contiguous() or \
-            lse.device != dev:
+        lse = torch.empty((B, N, H), dtype=torch.float32, device=device)
+    elif lse.shape != (B, N, H) or lse.dtype is not torch.float32 or not lse.is_contiguous() or \
+            lse.get_device() != dev:
         raise TypeError("lse must be a contiguous float32 [B, N, heads] tensor")
-    if mask is not None and (mask.dtype not in (torch.uint8, torch.bool) or mask.device != dev or
-                             mask.shape != (B, N, N) or not mask.is_contiguous()):
+    if mask is not None and (mask.dtype not in (torch.uint8, torch.bool) or
+                             mask.shape != (B, N, N) or mask.get_device() != dev or
+                             not mask.is_contiguous()):
         raise TypeError("mask must be a contiguous uint8 or bool [B, N, N] tensor")
-    dt = _dtype_code(k_cache)
+    L, dt = _lib or lib(), _paged_dtype(dtype)
     if workspace is None:
-        ws = lib().spec_tree_attention_workspace_size(B, N, H, cache.n_kv_heads, D, shared_len, dt)
-        workspace = torch.empty(max(int(ws), 256), dtype=torch.uint8, device=dev)
+        ws = L.spec_tree_attention_workspace_size(B, N, H, cache.n_kv_heads, D, shared_len, dt)
+        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=device)
     max_pages = page_table.shape[-1]
-    rc = lib().spec_tree_attention_paged(
+    rc = L.spec_tree_attention_paged(
         q.data_ptr(), lq, k_cache.data_ptr(), v_cache.data_ptr(), cache, dt, B, N, H,
         _int32(page_table, (B, max_pages), dev, "page_table"), max_pages,
         _int32(prefix_len, (B,), dev, "prefix_len"), _int32(counts, (B,), dev, "counts"),
         None if mask is None else mask.data_ptr(), int(shared_len),
-        D ** -0.5 if scale is None else float(scale), out.data_ptr(), lo, lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+        D ** -0.5 if scale is None else scale, out.data_ptr(), lo, lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _paged_stream(stream, dev))
     if rc != 0:
         raise SpecError(rc, "spec_tree_attention_paged")
     return {"out": out, "lse": lse}
@@ -573,23 +601,25 @@ def commit_accepted_path_paged(cache: torch.Tensor, page_table: torch.Tensor,
     """spec_commit_accepted_path_paged on a device cache [planes, n_pages, page_size, heads,
     head_dim] (or [planes, n_pages, page_size, row]; any dtype and strides, head vectors
     contiguous), in place: planes are a layer's keys or values."""
-    if cache.dim() == 4:
-        cache = cache.unsqueeze(3)
-    if cache.dim() != 5 or (cache.stride(4) != 1 and cache.shape[4] > 1):
+    shape, st, es, dev = cache.shape, cache.stride(), cache.element_size(), cache.get_device()
+    if len(shape) == 4:
+        shape, st = (*shape[:3], 1, shape[3]), (*st[:3], shape[3], st[3])
+    if len(shape) != 5 or (st[4] != 1 and shape[4] > 1):
         raise ValueError("cache must be [planes, n_pages, page_size, heads, head_dim] with "
                          "contiguous head vectors")
-    P, n_pages, page_size, H, D = cache.shape
-    st, es = cache.stride(), cache.element_size()
+    if dev < 0:
+        raise ValueError("the cache must be on a CUDA device")
+    P, n_pages, page_size, H, D = shape
     if st[3] == D:  # heads side by side: one wider row
         H, D = 1, H * D
     B, W = accepted_path.shape
-    dev, max_pages = cache.device, page_table.shape[-1]
-    rc = lib().spec_commit_accepted_path_paged(
+    max_pages = page_table.shape[-1]
+    rc = (_lib or lib()).spec_commit_accepted_path_paged(
         cache.data_ptr(), B, P, H, n_pages, page_size, st[0] * es, st[1] * es, st[2] * es,
         0 if H == 1 else st[3] * es, D * es, _int32(page_table, (B, max_pages), dev, "page_table"),
         max_pages, _int32(prefix_len, (B,), dev, "prefix_len"),
         _int32(accepted_path, (B, W), dev, "accepted_path"),
-        _int32(accept_len, (B,), dev, "accept_len"), W, _stream_ptr(stream))
+        _int32(accept_len, (B,), dev, "accept_len"), W, _paged_stream(stream, dev))
     if rc != 0:
         raise SpecError(rc, "spec_commit_accepted_path_paged")
 

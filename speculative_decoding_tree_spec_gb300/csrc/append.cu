@@ -18,6 +18,7 @@ namespace svk {
 namespace {
 
 constexpr int kAppendThreads = 128;
+constexpr int kAppendBatch = 3;  // heads whose loads a thread has in flight
 
 struct AppendJob {
   const unsigned char *q, *k, *v;
@@ -114,29 +115,41 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendJob job) {
     xa = pack_unit<T>(a);
     xb = pack_unit<T>(c);
   };
+  // Heads in batches: the loads of a batch stand before its first store.
   const int total = job.Hq + 2 * job.Hkv;
-  for (int h = lane_head; h < total; h += heads_step) {
-    const unsigned char* src;
-    unsigned char* dst;
-    const bool is_q = h < job.Hq, is_v = h >= job.Hq + job.Hkv;
-    if (is_q) {
-      src = job.q + b * job.lq.batch_stride + n * job.lq.node_stride + h * job.lq.head_stride;
-      dst = job.out_q + b * job.lo.batch_stride + n * job.lo.node_stride + h * job.lo.head_stride;
-    } else {
-      const int g = h - job.Hq - (is_v ? job.Hkv : 0);
-      const spec_node_layout& l = is_v ? job.lv : job.lk;
-      src = (is_v ? job.v : job.k) + b * l.batch_stride + n * l.node_stride + g * l.head_stride;
-      dst = (is_v ? job.vc : job.kc) + slot + g * job.head_stride;
-      if (slot < 0) continue;
+  for (int h0 = lane_head; h0 < total; h0 += kAppendBatch * heads_step) {
+    uint4 xa[kAppendBatch], xb[kAppendBatch];
+    unsigned char* dst[kAppendBatch];
+#pragma unroll
+    for (int i = 0; i < kAppendBatch; ++i) {
+      const int h = h0 + i * heads_step;
+      dst[i] = nullptr;
+      xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
+      if (h >= total) continue;
+      const unsigned char* src;
+      if (h < job.Hq) {
+        src = job.q + b * job.lq.batch_stride + n * job.lq.node_stride + h * job.lq.head_stride;
+        dst[i] = job.out_q + b * job.lo.batch_stride + n * job.lo.node_stride +
+                 h * job.lo.head_stride;
+      } else {
+        const bool is_v = h >= job.Hq + job.Hkv;
+        const int g = h - job.Hq - (is_v ? job.Hkv : 0);
+        const spec_node_layout& l = is_v ? job.lv : job.lk;
+        src = (is_v ? job.v : job.k) + b * l.batch_stride + n * l.node_stride + g * l.head_stride;
+        if (slot >= 0) dst[i] = (is_v ? job.vc : job.kc) + slot + g * job.head_stride;
+      }
+      if (real && dst[i]) {
+        xa[i] = *reinterpret_cast<const uint4*>(src + ua * 16);
+        if (has_b) xb[i] = *reinterpret_cast<const uint4*>(src + ub * 16);
+      }
     }
-    uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
-    if (real) {
-      xa = *reinterpret_cast<const uint4*>(src + ua * 16);
-      if (has_b) xb = *reinterpret_cast<const uint4*>(src + ub * 16);
-      if (turn && !is_v) rotate(xa, xb);
+#pragma unroll
+    for (int i = 0; i < kAppendBatch; ++i) {
+      if (!dst[i]) continue;
+      if (real && turn && h0 + i * heads_step < job.Hq + job.Hkv) rotate(xa[i], xb[i]);
+      *reinterpret_cast<uint4*>(dst[i] + ua * 16) = xa[i];
+      if (has_b) *reinterpret_cast<uint4*>(dst[i] + ub * 16) = xb[i];
     }
-    *reinterpret_cast<uint4*>(dst + ua * 16) = xa;
-    if (has_b) *reinterpret_cast<uint4*>(dst + ub * 16) = xb;
   }
 }
 

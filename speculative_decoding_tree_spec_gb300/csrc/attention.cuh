@@ -29,18 +29,6 @@ constexpr int kAttnRowsTile = 16;  // rows of the few-rows kernel's tile
 
 enum AttnPhase { kOwn = 0, kShared = 1 };
 
-// x / d by a multiplication: the high half of x * ceil(2^64 / d) is exact for x below 2^32.
-struct FastDiv {
-  uint64_t magic;
-  int d;
-  __host__ static FastDiv make(int d) {
-    return FastDiv{d > 1 ? ~0ull / (uint64_t)d + 1u : 0u, d};
-  }
-  __device__ __forceinline__ int div(int x) const {
-    return d == 1 ? x : (int)__umul64hi((uint64_t)(uint32_t)x, magic);
-  }
-};
-
 struct AttnJob {  // (the kernels' argument)
   const void *q, *k, *v;
   void* out;

@@ -73,9 +73,11 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitJob job) {
 // and a row may be split over heads that lie apart.
 struct PagedCommitJob {
   unsigned char* cache;
-  int B, n_planes, n_heads, n_pages, max_pages, W;
+  int n_pages, max_pages, W;
+  int items;              // 16-byte columns of a tree: planes * heads * columns of a row
+  int blocks_per_tree;
+  FastDiv by_vec, by_head;
   int64_t plane_stride, page_stride, pos_stride, head_stride;  // bytes
-  int64_t row_bytes;                                           // multiple of 16
   PageDiv pd;
   const int32_t* table;
   const int32_t* prefix_len;
@@ -83,45 +85,39 @@ struct PagedCommitJob {
   const int32_t* accept_len;
 };
 
-// One thread per (plane, tree, head, 16-byte column) item, grid-stride, moves in batches
-// as above: all addresses of a batch, then all loads, then all stores.
-__global__ void __launch_bounds__(kCommitThreads) paged_commit_kernel(PagedCommitJob job) {
-  const int64_t nvec = job.row_bytes / 16, per_tree = nvec * job.n_heads;
-  const int64_t total = (int64_t)job.B * job.n_planes * per_tree;
-  for (int64_t item = (int64_t)blockIdx.x * kCommitThreads + threadIdx.x; item < total;
-       item += (int64_t)gridDim.x * kCommitThreads) {
-    const int64_t pair = item / per_tree, in_tree = item - pair * per_tree;
-    const int64_t head = in_tree / nvec, v = in_tree - head * nvec;
-    const int b = (int)(pair % job.B);
-    const int64_t plane = pair / job.B;
-    const int a = min(job.accept_len[b], job.W - 1);
-    if (a <= 0) continue;
-    const int base = job.prefix_len[b];
-    const int32_t* path = job.path + (int64_t)b * job.W;
-    const int32_t* row = job.table + (int64_t)b * job.max_pages;
-    unsigned char* col = job.cache + plane * job.plane_stride + head * job.head_stride + v * 16;
-    auto at = [&](int node) {  // node 0 is at `base`; overflowing sums have no page
-      const int64_t t = (int64_t)base + node;
-      return t >= 0 && t <= 0x7fffffff
-                 ? paged_offset(row, job.max_pages, job.n_pages, job.pd, job.page_stride,
-                                job.pos_stride, (int)t)
-                 : (int64_t)-1;
-    };
-    for (int k0 = 1; k0 <= a; k0 += kBatchMoves) {
+// A block takes one tree and some of its columns (every blocks_per_tree-th run of 256).  Its
+// first threads find the rows of up to kBatchMoves moves through the page table, once for all
+// columns; each thread then loads a column of every one of them before it stores any, so a
+// column's moves cost one latency.  What bounds it: the chain path -> page table -> row ->
+// store, about 2 us, until the rows themselves take longer.  Looking the rows up in every
+// thread (94 registers, a quarter of the threads resident) took 23.3 us instead of the time
+// in the design notes' table on 64 planes x 64 trees.
+__global__ void __launch_bounds__(kCommitThreads, 4) paged_commit_kernel(PagedCommitJob job) {
+  __shared__ int64_t src[kBatchMoves], dst[kBatchMoves];
+  const int b = blockIdx.x / job.blocks_per_tree, part = blockIdx.x % job.blocks_per_tree;
+  const int a = min(job.accept_len[b], job.W - 1);
+  const int64_t base = job.prefix_len[b];
+  const int32_t* path = job.path + (int64_t)b * job.W;
+  for (int k0 = 1; k0 <= a; k0 += kBatchMoves) {
+    if (threadIdx.x < 2 * kBatchMoves) {
+      const int i = threadIdx.x % kBatchMoves, k = k0 + i;
+      const int node = k < job.W ? path[k] : 0;  // (read beside accept_len, not after it)
+      const bool to = threadIdx.x >= kBatchMoves;
+      const int64_t t = base + (to ? k : node);
+      int64_t at = -1;
+      if (k <= a && node != k && t >= 0 && t <= SPEC_MAX_POSITIONS)
+        at = paged_offset(job.table + (int64_t)b * job.max_pages, job.max_pages, job.n_pages,
+                          job.pd, job.page_stride, job.pos_stride, (int)t);
+      (to ? dst : src)[i] = at;
+    }
+    __syncthreads();
+    for (int item = part * kCommitThreads + threadIdx.x; item < job.items;
+         item += job.blocks_per_tree * kCommitThreads) {
+      const int row = job.by_vec.div(item), plane = job.by_head.div(row);
+      unsigned char* col = job.cache + plane * job.plane_stride +
+                           (row - plane * job.by_head.d) * job.head_stride +
+                           (int64_t)(item - row * job.by_vec.d) * 16;
       uint4 x[kBatchMoves];
-      int64_t src[kBatchMoves], dst[kBatchMoves];
-#pragma unroll
-      for (int i = 0; i < kBatchMoves; ++i) {
-        const int k = k0 + i;
-        src[i] = dst[i] = -1;
-        if (k <= a) {
-          const int node = path[k];
-          if (node != k) {
-            src[i] = at(node);
-            dst[i] = at(k);
-          }
-        }
-      }
 #pragma unroll
       for (int i = 0; i < kBatchMoves; ++i)
         if (src[i] >= 0 && dst[i] >= 0) x[i] = *reinterpret_cast<const uint4*>(col + src[i]);
@@ -129,6 +125,7 @@ __global__ void __launch_bounds__(kCommitThreads) paged_commit_kernel(PagedCommi
       for (int i = 0; i < kBatchMoves; ++i)
         if (src[i] >= 0 && dst[i] >= 0) *reinterpret_cast<uint4*>(col + dst[i]) = x[i];
     }
+    __syncthreads();
   }
 }
 
@@ -156,30 +153,33 @@ extern "C" int spec_commit_accepted_path_paged(
       ((plane_stride | page_stride | pos_stride | head_stride | row_bytes) & 15))
     return SPEC_ERR_MISALIGNED;
   if (row_bytes > pos_stride && page_size > 1) return SPEC_ERR_INVALID_ARG;  // rows may not overlap
-  const int64_t pairs = (int64_t)B * n_planes;
-  if (pairs > 0x7fffffff) return SPEC_ERR_TOO_LARGE;
+  const int64_t nvec = row_bytes / 16;
+  if ((int64_t)n_planes * n_heads > 0x3fffffff || nvec > 0x3fffffff ||
+      (int64_t)n_planes * n_heads * nvec > 0x3fffffff)
+    return SPEC_ERR_TOO_LARGE;
   PagedCommitJob job{};
   job.cache = static_cast<unsigned char*>(cache);
-  job.B = B;
-  job.n_planes = n_planes;
-  job.n_heads = n_heads;
   job.n_pages = n_pages;
   job.max_pages = max_pages;
   job.W = W;
+  job.items = (int)(n_planes * n_heads * nvec);
+  job.by_vec = FastDiv::make((int)nvec);
+  job.by_head = FastDiv::make(n_heads);
   job.plane_stride = plane_stride;
   job.page_stride = page_stride;
   job.pos_stride = pos_stride;
   job.head_stride = head_stride;
-  job.row_bytes = row_bytes;
   job.pd = PageDiv::make(page_size);
   job.table = page_table;
   job.prefix_len = prefix_len;
   job.path = accepted_path;
   job.accept_len = accept_len;
-  const int64_t items = pairs * n_heads * (row_bytes / 16);
-  int64_t blocks = (items + kCommitThreads - 1) / kCommitThreads;
-  const int64_t cap = (int64_t)device_sm_count() * 16;  // grid-stride beyond this
-  if (blocks > cap) blocks = cap;
+  // enough blocks to fill the GPU twice over, and no more than there are columns
+  const int runs = (job.items + kCommitThreads - 1) / kCommitThreads;
+  const int wanted = (device_sm_count() * 16 + B - 1) / B;
+  job.blocks_per_tree = runs < wanted ? runs : wanted;
+  const int64_t blocks = (int64_t)B * job.blocks_per_tree;
+  if (blocks > 0x7fffffff) return SPEC_ERR_TOO_LARGE;
   paged_commit_kernel<<<(unsigned)blocks, kCommitThreads, 0,
                         reinterpret_cast<cudaStream_t>(stream)>>>(job);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

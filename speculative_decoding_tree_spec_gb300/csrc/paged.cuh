@@ -11,6 +11,18 @@
 
 namespace svk {
 
+// x / d by a multiplication: the high half of x * ceil(2^64 / d) is exact for x below 2^32.
+struct FastDiv {
+  uint64_t magic;
+  int d;
+  __host__ static FastDiv make(int d) {
+    return FastDiv{d > 1 ? ~0ull / (uint64_t)d + 1u : 0u, d};
+  }
+  __device__ __forceinline__ int div(int x) const {
+    return d == 1 ? x : (int)__umul64hi((uint64_t)(uint32_t)x, magic);
+  }
+};
+
 // t / page_size and t % page_size; `shift` >= 0 for a power of two.
 struct PageDiv {
   int32_t size, shift;

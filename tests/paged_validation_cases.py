@@ -99,7 +99,7 @@ COMMIT = [
     (dict(head_stride=8), -3),
     (dict(row_bytes=128, pos_stride=64), -1),
     (dict(max_pages=1 << 30), -6),
-    (dict(B=1 << 20, n_planes=1 << 12), -6),
+    (dict(n_planes=1 << 20, n_heads=1 << 12), -6),
 ]
 
 
