@@ -22,6 +22,8 @@ constexpr int kRowsThreads = 32 * kRowsWarps;
 constexpr int kGroup = 16;       // keys of a warp's step
 constexpr int kRowsKB = kGroup * kRowsWarps;
 constexpr int kRowsC = 2;        // a tile's fixed costs in blocks
+constexpr int kMaxSplit = 8;     // CTAs of a cluster that share a tile
+constexpr int kSplitBlocks = 8;  // blocks of a tile that a CTA of a cluster takes at most
 constexpr int kCombineThreads = 512;
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -71,6 +73,11 @@ __device__ __forceinline__ void split_tf32_inf(float x, uint32_t& hi, uint32_t& 
 // instructions: at 16 rows the keys' bytes, not the products, set the time.  fp32 inputs are
 // split into two tf32 parts each.
 // ---------------------------------------------------------------------------------------
+//
+// Two ways to cut the work.  SPLIT = false: the work list of attention.cuh, even whatever the
+// lengths are, with the join in a second kernel.  SPLIT = true, for few or short tiles (see
+// launch_rows): a cluster of CTAs takes one tile, each an equal run of its blocks, and joins
+// the parts through distributed shared memory: no work list, no second launch.
 template <typename T, int DP>
 struct RowsCfg {
   static constexpr int kRowBytes = DP * (int)sizeof(T);
@@ -82,7 +89,52 @@ struct RowsCfg {
   static constexpr int kCtasPerSm = kSmem > 110 * 1024 ? 1 : 2;
 };
 
-template <typename T, int DP>
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
+                   : "memory");
+}
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  uint32_t a;
+  float x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
+  uint32_t a;
+  float4 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+
+// Joins (ms, ls, x) to (m, l, o).
+template <int C>
+__device__ __forceinline__ void join_part(float& m, float& l, float (&o)[C], float ms, float ls,
+                                          const float (&x)[C]) {
+  if (ms == -CUDART_INF_F && ls == 0.f) return;  // sees none of these keys (NaN goes on)
+  const float mn = fmaxf(m, ms);
+  const float a = m == -CUDART_INF_F ? 0.f : exp2f(m - mn), b = exp2f(ms - mn);
+  l = l * a + ls * b;
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = o[i] * a + x[i] * b;
+  m = mn;
+}
+
+template <typename T, int DP, bool SPLIT>
 __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
   using Cfg = RowsCfg<T, DP>;
   constexpr bool F32 = sizeof(T) == 4;
@@ -92,9 +144,18 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, tq = lane & 3;  // fragment row, column pair
   const int cta = blockIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may line up
-  const AttnRange range = attn_range<kRowsR, kRowsKB, kRowsC, kRowsThreads>(job, cta, gridDim.x);
+  AttnRange range{0, 0, 0, 0};
+  if (!SPLIT) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may line up
+    range = attn_range<kRowsR, kRowsKB, kRowsC, kRowsThreads>(job, cta, gridDim.x);
+  } else {
+    const int tile = cta / (int)cluster_size();
+    range.units = 1;  // one walk
+    range.head = tile / job.entries;
+    range.entry = tile - range.head * job.entries;
+  }
   if (threadIdx.x == 0) poison = 0;
+  __syncthreads();
   int4 desc = make_int4(0, 0, 0, kSlotNone);
   unsigned char* ring = attn_dyn + warp * S * Cfg::kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
@@ -104,8 +165,17 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
   for (AttnWalk<kRowsC> walk(range); walk.left > 0; walk.next(job)) {
     const AttnTile t = attn_tile<kRowsR, kRowsKB>(job, walk.entry);
     const int head = walk.head, entry = walk.entry;
-    walk.take(t.blocks);
-    const int block = walk.first, nb = walk.blocks;
+    int block, nb;
+    if (SPLIT) {
+      const int rank = (int)cluster_rank(), size = (int)cluster_size();
+      block = t.blocks * rank / size;
+      nb = t.blocks * (rank + 1) / size - block;
+      walk.left = 0;
+    } else {
+      walk.take(t.blocks);
+      block = walk.first;
+      nb = walk.blocks;
+    }
     const int32_t* table_row = job.table + (int64_t)t.b * job.max_pages;
     const T* kh = static_cast<const T*>(job.k) + head * job.head_stride;
     const T* vh = static_cast<const T*>(job.v) + head * job.head_stride;
@@ -151,18 +221,26 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
 
     // ---- this warp's groups: keys seg0 + 16 (4 i + warp) .. + 15 ----
     const int groups = nb;
-    int64_t off_next = -1;  // lane l < 16: offset of key l of the next group to be issued
+    // The page of this lane's key (lane < 16) of the next group to be issued, read a group
+    // ahead and not looked at before: the read's latency hides behind the group between.
+    int page_next = -1, slot_next = 0;
     auto lookup = [&](int i) {
       const int pos = seg0 + (i * kRowsWarps + warp) * kGroup + lane;
-      off_next = (i < groups && lane < kGroup && pos < seg1)
-                     ? paged_offset(table_row, job.max_pages, job.n_pages, job.pd,
-                                    job.page_stride, job.pos_stride, pos)
-                     : (int64_t)-1;
+      page_next = -1;
+      if (i < groups && lane < kGroup && pos < seg1) {
+        const int at = job.pd.div(pos);  // below max_pages: seg1 lies within the table
+        page_next = table_row[at];
+        slot_next = pos - at * job.pd.size;
+      }
     };
     unsigned ok_ring[S];  // per stage: keys that exist
     auto issue = [&](int i, int stage) {
       const uint32_t dst = ring_u + stage * Cfg::kStageBytes;
-      const unsigned ok = __ballot_sync(kFull, off_next >= 0);
+      const bool exists = (unsigned)page_next < (unsigned)job.n_pages;
+      const unsigned ok = __ballot_sync(kFull, exists);
+      const int64_t off_mine = exists ? (int64_t)page_next * job.page_stride +
+                                            (int64_t)slot_next * job.pos_stride
+                                      : (int64_t)-1;
 #pragma unroll
       for (int s = 0; s < S; ++s)
         if (s == stage) ok_ring[s] = ok;
@@ -172,7 +250,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
 #pragma unroll
         for (int rr = 0; rr < kGroup; rr += rows_step) {
           const int r = rr + r0;
-          const int64_t off = __shfl_sync(kFull, off_next, r);
+          const int64_t off = __shfl_sync(kFull, off_mine, r);
 #pragma unroll
           for (int cc = 0; cc < CH; cc += 32) {
             const int ch = ch0 + cc;
@@ -409,6 +487,34 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
       if (attn_row(job, t, t.row0 + r, b, n, g))
         add_nonfinite<T, C>(job, t, head, n, max(t.clear, seg0), seg1, c0, ot);
     }
+    if (SPLIT) {
+      // the part of this CTA, then some columns of all of the cluster's parts
+      float* po = sm + 2 * kRowsWarps * kRowsR;  // [16][OP], then [16] m and l
+      float* pm = po + kRowsR * OP;
+      if (c0 == 0) {
+        pm[r] = mt;
+        pm[kRowsR + r] = lt;
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) po[r * OP + c0 + i] = ot[i];
+      cluster_barrier();
+      const int rank = (int)cluster_rank(), size = (int)cluster_size();
+      constexpr int UNITS = kRowsR * DP / 8;
+      for (int u = UNITS / size * rank + threadIdx.x; u < UNITS / size * (rank + 1);
+           u += kRowsThreads) {
+        const int ur = u / (DP / 8), uc = (u % (DP / 8)) * 8;
+        float m8 = -CUDART_INF_F, l8 = 0.f, o8[8] = {};
+#pragma unroll 4
+        for (int p = 0; p < size; ++p) {
+          const float4 a = ld_cluster4(po + ur * OP + uc, p), b = ld_cluster4(po + ur * OP + uc + 4, p);
+          const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          join_part<8>(m8, l8, o8, ld_cluster(pm + ur, p), ld_cluster(pm + kRowsR + ur, p), x);
+        }
+        write_row<T, 8>(job, t, head, t.row0 + ur, uc, DP, m8, l8, o8);
+      }
+      cluster_barrier();  // the peers have read this CTA's part
+      return;
+    }
     if (nb == t.blocks) {
       write_row<T, C>(job, t, head, t.row0 + r, c0, DP, mt, lt, ot);
     } else {
@@ -443,19 +549,6 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
 // every CTA: with GROUPS > 1 the parts are dealt to that many groups of threads, each joining
 // its own in the order of the keys, and the groups are joined through shared memory.
 // ---------------------------------------------------------------------------------------
-
-// Joins (ms, ls, x) to (m, l, o).
-template <int C>
-__device__ __forceinline__ void join_part(float& m, float& l, float (&o)[C], float ms, float ls,
-                                          const float (&x)[C]) {
-  if (ms == -CUDART_INF_F && ls == 0.f) return;  // sees none of these keys (NaN goes on)
-  const float mn = fmaxf(m, ms);
-  const float a = m == -CUDART_INF_F ? 0.f : exp2f(m - mn), b = exp2f(ms - mn);
-  l = l * a + ls * b;
-#pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = o[i] * a + x[i] * b;
-  m = mn;
-}
 
 template <int DP, int R>
 struct CombineCfg {
@@ -549,6 +642,12 @@ cudaError_t launch_combine(const AttnJob& job, int ctas, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, DP, R, KB>, job, ctas);
 }
 
+// Which cut: a tile to a cluster of up to eight CTAs where that many tiles' clusters are
+// resident at once and no CTA takes more than kSplitBlocks blocks even if the table's positions
+// are all in use (the lengths are on the device).  Else the even work list, cut for
+// the CTAs that are resident (cut for two or four times as many, so that a CTA that is done
+// makes room for another, 64 requests of 4096 positions took 213 and 220 us instead of 204: the
+// starts and the parts to join cost more than the even finish gives).
 template <typename T, int DP>
 cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
   using Cfg = RowsCfg<T, DP>;
@@ -557,16 +656,39 @@ cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(attn_rows_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg::kSmem);
+    e = cudaFuncSetAttribute(attn_rows_kernel<T, DP, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attn_rows_kernel<T, DP, true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   const int rows = job.phase == kShared ? job.B * job.N * job.G : job.N * job.G;
   job.row_tiles = (rows + kRowsR - 1) / kRowsR;
   job.entries = job.phase == kShared ? job.row_tiles : job.row_tiles * job.B;
-  const int grid = min(device_sm_count() * Cfg::kCtasPerSm, kAttnMaxCtas);
-  attn_rows_kernel<T, DP><<<grid, kRowsThreads, Cfg::kSmem, s>>>(job);
+  const int resident = device_sm_count() * Cfg::kCtasPerSm;
+  const int64_t tiles = (int64_t)job.entries * job.Hkv;
+  const int64_t positions = job.phase == kShared ? job.shared_len
+                                                 : (int64_t)job.max_pages * job.pd.size - job.shared_len;
+  int split = kMaxSplit;
+  while (split > 1 && tiles * split > resident) split /= 2;
+  if ((positions + kRowsKB - 1) / kRowsKB <= (int64_t)kSplitBlocks * split && tiles <= 0x7fffffff) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_rows_kernel<T, DP, true>, job);
+  }
+  const int grid = min(resident, kAttnMaxCtas);
+  attn_rows_kernel<T, DP, false><<<grid, kRowsThreads, Cfg::kSmem, s>>>(job);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_combine<T, DP, kRowsR, kRowsKB>(job, grid, s);
@@ -577,7 +699,7 @@ constexpr size_t kAttnSlotRows =
     2 * (size_t)(kAttnTcSlots > kAttnMaxCtas * kRowsR ? kAttnTcSlots : kAttnMaxCtas * kRowsR);
 
 struct AttnWs {
-  size_t desc, ms, o, shared_lse, shared_o, total;
+  size_t desc, ms, o, own_lse, own_o, total;
 };
 
 int padded_dim(int d) { return d <= 64 ? 64 : 128; }
@@ -592,11 +714,11 @@ AttnWs attn_ws(int64_t rows, int Hq, int D, int shared_len) {
   off = align_up(off + kAttnSlotRows * 2 * 4, 256);
   w.o = off;
   off = align_up(off + kAttnSlotRows * DP * 4, 256);
-  w.shared_lse = off;
-  w.shared_o = off;
+  w.own_lse = off;
+  w.own_o = off;
   if (shared_len > 0) {
     off = align_up(off + (size_t)rows * Hq * 4, 256);
-    w.shared_o = off;
+    w.own_o = off;
     off = align_up(off + (size_t)rows * Hq * DP * 4, 256);
   }
   w.total = off;
@@ -698,11 +820,11 @@ extern "C" int spec_tree_attention_paged(
   job.part_desc = reinterpret_cast<int4*>(ws + w.desc);
   job.part_ms = reinterpret_cast<float*>(ws + w.ms);
   job.part_o = reinterpret_cast<float*>(ws + w.o);
-  job.shared_lse = reinterpret_cast<float*>(ws + w.shared_lse);
-  job.shared_o = reinterpret_cast<float*>(ws + w.shared_o);
+  job.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
+  job.own_o = reinterpret_cast<float*>(ws + w.own_o);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool narrow = padded_dim(job.D) == 64;
-  for (int phase = shared_len > 0 ? kShared : kOwn; phase >= kOwn; --phase) {
+  for (int phase = kOwn; phase <= (shared_len > 0 ? kShared : kOwn); ++phase) {
     job.phase = phase;
     cudaError_t e = cudaSuccess;
     bool taken = false;

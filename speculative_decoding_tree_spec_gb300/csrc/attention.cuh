@@ -10,10 +10,12 @@
 // the order of the keys.  The split depends on the lengths and the grid alone, so a call is
 // reproducible bit for bit.
 //
-// Two phases: kOwn takes each sequence's own positions (from shared_len on) and writes the
-// call's outputs; kShared takes the positions all sequences share, for the rows of all
-// sequences at once (row r = (b * N + node) * G + g), and writes a normalised result that
-// kOwn joins with its own.
+// Two phases: kOwn takes each sequence's own positions (from shared_len on); kShared, after it,
+// the positions all sequences share, for the rows of all sequences at once (row r = (b * N +
+// node) * G + g).  With shared positions kOwn leaves a normalised fp32 result that kShared
+// joins with its own: the shared tiles are the long ones, beside which the join costs little
+// (the other order, the join in the short own tiles, took 187 us instead of 150 for the own part
+// of 256 x 26-node trees on 16 to 400 positions).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,7 +24,7 @@
 
 namespace svk {
 
-constexpr int kAttnMaxCtas = 512;  // grid limit: two slots per CTA in the workspace
+constexpr int kAttnMaxCtas = 512;   // grid limit: two slots per CTA in the workspace
 constexpr int kAttnTcSlots = 256 * 256;  // tensor-memory kernel: limit of CTAs * rows of a tile
 constexpr int kAttnTcKeys = 128;  // keys of the tensor-memory kernel's block
 constexpr int kAttnRowsTile = 16;  // rows of the few-rows kernel's tile
@@ -44,10 +46,11 @@ struct AttnJob {  // (the kernels' argument)
   FastDiv by_g, by_ng;  // G, N * G
   float scale_log2;  // scale * log2(e)
   int phase;
-  // result of the shared positions, [Hkv][B * N * G] rows: normalised output (row pitch DP)
-  // and its log2-sum-exp2
-  float* shared_o;
-  float* shared_lse;
+  int q_tma;  // queries come by tensor map
+  // result of the own positions where there are shared ones, [Hkv][B * N * G] rows:
+  // normalised output (row pitch DP) and its log2-sum-exp2
+  float* own_o;
+  float* own_lse;
   // two slots per CTA: [slot][R] maximum and sum, [slot][R][DP] output
   float* part_ms;
   float* part_o;
@@ -265,63 +268,64 @@ template <typename T> __device__ __forceinline__ bool unit_nonfinite(const uint4
   return bad;
 }
 
-// One row's result: its part (m, l, o[0..n) of columns c0..) joined with the shared
-// positions' result and written, or, in the shared phase, left for that join.
+// Whether the result of row (b, node) counts: a query that is no padding, of a sequence that
+// does stand behind the shared positions.
+__device__ __forceinline__ bool attn_query(const AttnJob& job, int b, int node) {
+  if (job.counts && node >= job.counts[b]) return false;
+  return job.shared_len == 0 || job.prefix[b] >= job.shared_len;
+}
+
+// Weights of a row's result (m, l, log2 units) and of the own positions' result left for it
+// (its log2-sum-exp2): out = o * w + own * w_own, and their log2-sum-exp2.
+struct AttnJoin {
+  float w, w_own, lse2;
+};
+__device__ __forceinline__ AttnJoin attn_join(float m, float l, float own) {
+  AttnJoin j;
+  j.w = l == 0.f ? 0.f : 1.f / l;
+  j.w_own = 0.f;
+  j.lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
+  if (own != -CUDART_INF_F) {
+    const float top = fmaxf(own, j.lse2);
+    const float eo = exp2f(own - top), es = l == 0.f ? 0.f : exp2f(j.lse2 - top);
+    j.w_own = eo / (eo + es);
+    j.w = l == 0.f ? 0.f : es / (eo + es) / l;
+    j.lse2 = top + log2f(eo + es);
+  }
+  return j;
+}
+
+// One row's result: its part (m, l, o[0..n) of columns c0..), left for the shared positions or
+// joined with what the own positions left, and written.
 template <typename T, int C>
 __device__ __forceinline__ void write_row(const AttnJob& job, const AttnTile& t, int head, int r,
                                           int c0, int DP, float m, float l, float (&o)[C]) {
   int b, node, g;
   if (!attn_row(job, t, r, b, node, g)) return;
-  if (job.phase == kShared) {
-    const int64_t row = (int64_t)head * job.B * job.N * job.G + r;
-    const float inv = 1.f / l;  // l > 0: every row of the shared positions sees them
-    float4* dst = reinterpret_cast<float4*>(job.shared_o + row * DP + c0);
+  const int64_t row = ((int64_t)head * job.B + (job.phase == kShared ? 0 : b)) * job.by_ng.d + r;
+  const bool leave = job.phase == kOwn && job.shared_len > 0;
+  const bool query = leave || attn_query(job, b, node);
+  const AttnJoin j = attn_join(m, l, job.phase == kShared && query ? job.own_lse[row] : -CUDART_INF_F);
+  const bool some = query && l != 0.f;
 #pragma unroll
-    for (int i = 0; i < C; i += 4)
-      dst[i / 4] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                            : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-    if (c0 == 0) job.shared_lse[row] = l == 0.f ? -CUDART_INF_F : m + log2f(l);
-    return;
+  for (int i = 0; i < C; ++i) o[i] = some ? o[i] * j.w : 0.f;
+  if (query && j.w_own != 0.f) {
+    const float* own = job.own_o + row * DP + c0;
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(own + i);
+      o[i] += x.x * j.w_own;
+      o[i + 1] += x.y * j.w_own;
+      o[i + 2] += x.z * j.w_own;
+      o[i + 3] += x.w * j.w_own;
+    }
   }
-  const bool real = node < t.count;
-  float lse2;
-  if (!real) {
-    lse2 = -CUDART_INF_F;
+  if (leave) {
+    float4* dst = reinterpret_cast<float4*>(job.own_o + row * DP + c0);
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
-  } else {
-    float w = l == 0.f ? 0.f : 1.f / l, ws = 0.f;
-    lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
-    const float* so = nullptr;
-    if (job.shared_len > 0) {
-      const int64_t row =
-          ((int64_t)head * job.B + b) * job.N * job.G + (int64_t)node * job.G + g;
-      const float s2 = job.shared_lse[row];
-      if (s2 != -CUDART_INF_F) {
-        so = job.shared_o + row * DP + c0;
-        const float top = fmaxf(s2, lse2);
-        const float es = exp2f(s2 - top);
-        const float eo = lse2 == -CUDART_INF_F ? 0.f : exp2f(lse2 - top);
-        ws = es / (es + eo);
-        w = l == 0.f ? 0.f : eo / (es + eo) / l;
-        lse2 = top + log2f(es + eo);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float x = l == 0.f ? 0.f : o[i] * w;
-      o[i] = x;
-    }
-    if (so) {
-#pragma unroll
-      for (int i = 0; i < C; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(so + i);
-        o[i] += x.x * ws;
-        o[i + 1] += x.y * ws;
-        o[i + 2] += x.z * ws;
-        o[i + 3] += x.w * ws;
-      }
-    }
+    for (int i = 0; i < C; i += 4) dst[i / 4] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    if (c0 == 0) job.own_lse[row] = j.lse2;
+    return;
   }
   const int h = head * job.G + g;
   T* dst = static_cast<T*>(job.out) + b * job.lo.batch_stride + node * job.lo.node_stride +
@@ -337,7 +341,8 @@ __device__ __forceinline__ void write_row(const AttnJob& job, const AttnTile& t,
     }
   }
   if (c0 == 0 && job.lse)
-    job.lse[((int64_t)b * job.N + node) * job.Hq + h] = lse2 * 0.693147180559945309f;
+    job.lse[((int64_t)b * job.N + node) * job.Hq + h] =
+        query ? j.lse2 * 0.693147180559945309f : -CUDART_INF_F;
 }
 
 // Infinities and NaN among the draft positions' values [from, to) that row (node) sees.  A

@@ -61,7 +61,7 @@ struct TcCfg {
 
 struct TcShared {
   uint64_t full[8], empty[8];  // ring entries: key and value blocks in turn
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], done;
   uint32_t tmem;
   int abort;
   int poison;
@@ -91,7 +91,8 @@ struct TcWait {
 template <int DP, int H>
 __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnJob job,
+                   const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttnJob job,
                    int box_rows) {
   using Cfg = TcCfg<DP, H>;
   constexpr int kTcR = Cfg::kR;
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
       mbar_init(&sh.empty[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&sh.q_full[w], 4);
+      mbar_init(&sh.q_full[w], job.q_tma ? 1 : 4);
+      mbar_init(&sh.q_empty[w], 1);
       mbar_init(&sh.s_full[w], 1);
       mbar_init(&sh.p_full[w][0], 4);
       mbar_init(&sh.p_full[w][1], 4);
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     const int boxes = kTcKB / box_rows;
+    uint32_t q_loads[H] = {};
     for (; walk.left > 0; walk.next(job)) {
       const AttnTile t = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);
       lens = attn_lens(job, walk.next_entry(job));
@@ -172,6 +175,24 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
       for (int i = 0; i < nb; ++i) {
         const int next = page_of(i + 1);
         issue(&tm_k, page, i);
+        if (i == 0 && job.q_tma) {
+          // the tile's queries, once the scores of the tile before have read theirs: rows
+          // (node, query head of the key head) of each half
+#pragma unroll
+          for (int w = 0; w < H; ++w) {
+            if (rows_all - t.row0 <= w * kTcHalf) break;
+            wait(&sh.q_empty[w], (q_loads[w]++ & 1u) ^ 1u);
+            if (__any_sync(kFull, wait.aborted())) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sh.q_full[w], Cfg::kQHalfBytes);
+#pragma unroll
+              for (int c = 0; c < Cfg::kChunks; ++c)
+                tma_load_4d(sq + w * Cfg::kQHalfBytes + c * Cfg::kQChunkBytes, &tm_q, c * 64,
+                            head * job.G, job.by_g.div(t.row0 + w * kTcHalf), t.b, &sh.q_full[w]);
+            }
+            __syncwarp();
+          }
+        }
         issue(&tm_v, page, i);
         page = next;
       }
@@ -180,11 +201,14 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     const uint32_t first = ent > (uint32_t)NST ? ent - NST : 0u;
     for (uint32_t e = first; e < ent; ++e)
       mbar_wait(&sh.full[e % NST], (e / NST) & 1u, kTcLimitNs);
+#pragma unroll
+    for (int w = 0; w < H; ++w)
+      if (q_loads[w] > 0) mbar_wait(&sh.q_full[w], (q_loads[w] - 1) & 1u, kTcLimitNs);
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     constexpr uint32_t idesc_s = bf16_idesc(kTcKB, false), idesc_o = bf16_idesc(DP, true);
     uint32_t seg[H] = {}, blk[H] = {};
-    auto scores = [&](int w, uint32_t stage) {
+    auto scores = [&](int w, uint32_t stage, bool last) {  // last: of the tile
       const uint64_t a = sw128_tile(sq + w * Cfg::kQHalfBytes, 16);
       const uint64_t b = sw128_tile(ring + stage * Cfg::kStageBytes, 16);
       if (elect_one()) {
@@ -195,6 +219,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
                       b + (uint64_t)(((ks >> 2) * Cfg::kChunkBytes + (ks & 3) * 32) >> 4), idesc_s,
                       ks > 0);
         tc05_commit(&sh.s_full[w]);
+        if (last) tc05_commit(&sh.q_empty[w]);
       }
       __syncwarp();
     };
@@ -225,7 +250,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
       tc05_fence_after();
 #pragma unroll
       for (int w = 0; w < H; ++w)
-        if (w < halves) scores(w, st);
+        if (w < halves) scores(w, st, nb == 1);
       release(st);
       advance();
       for (int i = 0; i < nb; ++i) {
@@ -261,7 +286,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
               wait(&sh.full[sk], pk);
               tc05_fence_after();
             }
-            scores(w, sk);
+            scores(w, sk, i + 2 == nb);
             if (w == halves - 1) release(sk);
           }
         }
@@ -283,9 +308,11 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     const int boxes = kTcKB / box_rows, box_shift = 31 - __clz(box_rows);
     uint32_t blk = 0, seg = 0;  // blocks and segments of this half so far
 
-    // the half's queries into shared memory (K-major, 128-byte swizzle): each warp its 32 rows,
-    // a few rows to a copy; landed_q, later, hands them to the products
+    // Where no tensor map takes them: the half's queries into shared memory (K-major, 128-byte
+    // swizzle), each warp its 32 rows, a few rows to a copy; landed_q, later, hands them to the
+    // products.
     auto load_q = [&](int hd, const AttnTile& t) {
+      if (job.q_tma) return;
       if (H == 2 && w == 1 && rows_all - t.row0 <= kTcHalf) return;
       int b, node, g;
       const bool real = attn_row(job, t, t.row0 + w * kTcHalf + tid, b, node, g);
@@ -305,13 +332,14 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
       }
     };
     auto landed_q = [&](const AttnTile& t) {
+      if (job.q_tma) return;
       if (H == 2 && w == 1 && rows_all - t.row0 <= kTcHalf) return;
       asm volatile("cp.async.wait_all;\n" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[w]);
     };
-    // a later tile's rows on their way into the L2: queries, mask, the shared positions' result
+    // the next tile's rows on their way into the L2: queries, mask, the own positions' result
     auto prefetch_rows = [&](int hd, int en) {
       AttnTile t;
       t.b = job.phase == kShared ? 0 : en / job.row_tiles;
@@ -321,20 +349,30 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
       const uint16_t* q = static_cast<const uint16_t*>(job.q) + b * job.lq.batch_stride +
                           node * job.lq.node_stride + (hd * job.G + g) * job.lq.head_stride;
       for (int d = 0; d < job.D; d += 64) prefetch_l2(q + d);
-      if (job.phase == kShared) return;
-      if (job.mask) prefetch_l2(job.mask + ((int64_t)b * job.N + node) * job.N);
-      if (job.shared_len > 0) {
-        const float* so = job.shared_o + (((int64_t)hd * job.B + b) * job.by_ng.d +
-                                          t.row0 + w * kTcHalf + tid) * DP;
+      if (job.phase == kShared) {
+        const float* own = job.own_o + ((int64_t)hd * job.B * job.by_ng.d + t.row0 +
+                                        w * kTcHalf + tid) * DP;
 #pragma unroll
-        for (int d = 0; d < DP; d += 32) prefetch_l2(so + d);
+        for (int d = 0; d < DP; d += 32) prefetch_l2(own + d);
+      } else if (job.mask) {
+        prefetch_l2(job.mask + ((int64_t)b * job.N + node) * job.N);
       }
+    };
+    // Page numbers of kTcCheck blocks, two boxes of each lane, read ahead (0 past the last
+    // visible key: masked there).  Only where one is no page are the keys of the blocks looked
+    // at one by one.
+    auto page_at = [&](const AttnTile& t, int pos0, int box) {
+      const int pos = pos0 + box * box_rows;
+      if (box >= kTcCheck * boxes || pos >= t.kend) return 0;
+      return job.table[(int64_t)t.b * job.max_pages + job.pd.div(pos)];  // kend lies within it
     };
     AttnTile t = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);
     if (walk.left > 0) {
       load_q(walk.head, t);
       landed_q(t);
     }
+    int ahead_a = page_at(t, t.kbeg + walk.unit * kTcKB, lane);
+    int ahead_b = page_at(t, t.kbeg + walk.unit * kTcKB, lane + 32);
     int4 desc = make_int4(0, 0, 0, kSlotNone);
     while (walk.left > 0) {
       walk.take(t.blocks);
@@ -342,7 +380,6 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
       walk.next(job);
       const bool more = walk.left > 0;
       lens = attn_lens(job, walk.entry);
-      if (more) prefetch_rows(walk.head, walk.entry);
       const int halves = H == 2 && rows_all - t.row0 > kTcHalf ? 2 : 1;
       const int seg0 = t.kbeg + block * kTcKB;
       if (nb != t.blocks) {
@@ -358,25 +395,15 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
         const int r = t.row0 + w * kTcHalf + tid;
         int rb, node, g;
         const bool real = attn_row(job, t, r, rb, node, g);
-        const int32_t* table_row = job.table + (int64_t)t.b * job.max_pages;
         float m = -CUDART_INF_F, l = 0.f;
-        // Page numbers of the next kTcCheck blocks, two boxes of each lane, read ahead (0 past
-        // the last visible key: masked there).  Only where one is no page are the keys of the
-        // blocks looked at one by one.
-        auto page_at = [&](int i, int box) {
-          const int pos = seg0 + i * kTcKB + box * box_rows;
-          if (i >= nb || box >= kTcCheck * boxes || pos >= t.kend) return 0;
-          return table_row[job.pd.div(pos)];  // kend lies within the table
-        };
-        int ahead_a = page_at(0, lane), ahead_b = page_at(0, lane + 32);
         bool bad = false;
         for (int i = 0; i < nb; ++i) {
           const int pos0 = seg0 + i * kTcKB;
           if (i % kTcCheck == 0) {
             bad = __any_sync(kFull, (unsigned)ahead_a >= (unsigned)job.n_pages ||
                                         (unsigned)ahead_b >= (unsigned)job.n_pages);
-            ahead_a = page_at(i + kTcCheck, lane);
-            ahead_b = page_at(i + kTcCheck, lane + 32);
+            ahead_a = page_at(t, pos0 + kTcCheck * kTcKB, lane);
+            ahead_b = page_at(t, pos0 + kTcCheck * kTcKB, lane + 32);
           }
           const bool drafts = pos0 + kTcKB > t.clear;  // rows may differ in what they see
           uint32_t sees[4];
@@ -422,7 +449,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
               }
             }
             if (bad) {
-              const int mine = page_at(i, lane);
+              const int mine = page_at(t, pos0, lane);
               const unsigned ok = __ballot_sync(
                   kFull, lane >= boxes || (unsigned)mine < (unsigned)job.n_pages);
 #pragma unroll
@@ -435,6 +462,26 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
           ++blk;
           __syncwarp();
           tc05_fence_after();
+          if (drafts || bad) {
+            // keys the row does not see become -inf where they lie, in a small loop of its own:
+            // the code that every block runs stays short (it does not fit the nearest
+            // instruction caches as it is)
+#pragma unroll 1
+            for (int ch = 0; ch < kTcKB; ch += 16) {
+              const uint32_t word = ch < 64 ? (ch < 32 ? sees[0] : sees[1])
+                                            : (ch < 96 ? sees[2] : sees[3]);
+              const uint32_t bits = word >> (ch & 16);
+              uint32_t x[16];
+              tc05_ld16(t_s + ch, x);
+              tc05_wait_ld();
+              tc05_landed16(x);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (!((bits >> k) & 1u)) x[k] = 0xff800000u;
+              tc05_st16(t_s + ch, x);
+            }
+            tc05_wait_st();
+          }
           uint32_t s[kTcKB];
           tc05_ld32(t_s, s);
           tc05_ld32(t_s + 32, s + 32);
@@ -445,11 +492,6 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
           tc05_landed(s + 32);
           tc05_landed(s + 64);
           tc05_landed(s + 96);
-          if (drafts || bad) {
-#pragma unroll
-            for (int k = 0; k < kTcKB; ++k)
-              if (!((sees[k >> 5] >> (k & 31)) & 1u)) s[k] = 0xff800000u;  // -inf
-          }
           float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
           for (int k = 0; k < kTcKB; k += 8)
@@ -489,26 +531,21 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
               return reinterpret_cast<uint4*>(vb + (u >> 3) * Cfg::kChunkBytes + key * 128 +
                                               (((u & 7) ^ (key & 7)) << 4));
             };
-            const int step = halves * kTcHalf, first = w * kTcHalf + tid;
-            for (int x = k0 * CPR + first; x < kn * CPR; x += 4 * step) {
-              uint4 v[4];
+            const int step = halves * kTcHalf;
+#pragma unroll 1
+            for (int x = k0 * CPR + w * kTcHalf + tid; x < kTcKB * CPR; x += step) {
+              uint4* at = unit_at(x);
+              const uint4 v = x < kn * CPR ? *at : make_uint4(~0u, ~0u, ~0u, ~0u);
+              if (!unit_nonfinite<uint16_t>(v)) continue;
+              uint32_t z[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = x + e * step < kn * CPR ? *unit_at(x + e * step) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (unit_nonfinite<uint16_t>(v[e])) {
-                  uint32_t z[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-                  for (int q = 0; q < 4; ++q) {
-                    if ((z[q] & 0x7f800000u) == 0x7f800000u) z[q] &= 0xffffu;
-                    if ((z[q] & 0x7f80u) == 0x7f80u) z[q] &= 0xffff0000u;
-                  }
-                  *unit_at(x + e * step) = make_uint4(z[0], z[1], z[2], z[3]);
-                  *((volatile int*)&sh.poison) = 1;
-                }
+              for (int q = 0; q < 4; ++q) {
+                if ((z[q] & 0x7f800000u) == 0x7f800000u) z[q] &= 0xffffu;
+                if ((z[q] & 0x7f80u) == 0x7f80u) z[q] &= 0xffff0000u;
+              }
+              *at = make_uint4(z[0], z[1], z[2], z[3]);
+              if (x < kn * CPR) *((volatile int*)&sh.poison) = 1;
             }
-            for (int x = max(kn, 0) * CPR + first; x < kTcKB * CPR; x += step)
-              *unit_at(x) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             asm volatile("bar.sync 2, %0;\n" ::"r"(halves * kTcHalf) : "memory");
           }
@@ -524,11 +561,6 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
               tc05_wait_ld();
               tc05_landed(z);
               tc05_landed(z + 32);
-              if (drafts || bad) {
-#pragma unroll
-                for (int k = 0; k < 64; ++k)
-                  if (!((sees[k >> 5] >> (k & 31)) & 1u)) z[k] = 0xff800000u;
-              }
             }
             uint32_t p[32];
 #pragma unroll
@@ -547,52 +579,59 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[w][part]);
           }
+          if (i == 0 && more) prefetch_rows(walk.head, walk.entry);
           sum = add_f32x2(sum, sum2);
           l += sum.x + sum.y;
         }
         // the last scores are read: the half's queries may be replaced
         const AttnTile t_next = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);
         if (more) load_q(walk.head, t_next);
+        ahead_a = page_at(t_next, t_next.kbeg, lane);
+        ahead_b = page_at(t_next, t_next.kbeg, lane + 32);
 
         // ---- epilogue.  Each thread scales its row; the rows leave through the warp's staging
-        // area, four lanes to the 64 bytes of a row, so that a store fills whole sectors. ----
+        // area, so that a store fills whole sectors. ----
         const bool whole = nb == t.blocks;
-        const bool wide = !whole || job.phase == kShared;  // fp32 rows
+        const bool leave = job.phase == kOwn && job.shared_len > 0;  // for the shared positions
+        const bool wide = !whole || leave;                           // fp32 rows
         const int slot = 2 * cta + (block == 0 ? 1 : 0);
         const int rr = w * kTcHalf + tid;
-        const int64_t shared_row = job.phase == kShared
-            ? (int64_t)head * job.B * job.N * job.G + r
-            : ((int64_t)head * job.B + rb) * job.N * job.G + r;
-        const bool prior = whole && job.phase == kOwn && job.shared_len > 0;
+        const int64_t own_row =
+            ((int64_t)head * job.B + (job.phase == kShared ? 0 : rb)) * job.by_ng.d + r;
+        const bool prior = whole && job.phase == kShared;
         int64_t to = -1;  // this row's destination
         if (!whole) to = ((int64_t)slot * kTcR + rr) * DP;
-        else if (real) to = job.phase == kShared ? shared_row * DP
-                                                 : rb * job.lo.batch_stride +
-                                                       node * job.lo.node_stride +
-                                                       (head * job.G + g) * job.lo.head_stride;
-        // this lane's part of the rows lane / 4 + 8 i of the warp
+        else if (real) to = leave ? own_row * DP
+                                  : rb * job.lo.batch_stride + node * job.lo.node_stride +
+                                        (head * job.G + g) * job.lo.head_stride;
+        // fp32 rows leave as 16 columns, four lanes to the 64 bytes of a row: this lane's part of
+        // the rows lane / 4 + 8 i of the warp
         const int sub = lane & 3;
-        int64_t dst[4], src[4];
+        int64_t src[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dst[i] = __shfl_sync(kFull, to, (lane >> 2) + 8 * i);
-          src[i] = __shfl_sync(kFull, real ? shared_row * DP : (int64_t)-1, (lane >> 2) + 8 * i);
-        }
+        for (int i = 0; i < 4; ++i)
+          src[i] = __shfl_sync(kFull, prior && real ? own_row * DP : (int64_t)-1,
+                               (lane >> 2) + 8 * i);
         unsigned char* stage = base_p + Cfg::kQBytes + NST * Cfg::kStageBytes +
                                (w * 4 + (warp & 3)) * 32 * kTcStagePitch;
         unsigned char* stage_row = stage + lane * kTcStagePitch;
         unsigned char* stage_out = stage + (lane >> 2) * kTcStagePitch + sub * 16;
-        float4 ahead[8];  // the shared positions' result, 32 columns ahead
+        float4 ahead[4], ahead2[4];  // the own positions' result, 16 and 32 columns ahead
         auto fetch = [&](int col) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            ahead[i] = src[i & 3] >= 0
-                           ? *reinterpret_cast<const float4*>(job.shared_o + src[i & 3] + col +
-                                                              (i >> 2) * 16 + sub * 4)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < 4; ++i)
+            ahead2[i] = src[i] >= 0 && col < DP
+                            ? *reinterpret_cast<const float4*>(job.own_o + src[i] + col + sub * 4)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
         };
-        if (prior) fetch(0);
-        const float s2 = prior && real ? job.shared_lse[shared_row] : -CUDART_INF_F;
+        if (prior) {
+          fetch(0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ahead[i] = ahead2[i];
+          fetch(16);
+        }
+        const bool query = real && (!whole || leave || attn_query(job, rb, node));
+        const float own_lse = prior && query ? job.own_lse[own_row] : -CUDART_INF_F;
         wait(&sh.o_full[w], seg & 1u);
         ++seg;
         if (more) landed_q(t_next);
@@ -621,101 +660,91 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
           tc05_wait_st();
         }
         const float m2 = m == -CUDART_INF_F ? m : m * c;
-        // the row's weight, and the shared positions' where they are joined
-        bool some = l != 0.f;
-        float wo = 1.f, ws = 0.f;
+        // the row's weight, and the own positions' where they are joined
+        bool some = true;
+        float wo = 1.f, w_own = 0.f;
         if (!whole) {
           job.part_ms[(slot * 2) * kTcR + rr] = m2;
           job.part_ms[(slot * 2 + 1) * kTcR + rr] = l;
-          some = true;
-        } else if (job.phase == kShared) {
-          wo = 1.f / l;
-          if (real) job.shared_lse[shared_row] = some ? m2 + log2f(l) : -CUDART_INF_F;
         } else {
-          const bool query = real && node < t.count;
-          some = some && query;
-          float lse2 = some ? m2 + log2f(l) : -CUDART_INF_F;
-          wo = 1.f / l;
-          if (query && s2 != -CUDART_INF_F) {
-            const float top = fmaxf(s2, lse2);
-            const float es = exp2f(s2 - top), eo = some ? exp2f(lse2 - top) : 0.f;
-            ws = es / (es + eo);
-            wo = eo / (es + eo) / l;
-            lse2 = top + log2f(es + eo);
-          }
-          if (real && job.lse)
+          const AttnJoin j = attn_join(m2, l, own_lse);
+          some = query && l != 0.f;
+          wo = j.w;
+          w_own = query ? j.w_own : 0.f;
+          if (leave && real) {
+            job.own_lse[own_row] = j.lse2;
+          } else if (real && job.lse) {
             job.lse[((int64_t)rb * job.N + node) * job.Hq + head * job.G + g] =
-                lse2 * 0.693147180559945309f;
+                query ? j.lse2 * 0.693147180559945309f : -CUDART_INF_F;
+          }
         }
 #pragma unroll 1
-        for (int ch = 0; ch < DP; ch += 32) {
-          uint32_t o[32];
+        for (int ch = 0; ch < DP; ch += 16) {
+          uint32_t o[16];
           __syncwarp();
-          tc05_ld32(t_o + ch, o);
+          tc05_ld16(t_o + ch, o);
           tc05_wait_ld();
-          tc05_landed(o);
-          float of[32];
+          tc05_landed16(o);
+          float of[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) of[k] = some ? __uint_as_float(o[k]) * wo : 0.f;
+          for (int k = 0; k < 16; ++k) of[k] = some ? __uint_as_float(o[k]) * wo : 0.f;
           if (prior) {
-            float4 x[8];
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(stage_out + 8 * i * kTcStagePitch) = ahead[4 * part + i];
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                x[4 * part + k] = *reinterpret_cast<const float4*>(stage_row + k * 16);
-              __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+              *reinterpret_cast<float4*>(stage_out + 8 * i * kTcStagePitch) = ahead[i];
+              ahead[i] = ahead2[i];
             }
-            if (ch + 32 < DP) fetch(ch + 32);
-            const bool joined = ws != 0.f;
+            fetch(ch + 32);
+            __syncwarp();
+            const bool joined = w_own != 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              of[4 * k] += joined ? x[k].x * ws : 0.f;
-              of[4 * k + 1] += joined ? x[k].y * ws : 0.f;
-              of[4 * k + 2] += joined ? x[k].z * ws : 0.f;
-              of[4 * k + 3] += joined ? x[k].w * ws : 0.f;
+            for (int k = 0; k < 16; k += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(stage_row + k * 4);
+              of[k] += joined ? x.x * w_own : 0.f;
+              of[k + 1] += joined ? x.y * w_own : 0.f;
+              of[k + 2] += joined ? x.z * w_own : 0.f;
+              of[k + 3] += joined ? x.w * w_own : 0.f;
             }
+            __syncwarp();
           }
           if (wide) {
-            float* out = job.phase == kShared && whole ? job.shared_o : job.part_o;
+            float* out = whole ? job.own_o : job.part_o;
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<float4*>(stage_row + k * 4) =
+                  make_float4(of[k], of[k + 1], of[k + 2], of[k + 3]);
+            __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 16; k += 4)
-                *reinterpret_cast<float4*>(stage_row + k * 4) =
-                    make_float4(of[16 * part + k], of[16 * part + k + 1], of[16 * part + k + 2],
-                                of[16 * part + k + 3]);
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (dst[i] >= 0)
-                  *reinterpret_cast<float4*>(out + dst[i] + ch + 16 * part + sub * 4) =
-                      *reinterpret_cast<const float4*>(stage_out + 8 * i * kTcStagePitch);
-              __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+              const int64_t dst = __shfl_sync(kFull, to, (lane >> 2) + 8 * i);
+              if (dst >= 0)
+                *reinterpret_cast<float4*>(out + dst + ch + sub * 4) =
+                    *reinterpret_cast<const float4*>(stage_out + 8 * i * kTcStagePitch);
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8)
+            for (int k = 0; k < 16; k += 8)
               *reinterpret_cast<uint4*>(stage_row + k * 2) =
                   make_uint4(pack_bf16(of[k], of[k + 1]), pack_bf16(of[k + 2], of[k + 3]),
                              pack_bf16(of[k + 4], of[k + 5]), pack_bf16(of[k + 6], of[k + 7]));
             __syncwarp();
-            uint16_t* out = static_cast<uint16_t*>(job.out);
+            const int unit = lane & 1;  // two lanes to the 32 bytes of a row
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (dst[i] >= 0 && ch + sub * 8 < job.D)
-                *reinterpret_cast<uint4*>(out + dst[i] + ch + sub * 8) =
-                    *reinterpret_cast<const uint4*>(stage_out + 8 * i * kTcStagePitch);
+            for (int i = 0; i < 2; ++i) {
+              const int row = (lane >> 1) + 16 * i;
+              const int64_t dst = __shfl_sync(kFull, to, row);
+              if (dst >= 0 && ch + unit * 8 < job.D)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(job.out) + dst + ch + unit * 8) =
+                    *reinterpret_cast<const uint4*>(stage + row * kTcStagePitch + unit * 16);
+            }
           }
         }
         tc05_fence_before();
         t = t_next;
       } else {
         t = attn_tile<kTcR, kTcKB>(job, walk.entry, lens);  // this half idles in this tile
+        ahead_a = page_at(t, t.kbeg, lane);
+        ahead_b = page_at(t, t.kbeg, lane + 32);
         if (more) {
           load_q(walk.head, t);
           landed_q(t);
@@ -770,13 +799,39 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, const AttnJob& job, int b
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [batch][node][head][d], a box being the rows of a half: 64 d of a key head's
+// query heads in 128 / G nodes.  The shared positions' tiles run over the nodes of all
+// sequences, so there batches and nodes have to be one direction.
+bool make_query_map(CUtensorMap* map, const AttnJob& job) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || kTcHalf % job.G != 0) return false;
+  int64_t nodes = job.N, batches = job.B, step = job.lq.node_stride;
+  if (job.phase == kShared) {
+    if (job.N == 1) step = job.lq.batch_stride;
+    else if (job.B > 1 && job.lq.batch_stride != job.N * job.lq.node_stride) return false;
+    nodes *= batches;
+    batches = 1;
+  }
+  const cuuint64_t dims[4] = {(cuuint64_t)job.D, (cuuint64_t)job.Hq, (cuuint64_t)nodes,
+                              (cuuint64_t)batches};
+  const cuuint64_t strides[3] = {(cuuint64_t)job.lq.head_stride * 2, (cuuint64_t)step * 2,
+                                 (cuuint64_t)job.lq.batch_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)job.G, (cuuint32_t)(kTcHalf / job.G), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(job.q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DP, int H>
 cudaError_t launch_tc(AttnJob job, int rows, cudaStream_t s, bool* taken) {
   using Cfg = TcCfg<DP, H>;
   const int box = tc_box_rows(job.pd.size);
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k, tm_v, tm_q;
   *taken = make_cache_map(&tm_k, job.k, job, box) && make_cache_map(&tm_v, job.v, job, box);
   if (!*taken) return cudaSuccess;
+  job.q_tma = make_query_map(&tm_q, job);
+  if (!job.q_tma) tm_q = tm_k;  // not used
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -791,7 +846,7 @@ cudaError_t launch_tc(AttnJob job, int rows, cudaStream_t s, bool* taken) {
   job.entries = job.phase == kShared ? job.row_tiles : job.row_tiles * job.B;
   const int most = kAttnTcSlots / Cfg::kR, sms = device_sm_count() * (3 - H);
   const int grid = sms < most ? sms : most;
-  attn_tc_kernel<DP, H><<<grid, Cfg::kThreads, Cfg::kSmem, s>>>(tm_k, tm_v, job, box);
+  attn_tc_kernel<DP, H><<<grid, Cfg::kThreads, Cfg::kSmem, s>>>(tm_k, tm_v, tm_q, job, box);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_attn_combine(job, DP, Cfg::kR, grid, s);
