@@ -667,6 +667,7 @@ cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
   const int rows = job.phase == kShared ? job.B * job.N * job.G : job.N * job.G;
   job.row_tiles = (rows + kRowsR - 1) / kRowsR;
   job.entries = job.phase == kShared ? job.row_tiles : job.row_tiles * job.B;
+  job.by_tiles = FastDiv::make(job.row_tiles);
   const int resident = device_sm_count() * Cfg::kCtasPerSm;
   const int64_t tiles = (int64_t)job.entries * job.Hkv;
   const int64_t positions = job.phase == kShared ? job.shared_len

@@ -43,7 +43,7 @@ struct AttnJob {  // (the kernels' argument)
   int row_tiles;   // tiles per sequence (kOwn) or in all (kShared)
   int entries;     // tiles of one key head
   PageDiv pd;
-  FastDiv by_g, by_ng;  // G, N * G
+  FastDiv by_g, by_ng, by_tiles;  // G, N * G, row_tiles
   float scale_log2;  // scale * log2(e)
   int phase;
   int q_tma;  // queries come by tensor map
@@ -83,7 +83,7 @@ struct AttnLens {
 __device__ __forceinline__ AttnLens attn_lens(const AttnJob& job, int entry) {
   AttnLens x{0, 0};
   if (job.phase == kOwn && entry < job.entries) {
-    const int b = entry / job.row_tiles;
+    const int b = job.by_tiles.div(entry);
     x.prefix = job.prefix[b];
     x.count = job.counts ? job.counts[b] : job.N;
   }
@@ -102,7 +102,7 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnJob& job, int entry, con
     t.kbeg = 0;
     t.kend = t.clear = min(job.shared_len, cap);
   } else {
-    t.b = entry / job.row_tiles;
+    t.b = job.by_tiles.div(entry);
     t.row0 = (entry - t.b * job.row_tiles) * R;
     t.prefix = min(max(lens.prefix, 0), cap);  // no position beyond the table exists
     t.count = min(max(lens.count, 0), job.N);

@@ -33,7 +33,9 @@ namespace svk {
 namespace {
 
 constexpr int kTcHalf = 128, kTcKB = kAttnTcKeys;
-constexpr int kTcC = 4;            // a tile's fixed costs in blocks
+// A tile's fixed costs in blocks.  With 2, 3, 4 and 6 two 4096-token prompts took 325, 305, 287
+// and 282 us (their tiles' lengths differ most); trees and shared prefixes hardly tell.
+constexpr int kTcC = 6;
 constexpr uint32_t kTcP = 64;      // P's column within a half's scores
 constexpr int kTcStagePitch = 80;  // bytes of a staged row: 64 and a pad against bank conflicts
 constexpr int kTcCheck = 4;        // blocks whose page numbers are checked at once
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     // the next tile's rows on their way into the L2: queries, mask, the own positions' result
     auto prefetch_rows = [&](int hd, int en) {
       AttnTile t;
-      t.b = job.phase == kShared ? 0 : en / job.row_tiles;
+      t.b = job.phase == kShared ? 0 : job.by_tiles.div(en);
       t.row0 = (en - t.b * job.row_tiles) * kTcR;
       int b, node, g;
       if (!attn_row(job, t, t.row0 + w * kTcHalf + tid, b, node, g)) return;
@@ -844,6 +846,7 @@ cudaError_t launch_tc(AttnJob job, int rows, cudaStream_t s, bool* taken) {
   }
   job.row_tiles = (rows + Cfg::kR - 1) / Cfg::kR;
   job.entries = job.phase == kShared ? job.row_tiles : job.row_tiles * job.B;
+  job.by_tiles = FastDiv::make(job.row_tiles);
   const int most = kAttnTcSlots / Cfg::kR, sms = device_sm_count() * (3 - H);
   const int grid = sms < most ? sms : most;
   attn_tc_kernel<DP, H><<<grid, Cfg::kThreads, Cfg::kSmem, s>>>(tm_k, tm_v, tm_q, job, box);
