@@ -55,14 +55,13 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 // x = hi + lo with both parts tf32: the products hi hi + hi lo + lo hi carry an fp32
 // product to about 2^-21.  The tensor cores' own sum cuts bits off where an fp32 add rounds, so
 // each step of 8 starts from 0 and is added to the running sums in fp32.
+//
+// hi is x cut to tf32's 10 bits, lo the rest rounded to as many.  An infinite x gives hi = x and
+// a finite lo (the minimum with a bound that no finite x's lo reaches drops inf - inf).
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(hi) : "f"(x));
-  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
-}
-// The same for a value that may be infinite: hi carries it, lo is 0.
-__device__ __forceinline__ void split_tf32_inf(float x, uint32_t& hi, uint32_t& lo) {
-  split_tf32(x, hi, lo);
-  if ((hi & 0x7f800000u) == 0x7f800000u) lo = 0u;
+  hi = __float_as_uint(x) & 0xffffe000u;
+  const float rest = fminf(x - __uint_as_float(hi), 0x1p117f);
+  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(lo) : "f"(rest));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -84,7 +83,7 @@ struct RowsCfg {
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kStageBytes = 2 * kGroup * kRowBytes;  // keys and values
   static constexpr int kStages = 3;
-  static constexpr int kQBytes = sizeof(T) == 4 ? kRowsR * DP * 4 : 0;
+  static constexpr int kQBytes = sizeof(T) == 4 ? 2 * kRowsR * DP * 4 : 0;  // split in two
   static constexpr int kSmem = kRowsWarps * kStages * kStageBytes + kQBytes;
   static constexpr int kCtasPerSm = kSmem > 110 * 1024 ? 1 : 2;
 };
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
   int4 desc = make_int4(0, 0, 0, kSlotNone);
   unsigned char* ring = attn_dyn + warp * S * Cfg::kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
-  float* sq = reinterpret_cast<float*>(attn_dyn + kRowsWarps * S * Cfg::kStageBytes);
+  uint32_t* sq = reinterpret_cast<uint32_t*>(attn_dyn + kRowsWarps * S * Cfg::kStageBytes);
   const float c = job.scale_log2;
 
   for (AttnWalk<kRowsC> walk(range); walk.left > 0; walk.next(job)) {
@@ -214,7 +213,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
           x = Elt<float>::at(static_cast<const float*>(job.q) + b * job.lq.batch_stride +
                                  n * job.lq.node_stride + (head * job.G + g) * job.lq.head_stride, d);
         // columns rotated by the row: the fragment reads below touch all banks
-        sq[r * DP + ((d + 4 * r) & (DP - 1))] = x;
+        const int at = r * DP + ((d + 4 * r) & (DP - 1));
+        split_tf32(x, sq[at], sq[kRowsR * DP + at]);
       }
       __syncthreads();
     }
@@ -333,7 +333,9 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = gr + 8 * (e & 1), d = ks * 8 + tq + 4 * (e >> 1);
-            split_tf32_inf(sq[r * DP + ((d + 4 * r) & (DP - 1))], ah[e], al[e]);
+            const int at = r * DP + ((d + 4 * r) & (DP - 1));
+            ah[e] = sq[at];
+            al[e] = sq[kRowsR * DP + at];
           }
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
             for (int e = 0; e < 2; ++e) {
               const float x = *reinterpret_cast<const float*>(
                   sk_p + key * RB + (((2 * ks + e) ^ (key & 7)) << 4) + tq * 4);
-              split_tf32_inf(x, bh[e], bl[e]);
+              split_tf32(x, bh[e], bl[e]);
             }
             float part[4] = {};
             mma_tf32(part, al, bh[0], bh[1]);
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
               const int key = nt * 8 + 2 * tq + e, d = dt * 8 + gr;
               const float x = *reinterpret_cast<const float*>(
                   sv_p + key * RB + (((d >> 2) ^ (key & 7)) << 4) + (d & 3) * 4);
-              split_tf32_inf(x, bh[e], bl[e]);
+              split_tf32(x, bh[e], bl[e]);
             }
             float part[4] = {};
             mma_tf32(part, al, bh[0], bh[1]);
@@ -643,7 +645,8 @@ cudaError_t launch_combine(const AttnJob& job, int ctas, cudaStream_t s) {
 }
 
 // Which cut: a tile to a cluster of up to eight CTAs where that many tiles' clusters are
-// resident at once and no CTA takes more than kSplitBlocks blocks even if the table's positions
+// resident at once (with twice as many 11-node fp32 trees took 42 us instead of 35) and no CTA
+// takes more than kSplitBlocks blocks even if the table's positions
 // are all in use (the lengths are on the device).  Else the even work list, cut for
 // the CTAs that are resident (cut for two or four times as many, so that a CTA that is done
 // makes room for another, 64 requests of 4096 positions took 213 and 220 us instead of 204: the

@@ -85,24 +85,27 @@ struct PagedCommitJob {
   const int32_t* accept_len;
 };
 
-// A block takes one tree and some of its columns (every blocks_per_tree-th run of 256).  Its
-// first threads find the rows of up to kBatchMoves moves through the page table, once for all
-// columns; each thread then loads a column of every one of them before it stores any, so a
-// column's moves cost one latency.  What bounds it: the chain path -> page table -> row ->
-// store, about 2 us, until the rows themselves take longer.  Looking the rows up in every
-// thread (94 registers, a quarter of the threads resident) took 23.3 us instead of the time
-// in the design notes' table on 64 planes x 64 trees.
+constexpr int kPagedMoves = 4;    // moves of a batch
+constexpr int kPagedColumns = 2;  // columns a thread moves at once
+
+// A block takes one tree and some of its columns (every blocks_per_tree-th run).  Its first
+// threads find the rows of up to kPagedMoves moves through the page table, once for all
+// columns; each thread then loads two columns of every one of them before it stores any.  What
+// bounds it is latency, the chain path -> page table -> row -> store: so all blocks are
+// resident at once, and a thread has eight loads in flight.  64 planes x 64 trees of 2 KB rows:
+// 23.3 us where every thread looked its rows up (a quarter of the threads resident), 16.3 us with
+// one column at a time and 3.4 waves of blocks.
 __global__ void __launch_bounds__(kCommitThreads, 4) paged_commit_kernel(PagedCommitJob job) {
-  __shared__ int64_t src[kBatchMoves], dst[kBatchMoves];
+  __shared__ int64_t src[kPagedMoves], dst[kPagedMoves];
   const int b = blockIdx.x / job.blocks_per_tree, part = blockIdx.x % job.blocks_per_tree;
   const int a = min(job.accept_len[b], job.W - 1);
   const int64_t base = job.prefix_len[b];
   const int32_t* path = job.path + (int64_t)b * job.W;
-  for (int k0 = 1; k0 <= a; k0 += kBatchMoves) {
-    if (threadIdx.x < 2 * kBatchMoves) {
-      const int i = threadIdx.x % kBatchMoves, k = k0 + i;
+  for (int k0 = 1; k0 <= a; k0 += kPagedMoves) {
+    if (threadIdx.x < 2 * kPagedMoves) {
+      const int i = threadIdx.x % kPagedMoves, k = k0 + i;
       const int node = k < job.W ? path[k] : 0;  // (read beside accept_len, not after it)
-      const bool to = threadIdx.x >= kBatchMoves;
+      const bool to = threadIdx.x >= kPagedMoves;
       const int64_t t = base + (to ? k : node);
       int64_t at = -1;
       if (k <= a && node != k && t >= 0 && t <= SPEC_MAX_POSITIONS)
@@ -111,19 +114,29 @@ __global__ void __launch_bounds__(kCommitThreads, 4) paged_commit_kernel(PagedCo
       (to ? dst : src)[i] = at;
     }
     __syncthreads();
-    for (int item = part * kCommitThreads + threadIdx.x; item < job.items;
-         item += job.blocks_per_tree * kCommitThreads) {
-      const int row = job.by_vec.div(item), plane = job.by_head.div(row);
-      unsigned char* col = job.cache + plane * job.plane_stride +
-                           (row - plane * job.by_head.d) * job.head_stride +
-                           (int64_t)(item - row * job.by_vec.d) * 16;
-      uint4 x[kBatchMoves];
+    constexpr int kRun = kPagedColumns * kCommitThreads;
+    for (int run = part * kRun; run < job.items; run += job.blocks_per_tree * kRun) {
+      unsigned char* col[kPagedColumns];
+      uint4 x[kPagedColumns][kPagedMoves];
 #pragma unroll
-      for (int i = 0; i < kBatchMoves; ++i)
-        if (src[i] >= 0 && dst[i] >= 0) x[i] = *reinterpret_cast<const uint4*>(col + src[i]);
+      for (int c = 0; c < kPagedColumns; ++c) {
+        const int item = run + c * kCommitThreads + threadIdx.x;
+        const int row = job.by_vec.div(item), plane = job.by_head.div(row);
+        col[c] = item < job.items ? job.cache + plane * job.plane_stride +
+                                        (row - plane * job.by_head.d) * job.head_stride +
+                                        (int64_t)(item - row * job.by_vec.d) * 16
+                                  : nullptr;
 #pragma unroll
-      for (int i = 0; i < kBatchMoves; ++i)
-        if (src[i] >= 0 && dst[i] >= 0) *reinterpret_cast<uint4*>(col + dst[i]) = x[i];
+        for (int i = 0; i < kPagedMoves; ++i)
+          if (col[c] && src[i] >= 0 && dst[i] >= 0)
+            x[c][i] = *reinterpret_cast<const uint4*>(col[c] + src[i]);
+      }
+#pragma unroll
+      for (int c = 0; c < kPagedColumns; ++c)
+#pragma unroll
+        for (int i = 0; i < kPagedMoves; ++i)
+          if (col[c] && src[i] >= 0 && dst[i] >= 0)
+            *reinterpret_cast<uint4*>(col[c] + dst[i]) = x[c][i];
     }
     __syncthreads();
   }
@@ -174,10 +187,11 @@ extern "C" int spec_commit_accepted_path_paged(
   job.prefix_len = prefix_len;
   job.path = accepted_path;
   job.accept_len = accept_len;
-  // enough blocks to fill the GPU twice over, and no more than there are columns
-  const int runs = (job.items + kCommitThreads - 1) / kCommitThreads;
-  const int wanted = (device_sm_count() * 16 + B - 1) / B;
-  job.blocks_per_tree = runs < wanted ? runs : wanted;
+  // no more blocks than are resident at once, and than there are columns
+  const int run = kPagedColumns * kCommitThreads;
+  const int runs = (job.items + run - 1) / run;
+  const int share = device_sm_count() * 4 / B;
+  job.blocks_per_tree = share < 1 ? 1 : share < runs ? share : runs;
   const int64_t blocks = (int64_t)B * job.blocks_per_tree;
   if (blocks > 0x7fffffff) return SPEC_ERR_TOO_LARGE;
   paged_commit_kernel<<<(unsigned)blocks, kCommitThreads, 0,
