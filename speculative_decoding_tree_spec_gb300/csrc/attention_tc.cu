@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     const int tid = (warp & 3) * 32 + lane;  // 0 .. 127: the row within the half
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + w * 256, t_o = t_s + 128;
-    const float c = job.scale_log2;  // >= 0: the maximum is taken before the scaling
+    const float c = job.scale_log2;  // > 0: maximum and mask stand before the scaling
     const int boxes = kTcKB / box_rows, box_shift = 31 - __clz(box_rows);
     uint32_t blk = 0, seg = 0;  // blocks and segments of this half so far
 
@@ -862,9 +862,9 @@ int64_t tc_rows(const AttnJob& job) {
 }  // namespace
 
 // Few rows do not pay for 128-row products, a box of fewer than 8 rows does not fill a swizzle
-// group, and the maximum is taken before the scaling.
+// group, and the maximum is taken, and masked keys set to -inf, before the scaling.
 bool attn_tc_fits(const AttnJob& job, spec_dtype dtype) {
-  return dtype == SPEC_BF16 && job.scale_log2 >= 0.f && job.pd.size % 8 == 0 && job.n_pages > 0 &&
+  return dtype == SPEC_BF16 && job.scale_log2 > 0.f && job.pd.size % 8 == 0 && job.n_pages > 0 &&
          tc_rows(job) > kAttnRowsTile;
 }
 

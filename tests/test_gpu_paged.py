@@ -288,6 +288,45 @@ def test_other_streams():
     c.check(got)
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-6])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 50])
+def test_scales(scale, dtype, N):
+    c = Case([150, 90], N, 8, 2, 64, 16, dtype, seed=2, mask="tree")
+    c.scale = scale
+    c.check()
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (6, 2)])  # with and without a tensor map of the queries
+def test_shared_prefix_with_padding_and_strided_queries(hq, hkv):
+    N, B = 30, 4
+    c = Case([96, 100, 131, 96], N, hq, hkv, 64, 16, seed=5, mask="tree", shared=96,
+             counts=[N, 0, 1, N - 3])
+    c.check()
+    wide = torch.randn((N, B, hq + 3, 64), generator=torch.Generator().manual_seed(1)).to(BF)
+    c.q = wide.permute(1, 0, 2, 3)[:, :, 1:hq + 1]  # batches and nodes are no one direction
+    c.check()
+
+
+def test_a_captured_call_replays_on_new_lengths():
+    c = Case([150, 90, 0], 40, 8, 2, 64, 16, seed=2, mask="tree", pad_nan=False)
+    dev = [c.device(x) for x in (c.q, c.k, c.v, c.table, c.prefix, c.mask)]
+    out = {"out": torch.empty_like(dev[0]), "lse": torch.empty((3, 40, 8), device=DEV)}
+    ws = torch.empty(binding.tree_attention_workspace_size(3, 40, 8, 2, 64), dtype=torch.uint8,
+                     device=DEV)
+    call = lambda: binding.tree_attention_paged(*dev[:5], c.scale, mask=dev[5], workspace=ws, **out)
+    call()  # the kernels' one-time set-up stays out of the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for prefix in ([100, 3, 0], [150, 90, 0]):
+        c.prefix = np.array(prefix, dtype=np.int32)
+        dev[4].copy_(torch.as_tensor(c.prefix))
+        graph.replay()
+        c.check(out)
+
+
 def test_empty_calls():
     for B, N in ((0, 3), (2, 0)):
         q = torch.zeros((B, N, 4, 64), dtype=BF, device=DEV)
