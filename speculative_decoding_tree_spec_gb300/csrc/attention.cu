@@ -70,13 +70,15 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 // keys with its own copies in flight, its own m, l and o, so no barrier stands in the loop;
 // the four are joined at the end of the tile.  The products are warp-level matrix
 // instructions: at 16 rows the keys' bytes, not the products, set the time.  fp32 inputs are
-// split into two tf32 parts each.
-// ---------------------------------------------------------------------------------------
+// split into two tf32 parts each.  64 requests of 1 to 8192 positions, one token each (1.07 GB):
+// 197 us and 6 us for the join, 5.4 TB/s; deeper or earlier copies, cache layouts with a head's
+// positions together and page numbers read further ahead change nothing in that.
 //
 // Two ways to cut the work.  SPLIT = false: the work list of attention.cuh, even whatever the
 // lengths are, with the join in a second kernel.  SPLIT = true, for few or short tiles (see
 // launch_rows): a cluster of CTAs takes one tile, each an equal run of its blocks, and joins
 // the parts through distributed shared memory: no work list, no second launch.
+// ---------------------------------------------------------------------------------------
 template <typename T, int DP>
 struct RowsCfg {
   static constexpr int kRowBytes = DP * (int)sizeof(T);
@@ -646,11 +648,35 @@ cudaError_t launch_combine(const AttnJob& job, int ctas, cudaStream_t s) {
 
 // Which cut: a tile to a cluster of up to eight CTAs where that many tiles' clusters are
 // resident at once (with twice as many 11-node fp32 trees took 42 us instead of 35) and no CTA
-// takes more than kSplitBlocks blocks even if the table's positions
-// are all in use (the lengths are on the device).  Else the even work list, cut for
-// the CTAs that are resident (cut for two or four times as many, so that a CTA that is done
-// makes room for another, 64 requests of 4096 positions took 213 and 220 us instead of 204: the
-// starts and the parts to join cost more than the even finish gives).
+// takes more than kSplitBlocks blocks even if the table's positions are all in use (the lengths
+// are on the device).  Else the even work list, cut for the CTAs that are resident (cut for
+// two or four times as many, so that a CTA that is done makes room for another, 64 requests of
+// 4096 positions took 213 and 220 us instead of 204: the starts and the parts to join cost
+// more than the even finish gives).  Returns the CTAs of a cluster, 0 for the list.
+int64_t rows_tiles(const AttnJob& job) {
+  const int64_t rows = job.phase == kShared ? (int64_t)job.B * job.N * job.G : (int64_t)job.N * job.G;
+  return (rows + kRowsR - 1) / kRowsR * (job.phase == kShared ? 1 : job.B) * job.Hkv;
+}
+int rows_split(const AttnJob& job, int resident) {
+  const int64_t tiles = rows_tiles(job);
+  const int64_t positions = job.phase == kShared
+                                ? job.shared_len
+                                : (int64_t)job.max_pages * job.pd.size - job.shared_len;
+  int split = kMaxSplit;
+  while (split > 1 && tiles * split > resident) split /= 2;
+  return (positions + kRowsKB - 1) / kRowsKB <= (int64_t)kSplitBlocks * split && tiles <= 0x7fffffff
+             ? split
+             : 0;
+}
+// bf16 calls whose rows the tensor-memory kernel could take, but which are one wave of
+// clusters here: one short launch instead of a long one and a join.  One request of 1000 positions
+// with 20 to 104 rows: 24 us a call instead of 27 to 30 (most of it the host's); 64 requests of
+// 2000, which are no such wave: 208 to 782 us instead of 121 to 129.
+bool rows_one_wave(const AttnJob& job) {
+  const int resident = device_sm_count() * RowsCfg<uint16_t, 128>::kCtasPerSm;
+  return rows_tiles(job) <= resident && rows_split(job, resident) > 0;
+}
+
 template <typename T, int DP>
 cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
   using Cfg = RowsCfg<T, DP>;
@@ -672,14 +698,10 @@ cudaError_t launch_rows(AttnJob job, cudaStream_t s) {
   job.entries = job.phase == kShared ? job.row_tiles : job.row_tiles * job.B;
   job.by_tiles = FastDiv::make(job.row_tiles);
   const int resident = device_sm_count() * Cfg::kCtasPerSm;
-  const int64_t tiles = (int64_t)job.entries * job.Hkv;
-  const int64_t positions = job.phase == kShared ? job.shared_len
-                                                 : (int64_t)job.max_pages * job.pd.size - job.shared_len;
-  int split = kMaxSplit;
-  while (split > 1 && tiles * split > resident) split /= 2;
-  if ((positions + kRowsKB - 1) / kRowsKB <= (int64_t)kSplitBlocks * split && tiles <= 0x7fffffff) {
+  const int split = rows_split(job, resident);
+  if (split > 0) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.gridDim = dim3((unsigned)(rows_tiles(job) * split));
     cfg.blockDim = dim3(kRowsThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.stream = s;
@@ -832,7 +854,7 @@ extern "C" int spec_tree_attention_paged(
     job.phase = phase;
     cudaError_t e = cudaSuccess;
     bool taken = false;
-    if (attn_tc_fits(job, dtype)) e = launch_attn_tc(job, s, &taken);
+    if (attn_tc_fits(job, dtype) && !rows_one_wave(job)) e = launch_attn_tc(job, s, &taken);
     if (e != cudaSuccess) return SPEC_ERR_CUDA;
     if (taken) continue;
     if (dtype == SPEC_BF16)

@@ -52,6 +52,8 @@ def _tree_masks(rng, B, N):
 
 
 class Case:
+    room = 0  # positions every table row has columns for at least
+
     def __init__(self, prefix, N, hq=4, hkv=2, d=64, page=16, dtype=BF, seed=0, mask=None,
                  counts=None, shared=0, spread=2.0, heads_first=False, pad_nan=True):
         rng = np.random.default_rng(seed)
@@ -59,6 +61,9 @@ class Case:
         B = len(prefix)
         prefix = np.asarray(prefix, dtype=np.int32)
         self.table, pool = _table(rng, prefix + N, page)
+        more = -(-self.room // page) - self.table.shape[1]
+        if more > 0:
+            self.table = np.pad(self.table, ((0, 0), (0, more)), constant_values=-1)
         if shared:
             self.table[:, :shared // page] = self.table[0, :shared // page]
         shape = (pool, hkv, page, d) if heads_first else (pool, page, hkv, d)
@@ -115,6 +120,13 @@ class Case:
         assert np.array_equal(np.isnan(got_lse), np.isnan(lse))
         assert (np.abs(got_lse - lse) <= d + (L + 8) * E + 4 * E * np.abs(lse))[some].all()
         return got
+
+
+@pytest.fixture(autouse=True, params=[0, 5000], ids=["tight", "roomy"])
+def _room(request, monkeypatch):
+    """A short table lets a call of few tiles go to clusters of the few-rows kernel; a table
+    with room for thousands of positions does not, whatever the lengths are."""
+    monkeypatch.setattr(Case, "room", request.param)
 
 
 HEADS = [(4, 4, 64), (8, 2, 128), (8, 1, 64), (6, 3, 96), (2, 1, 8), (32, 8, 128), (5, 1, 104)]
@@ -297,11 +309,12 @@ def test_scales(scale, dtype, N):
     c.check()
 
 
+@pytest.mark.parametrize("shared", [96, 4608])
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (6, 2)])  # with and without a tensor map of the queries
-def test_shared_prefix_with_padding_and_strided_queries(hq, hkv):
+def test_shared_prefix_with_padding_and_strided_queries(hq, hkv, shared):
     N, B = 30, 4
-    c = Case([96, 100, 131, 96], N, hq, hkv, 64, 16, seed=5, mask="tree", shared=96,
-             counts=[N, 0, 1, N - 3])
+    c = Case([shared, shared + 4, shared + 35, shared], N, hq, hkv, 64, 16, seed=5, mask="tree",
+             shared=shared, counts=[N, 0, 1, N - 3])
     c.check()
     wide = torch.randn((N, B, hq + 3, 64), generator=torch.Generator().manual_seed(1)).to(BF)
     c.q = wide.permute(1, 0, 2, 3)[:, :, 1:hq + 1]  # batches and nodes are no one direction
