@@ -433,6 +433,7 @@ int spec_paged_append_rope(const void* q, spec_node_layout q_layout, void* out_q
  *   the result is rounded once.
  * workspace: device, 256-byte aligned, spec_tree_attention_workspace_size() bytes; not
  *   initialised by the caller, not preserved between calls.
+ * A device-side wait that gives up (2 s) makes the results it concerns NaN.
  * Bases and strides are multiples of 16 bytes and head_dim of 16 bytes, head_dim <=
  * SPEC_ATTN_MAX_HEAD_DIM.  Asynchronous on `stream`; allocates nothing.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED_DTYPE, SPEC_ERR_MISALIGNED,
