@@ -414,8 +414,9 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
           const bool drafts = pos0 + kTcKB > t.clear;  // rows may differ in what they see
           uint32_t sees[4];
           if (drafts || bad) {
-            // bit k of word j: this row sees key 32 j + k of the block
-            const int lim = min(t.prefix, t.kend) - pos0;
+            // bit k of word j: this row sees key 32 j + k of the block; at first those that every
+            // row sees (without a mask the first drafts are among them)
+            const int lim = t.clear - pos0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int n = min(max(lim - 32 * j, 0), 32);
