@@ -57,7 +57,10 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 // each step of 8 starts from 0 and is added to the running sums in fp32.
 //
 // hi is x cut to tf32's 10 bits, lo the rest rounded to as many.  An infinite x gives hi = x and
-// a finite lo (the minimum with a bound that no finite x's lo reaches drops inf - inf).
+// a finite lo (the minimum with a bound that no finite x's lo reaches drops inf - inf), and a NaN
+// whose payload lies in the cut bits looks like an infinity.  The cross products with an infinite
+// hi are NaN where the other operand's lo is 0, so a result that is not finite is taken again
+// without the split: plain_score, take_nonfinite.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;
   const float rest = fminf(x - __uint_as_float(hi), 0x1p117f);
@@ -133,6 +136,51 @@ __device__ __forceinline__ void join_part(float& m, float& l, float (&o)[C], flo
 #pragma unroll
   for (int i = 0; i < C; ++i) o[i] = o[i] * a + x[i] * b;
   m = mn;
+}
+
+// q . k without the split, for scores that are not finite: k in shared memory, its 16-byte units
+// swizzled by the key's number.
+static __device__ __noinline__ float plain_score(const float* q, const unsigned char* k, int key,
+                                                 int D) {
+  float s = 0.f;
+  for (int d = 0; d < D; ++d)
+    s = fmaf(q[d], *reinterpret_cast<const float*>(k + (((d >> 2) ^ (key & 7)) << 4) + (d & 3) * 4),
+             s);
+  return s;
+}
+
+// The columns of o that are not finite, from the positions [from, to), which all rows of the tile
+// see: where values among them are infinite or NaN, their sum is the result, whatever their
+// weights are.  (Else the column is left: scores that are NaN, or an overflow.)
+template <int C>
+static __device__ __noinline__ void take_nonfinite(const AttnJob& job, const AttnTile& t, int head,
+                                                   int from, int to, int c0, float* o) {
+  const int32_t* row = job.table + (int64_t)t.b * job.max_pages;
+  float sum[C];
+  unsigned odd = 0, found = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    sum[i] = 0.f;
+    if (!(fabsf(o[i]) < CUDART_INF_F) && c0 + i < job.D) odd |= 1u << i;
+  }
+  for (int pos = from; pos < to; ++pos) {
+    const int64_t off = paged_offset(row, job.max_pages, job.n_pages, job.pd, job.page_stride,
+                                     job.pos_stride, pos);
+    if (off < 0) continue;
+    const float* v = static_cast<const float*>(job.v) + off + head * job.head_stride + c0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if (!((odd >> i) & 1u)) continue;
+      const float x = v[i];
+      if (!(fabsf(x) < CUDART_INF_F)) {
+        sum[i] += x;
+        found |= 1u << i;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if ((found >> i) & 1u) o[i] = sum[i];
 }
 
 template <typename T, int DP, bool SPLIT>
@@ -357,6 +405,23 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
             for (int e = 0; e < 4; ++e) s[nt][e] += part[e];
           }
         }
+        bool odd = false;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) odd |= !(fabsf(s[nt][e]) < CUDART_INF_F);
+        if (odd) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = nt * 8 + 2 * tq + (e & 1);
+              if (real[e >> 1] && !(fabsf(s[nt][e]) < CUDART_INF_F))
+                s[nt][e] = plain_score(reinterpret_cast<const float*>(qrow[e >> 1]),
+                                       sk_p + key * RB, key, job.D);
+            }
+        }
+        __syncwarp();
       }
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
@@ -485,6 +550,12 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(AttnJob job) {
       lt += a * sm[(kRowsWarps + w) * kRowsR + r];
 #pragma unroll
       for (int i = 0; i < C; ++i) ot[i] += a * so[(w * kRowsR + r) * OP + c0 + i];
+    }
+    if (F32) {
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < C; ++i) odd |= !(fabsf(ot[i]) < CUDART_INF_F);
+      if (odd) take_nonfinite<C>(job, t, head, seg0, min(seg1, t.clear), c0, ot);
     }
     if (poison) {
       int b, n, g;
