@@ -96,9 +96,10 @@ def commit(cache, table, prefix_len, accepted_path, accept_len):
     out = np.array(cache, copy=True)
     n_pages, page_size = out.shape[1:3]
     for b in range(len(prefix_len)):
+        pre = max(int(prefix_len[b]), 0)
         for k in range(1, int(accept_len[b]) + 1):
-            src = slot(table[b], n_pages, page_size, int(prefix_len[b]) + int(accepted_path[b][k]))
-            dst = slot(table[b], n_pages, page_size, int(prefix_len[b]) + k)
+            src = slot(table[b], n_pages, page_size, pre + int(accepted_path[b][k]))
+            dst = slot(table[b], n_pages, page_size, pre + k)
             if src is not None and dst is not None:
                 out[:, dst[0], dst[1]] = out[:, src[0], src[1]]
     return out

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kCommitThreads, 4) paged_commit_kernel(PagedCo
   __shared__ int64_t src[kPagedMoves], dst[kPagedMoves];
   const int b = blockIdx.x / job.blocks_per_tree, part = blockIdx.x % job.blocks_per_tree;
   const int a = min(job.accept_len[b], job.W - 1);
-  const int64_t base = job.prefix_len[b];
+  const int64_t base = max(job.prefix_len[b], 0);  // as the append that stored the nodes
   const int32_t* path = job.path + (int64_t)b * job.W;
   for (int k0 = 1; k0 <= a; k0 += kPagedMoves) {
     if (threadIdx.x < 2 * kPagedMoves) {
