@@ -438,8 +438,8 @@ int spec_paged_append_rope(const void* q, spec_node_layout q_layout, void* out_q
  * SPEC_ATTN_MAX_HEAD_DIM.  Asynchronous on `stream`; allocates nothing.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED_DTYPE, SPEC_ERR_MISALIGNED,
  * SPEC_ERR_WORKSPACE, SPEC_ERR_TOO_LARGE (head_dim, B * N * n_q_heads >= 2^30, max_pages *
- * page_size above SPEC_MAX_POSITIONS), SPEC_ERR_CUDA.  The size function returns 0 for
- * invalid sizes.
+ * page_size or shared_len above SPEC_MAX_POSITIONS), SPEC_ERR_CUDA.  The size function returns
+ * 0 for invalid sizes.
  */
 size_t spec_tree_attention_workspace_size(int32_t B, int32_t N, int32_t n_q_heads,
                                           int32_t n_kv_heads, int32_t head_dim,

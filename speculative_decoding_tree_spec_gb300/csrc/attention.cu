@@ -848,7 +848,9 @@ extern "C" size_t spec_tree_attention_workspace_size(int32_t B, int32_t N, int32
                                                      int32_t n_kv_heads, int32_t head_dim,
                                                      int32_t shared_len, spec_dtype dtype) {
   if (!attn_sizes_ok(B, N, n_q_heads, n_kv_heads, head_dim, shared_len)) return 0;
-  if (head_dim > SPEC_ATTN_MAX_HEAD_DIM || (int64_t)B * N * n_q_heads > 0x3fffffff) return 0;
+  if (head_dim > SPEC_ATTN_MAX_HEAD_DIM || (int64_t)B * N * n_q_heads > 0x3fffffff ||
+      shared_len > SPEC_MAX_POSITIONS)
+    return 0;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return 0;
   return attn_ws((int64_t)B * N, n_q_heads, head_dim, shared_len).total;
 }
@@ -866,7 +868,9 @@ extern "C" int spec_tree_attention_paged(
   if (!attn_sizes_ok(B, N, n_q_heads, cache.n_kv_heads, cache.head_dim, shared_len) ||
       shared_len % cache.page_size != 0 || !(fabsf(scale) <= FLT_MAX))
     return SPEC_ERR_INVALID_ARG;
-  if (cache.head_dim > SPEC_ATTN_MAX_HEAD_DIM || (int64_t)B * N * n_q_heads > 0x3fffffff)
+  // (the kernels add up to a few blocks to a position in 32 bits)
+  if (cache.head_dim > SPEC_ATTN_MAX_HEAD_DIM || (int64_t)B * N * n_q_heads > 0x3fffffff ||
+      shared_len > SPEC_MAX_POSITIONS)
     return SPEC_ERR_TOO_LARGE;
   if (B == 0 || N == 0) return SPEC_OK;
   if (!q || !k_cache || !v_cache || !page_table || !prefix_len || !out || !workspace)
