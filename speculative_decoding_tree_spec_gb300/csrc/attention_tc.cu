@@ -94,6 +94,13 @@ struct TcWait {
   }
 };
 
+// The softmax warps of a tile's halves meet.  A number for each count of threads: after a wait that
+// gave up, a half may be in a later tile than the other.
+template <int NUMBER, int THREADS>
+__device__ __forceinline__ void half_barrier() {
+  asm volatile("bar.sync %0, %1;\n" ::"n"(NUMBER), "n"(THREADS) : "memory");
+}
+
 template <int DP, int H>
 __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -554,7 +561,8 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
               if (x < kn * CPR) *((volatile int*)&sh.poison) = 1;
             }
             fence_proxy_async_smem();
-            asm volatile("bar.sync 2, %0;\n" ::"r"(halves * kTcHalf) : "memory");
+            if (halves == 2) half_barrier<3, 2 * kTcHalf>();
+            else half_barrier<2, kTcHalf>();
           }
           const float mc = m == -CUDART_INF_F ? 0.f : m * c;
           const float2 c2 = make_float2(c, c), n2 = make_float2(-mc, -mc);
