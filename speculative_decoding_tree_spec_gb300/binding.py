@@ -447,8 +447,23 @@ def _int32(t, shape, dev: int, what):
     return t.data_ptr()
 
 
-def _paged_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+def _elsewhere(stream, dev: int):
+    """A context that makes `stream` (None: device `dev`'s current one) and device `dev` current, or
+    None where they are.  Under it, what a call allocates belongs to the stream that its kernels
+    run on, and the kernels start on the device that holds their data."""
+    on_device = torch._C._cuda_getDevice() == dev
+    if stream is None:
+        return None if on_device else torch.cuda.device(dev)
+    raw = int(stream.cuda_stream)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"the stream belongs to device {stream.device_index}, the tensors to {dev}")
+    else:
+        stream = (torch.cuda.ExternalStream(raw, device=dev) if raw
+                  else torch.cuda.default_stream(dev))
+    if on_device and raw == torch._C._cuda_getCurrentRawStream(dev):
+        return None
+    return torch.cuda.stream(stream)
 
 
 def _paged_cache(k_cache: torch.Tensor, v_cache: torch.Tensor):
@@ -498,8 +513,15 @@ def paged_append_rope(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
     (default n; the position_ids of tree_build for a draft tree).  cos_sin [n_positions,
     rot_dim] float32: the cosines, then the sines (None: no rotation).  counts [B] int32:
     tokens n >= counts[b] are padding.  Returns the rotated queries (out_q, or a new tensor;
-    None if q is None)."""
+    None if q is None).  With `stream` given, the call runs and allocates as under
+    torch.cuda.stream(stream), and what is on another stream has to be ordered as there."""
     cache, dtype, dev = _paged_cache(k_cache, v_cache)
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return paged_append_rope(q, k, v, k_cache, v_cache, page_table, prefix_len, cos_sin,
+                                     position_ids=position_ids, counts=counts,
+                                     interleaved=interleaved, out_q=out_q)
     B, N = k.shape[:2]
     D = cache.head_dim
     lk, hk = _nodes(k, dtype, dev, B, N, D, "k")
@@ -533,7 +555,7 @@ def paged_append_rope(q, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
         _int32(prefix_len, (B,), dev, "prefix_len"), _int32(counts, (B,), dev, "counts"),
         _int32(position_ids, (B, N), dev, "position_ids"),
         None if cos_sin is None else cos_sin.data_ptr(), n_positions, rot,
-        SPEC_ROPE_INTERLEAVED if interleaved else 0, _paged_stream(stream, dev))
+        SPEC_ROPE_INTERLEAVED if interleaved else 0, torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise SpecError(rc, "spec_paged_append_rope")
     return out_q
@@ -555,8 +577,15 @@ def tree_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     before the tree and the drafts j with mask[b, n, j] != 0 (mask [B, N, N] uint8 as tree_build
     gives it; None: j <= n, which is decoding at N = 1 and a prompt otherwise).  scale defaults
     to head_dim ** -0.5.  shared_len: positions that all sequences share, read once.  Returns
-    {"out": [B, N, heads, head_dim], "lse": [B, N, heads] float32 natural logarithm}."""
+    {"out": [B, N, heads, head_dim], "lse": [B, N, heads] float32 natural logarithm}.  `stream` as
+    in paged_append_rope."""
     cache, dtype, dev = _paged_cache(k_cache, v_cache)
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return tree_attention_paged(q, k_cache, v_cache, page_table, prefix_len, scale, mask=mask,
+                                        counts=counts, shared_len=shared_len, out=out, lse=lse,
+                                        workspace=workspace)
     B, N, H, D = q.shape
     if D != cache.head_dim:
         raise ValueError("q and the caches must share head_dim")
@@ -589,7 +618,7 @@ def tree_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         _int32(prefix_len, (B,), dev, "prefix_len"), _int32(counts, (B,), dev, "counts"),
         None if mask is None else mask.data_ptr(), int(shared_len),
         D ** -0.5 if scale is None else scale, out.data_ptr(), lo, lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _paged_stream(stream, dev))
+        workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise SpecError(rc, "spec_tree_attention_paged")
     return {"out": out, "lse": lse}
@@ -609,6 +638,11 @@ def commit_accepted_path_paged(cache: torch.Tensor, page_table: torch.Tensor,
                          "contiguous head vectors")
     if dev < 0:
         raise ValueError("the cache must be on a CUDA device")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return commit_accepted_path_paged(cache, page_table, prefix_len, accepted_path,
+                                              accept_len)
     P, n_pages, page_size, H, D = shape
     if st[3] == D:  # heads side by side: one wider row
         H, D = 1, H * D
@@ -619,7 +653,7 @@ def commit_accepted_path_paged(cache: torch.Tensor, page_table: torch.Tensor,
         0 if H == 1 else st[3] * es, D * es, _int32(page_table, (B, max_pages), dev, "page_table"),
         max_pages, _int32(prefix_len, (B,), dev, "prefix_len"),
         _int32(accepted_path, (B, W), dev, "accepted_path"),
-        _int32(accept_len, (B,), dev, "accept_len"), W, _paged_stream(stream, dev))
+        _int32(accept_len, (B,), dev, "accept_len"), W, torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise SpecError(rc, "spec_commit_accepted_path_paged")
 
