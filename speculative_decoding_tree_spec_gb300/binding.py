@@ -611,6 +611,8 @@ def tree_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if workspace is None:
         ws = L.spec_tree_attention_workspace_size(B, N, H, cache.n_kv_heads, D, shared_len, dt)
         workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on the cache's device")
     max_pages = page_table.shape[-1]
     rc = L.spec_tree_attention_paged(
         q.data_ptr(), lq, k_cache.data_ptr(), v_cache.data_ptr(), cache, dt, B, N, H,
@@ -618,7 +620,8 @@ def tree_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         _int32(prefix_len, (B,), dev, "prefix_len"), _int32(counts, (B,), dev, "counts"),
         None if mask is None else mask.data_ptr(), int(shared_len),
         D ** -0.5 if scale is None else scale, out.data_ptr(), lo, lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), torch._C._cuda_getCurrentRawStream(dev))
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise SpecError(rc, "spec_tree_attention_paged")
     return {"out": out, "lse": lse}

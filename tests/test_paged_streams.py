@@ -16,7 +16,7 @@ class FakeStream:
 class FakeTensor:
     def __init__(self, shape, dtype, dev, made_on=None, strides=None):
         self.shape, self.dtype, self.dev, self.made_on = torch.Size(shape), dtype, dev, made_on
-        self.device = torch.device("cuda", dev)
+        self.device = torch.device("cuda", dev) if dev >= 0 else torch.device("cpu")
         self._strides = tuple(torch.empty(shape, device="meta").stride()) if strides is None else strides
 
     def stride(self):
