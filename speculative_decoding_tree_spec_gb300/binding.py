@@ -8,6 +8,8 @@ fails loudly otherwise -- there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 
@@ -191,6 +193,45 @@ def _stream_ptr(stream) -> int:
     return int(s.cuda_stream)
 
 
+def _elsewhere(stream, dev: int):
+    """A context that makes `stream` (None: device `dev`'s current one) and device `dev` current, or
+    None where they are.  Under it, what a call allocates belongs to the stream that its kernels
+    run on, and the kernels start on the device that holds their data."""
+    on_device = torch._C._cuda_getDevice() == dev
+    if stream is None:
+        return None if on_device else torch.cuda.device(dev)
+    raw = int(stream.cuda_stream)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"the stream belongs to device {stream.device_index}, the tensors to {dev}")
+    else:
+        stream = (torch.cuda.ExternalStream(raw, device=dev) if raw
+                  else torch.cuda.default_stream(dev))
+    if on_device and raw == torch._C._cuda_getCurrentRawStream(dev):
+        return None
+    return torch.cuda.stream(stream)
+
+
+def _on_stream(f):
+    """A call whose allocations, and copies of its results, belong to its argument `stream`."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        there = None if stream is None else _elsewhere(stream, _stream_device(stream))
+        if there is None:
+            return f(*args, **kw)
+        with there:
+            return f(*args, **kw)
+
+    return call
+
+
+def _stream_device(stream) -> int:
+    return stream.device_index if isinstance(stream, torch.cuda.Stream) else torch._C._cuda_getDevice()
+
+
 def workspace_size(B: int, N: int, V: int, dtype=torch.bfloat16) -> int:
     code = SPEC_BF16 if dtype == torch.bfloat16 else SPEC_F32
     return int(lib().spec_verify_workspace_size(B, N, V, code))
@@ -210,6 +251,7 @@ def _row_layout(t: torch.Tensor, B: int, N: int, V: int, broadcast: bool):
     return t.stride(1), t.stride(0)
 
 
+@_on_stream
 def verify_tree(p: torch.Tensor, q, draft_tokens: torch.Tensor, parent_idx: torch.Tensor,
                 max_depth: int, temperature: float, top_k: int = 0, top_p: float = 1.0,
                 seed: int = 0, offset: int = 0, flags: int = 0, *, batch_broadcast: bool = False,
@@ -263,6 +305,7 @@ def verify_tree(p: torch.Tensor, q, draft_tokens: torch.Tensor, parent_idx: torc
     return out
 
 
+@_on_stream
 def verify_tree_per_request(p: torch.Tensor, q: torch.Tensor, draft_tokens: torch.Tensor,
                             parent_idx: torch.Tensor, max_depth: int, temperature: torch.Tensor,
                             top_k=None, top_p=None, seed: int = 0, offset: int = 0,
@@ -353,6 +396,7 @@ def verify_tree_noalloc(p: torch.Tensor, q, draft_tokens: torch.Tensor, parent_i
     return out
 
 
+@_on_stream
 def verify_tree_fused_lmhead(features: torch.Tensor, weight: torch.Tensor, q,
                              draft_tokens: torch.Tensor, parent_idx: torch.Tensor, max_depth: int,
                              temperature: float, top_k: int = 0, top_p: float = 1.0,
@@ -445,25 +489,6 @@ def _int32(t, shape, dev: int, what):
         raise TypeError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on the "
                         "cache's device")
     return t.data_ptr()
-
-
-def _elsewhere(stream, dev: int):
-    """A context that makes `stream` (None: device `dev`'s current one) and device `dev` current, or
-    None where they are.  Under it, what a call allocates belongs to the stream that its kernels
-    run on, and the kernels start on the device that holds their data."""
-    on_device = torch._C._cuda_getDevice() == dev
-    if stream is None:
-        return None if on_device else torch.cuda.device(dev)
-    raw = int(stream.cuda_stream)
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device_index != dev:
-            raise ValueError(f"the stream belongs to device {stream.device_index}, the tensors to {dev}")
-    else:
-        stream = (torch.cuda.ExternalStream(raw, device=dev) if raw
-                  else torch.cuda.default_stream(dev))
-    if on_device and raw == torch._C._cuda_getCurrentRawStream(dev):
-        return None
-    return torch.cuda.stream(stream)
 
 
 def _paged_cache(k_cache: torch.Tensor, v_cache: torch.Tensor):
@@ -661,6 +686,7 @@ def commit_accepted_path_paged(cache: torch.Tensor, page_table: torch.Tensor,
         raise SpecError(rc, "spec_commit_accepted_path_paged")
 
 
+@_on_stream
 def draft_topk(logits: torch.Tensor, k: int, temperature: float = 1.0, stream=None) -> dict:
     """spec_draft_topk on [R, V] device rows (row pitch from the tensor's stride):
     tokens [R, k] int32, probs [R, k] float32, status [R] int32."""
@@ -680,6 +706,7 @@ def draft_topk(logits: torch.Tensor, k: int, temperature: float = 1.0, stream=No
     return out
 
 
+@_on_stream
 def draft_topk_fused_lmhead(features: torch.Tensor, weight: torch.Tensor, k: int,
                             temperature: float = 1.0, want_logits: bool = False, workspace=None,
                             stream=None) -> dict:
@@ -714,6 +741,7 @@ def draft_topk_fused_lmhead(features: torch.Tensor, weight: torch.Tensor, k: int
     return out
 
 
+@_on_stream
 def tree_expand_topk(cand_parent: torch.Tensor, cand_prob: torch.Tensor, layer_begin: int,
                      layer_end: int, k: int, stream=None) -> torch.Tensor:
     """spec_tree_expand_topk: [B, k] int32 candidate numbers to expand next."""
@@ -726,6 +754,7 @@ def tree_expand_topk(cand_parent: torch.Tensor, cand_prob: torch.Tensor, layer_b
     return out
 
 
+@_on_stream
 def tree_build(cand_parent: torch.Tensor, cand_token: torch.Tensor, cand_prob: torch.Tensor,
                root_token: torch.Tensor, m: int, stream=None) -> dict:
     """spec_tree_build: the flattened draft (tokens, parent_idx, position_ids, src, mask,
@@ -752,6 +781,7 @@ def tree_build(cand_parent: torch.Tensor, cand_token: torch.Tensor, cand_prob: t
     return out
 
 
+@_on_stream
 def verify_tree_host(p_host: torch.Tensor, q_host, tokens_host: torch.Tensor,
                      parents_host: torch.Tensor, max_depth: int, temperature: float,
                      top_k: int = 0, top_p: float = 1.0, seed: int = 0, offset: int = 0,
@@ -778,6 +808,7 @@ def verify_tree_host(p_host: torch.Tensor, q_host, tokens_host: torch.Tensor,
     return host
 
 
+@_on_stream
 def filter_rows(logits: torch.Tensor, temperature: float, top_k: int = 0, top_p: float = 1.0,
                 flags: int = 0, stream=None):
     """spec_filter_rows on a [R, V] device tensor.  Returns a dict of device tensors
@@ -804,6 +835,7 @@ def filter_rows(logits: torch.Tensor, temperature: float, top_k: int = 0, top_p:
     }
 
 
+@_on_stream
 def philox_words(seed: int, offset: int, b_idx: torch.Tensor, node_idx: torch.Tensor, stream=None):
     """[n, 4] int64 tensor of the Philox words for (seed, offset, b_idx[i], node_idx[i])."""
     n = b_idx.numel()
@@ -820,6 +852,7 @@ class PreparedVerify:
     """A spec_verify_tree_phases call with every argument fixed (device tensors
     allocated once), for loops that call the same verify step many times."""
 
+    @_on_stream
     def __init__(self, p, q, draft_tokens, parent_idx, max_depth, temperature, top_k=0,
                  top_p=1.0, seed=0, offset=0, flags=0, batch_broadcast=False, stream=None,
                  per_request=None):
@@ -844,6 +877,7 @@ class PreparedVerify:
         ws_bytes = int(lib().spec_verify_workspace_size(B, N, V, dt))
         self.workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
         self._keep = (p, q, draft_tokens, parent_idx, per_request)
+        self._stream = torch.cuda.current_stream() if stream is None else stream
         if per_request is not None:
             T_r, k_r, p_r = per_request
             self._fn = lib().spec_verify_tree_per_request
@@ -877,6 +911,10 @@ class PreparedVerify:
 
     def read_counters(self) -> dict:
         """Run the whole step once more with the work counters requested; returns them."""
+        return self._read_counters(stream=self._stream)
+
+    @_on_stream
+    def _read_counters(self, stream) -> dict:
         rc = self._fn(SPEC_PHASE_ALL, *self._counter_args)
         if rc != 0:
             raise SpecError(rc, "spec_verify_tree_phases")
