@@ -132,8 +132,6 @@ cudaError_t launch_philox_words(uint64_t seed, uint64_t offset, const int32_t* b
                                 const int32_t* node_idx, int32_t n, uint32_t* out,
                                 cudaStream_t s);
 int device_sm_count();
-// Host checks of a paged cache's sizes (append.cu): SPEC_OK or an error code.
-int check_paged_layout(const spec_paged_layout& l, int32_t max_pages);
 
 // Fused LM head (lmhead.cu): bytes of the per-(row, column tile) statistics, and the
 // launch of the GEMM + statistics kernel and of the combine kernel that writes the

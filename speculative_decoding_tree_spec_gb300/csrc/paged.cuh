@@ -48,4 +48,7 @@ __device__ __forceinline__ int64_t paged_offset(const int32_t* table_row, int ma
   return (int64_t)page * page_stride + (int64_t)(t - at * pd.size) * pos_stride;
 }
 
+// Host checks of a paged cache's sizes (append.cu): SPEC_OK or an error code.
+int check_paged_layout(const spec_paged_layout& l, int32_t max_pages);
+
 }  // namespace svk
