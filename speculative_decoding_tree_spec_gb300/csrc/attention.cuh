@@ -14,8 +14,9 @@
 // the positions all sequences share, for the rows of all sequences at once (row r = (b * N +
 // node) * G + g).  With shared positions kOwn leaves a normalised fp32 result that kShared
 // joins with its own: the shared tiles are the long ones, beside which the join costs least
-// (the join in the short own tiles made the own part of 256 x 26-node trees on 16 to 400
-// positions 212 us instead of 163, and the shared part 45 us shorter).
+// (in the first measurement of both orders the join in the short own tiles made the own part of
+// 256 x 26-node trees on 16 to 400 positions 212 us instead of 163, and the shared part 45 us
+// shorter; the own part takes 140 us now, 131 and its join of cut tiles).
 #pragma once
 
 #include <cuda_bf16.h>

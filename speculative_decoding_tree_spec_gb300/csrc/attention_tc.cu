@@ -17,10 +17,12 @@
 // P goes over their place, so that the lower 64 can be read a second time and no thread needs
 // more than about 128 registers for them.
 // (Blocks of 64 keys with two score buffers per half, which take the scores off that chain,
-// were slower: a 128 x 64 product takes the tensor cores as long as a 128 x 128 one.  So were a
-// fixed reference in the maximum's place and a part of the exponentials by polynomial: what
-// bounds the kernel is issue and latency in that chain.  26624 rows of 8192 shared positions,
-// 893 GFLOP: 702 us with the join of the own part, 1272 TFLOP/s, 68 % of the measured rate.)
+// were slower: a 128 x 64 product takes the tensor cores as long as a 128 x 128 one.  A fixed
+// reference in the maximum's place was no faster, a part of the exponentials by polynomial
+// slower.  What bounds the kernel is latency in that chain: with two softmax warps per
+// scheduler, each thread alone with its row, the issue slots are 33 % and the tensor pipe 45 %
+// active (6656 rows of 4096 positions).  26624 rows of 8192 shared positions, 893 GFLOP: 703 us
+// with the join of the own part, 1270 TFLOP/s, 68 % of the measured rate.)
 // The output stays in tensor memory and is scaled only when a row's maximum has risen by more
 // than 2^8 since it was last scaled (the exponentials then stay below 2^8, far inside bf16's
 // and fp32's range, and the quotient by their sum is the same), so the read-modify-write of
@@ -36,8 +38,10 @@ namespace svk {
 namespace {
 
 constexpr int kTcHalf = 128, kTcKB = kAttnTcKeys;
-// A tile's fixed costs in blocks.  With 2, 3, 4 and 6 two 4096-token prompts took 325, 305, 287
-// and 282 us (their tiles' lengths differ most); trees and shared prefixes hardly tell.
+// A tile's fixed costs in blocks.  With 2, 3, 4 and 6 two 4096-token prompts take 316, 297, 279
+// and 273 us (their tiles' lengths differ most), 64 trees of 240 rows on 512 to 4096 positions
+// 182, 181, 179 and 178, of 80 rows on 2000 positions 118, 118, 118 and 120; 26624 rows of shared
+// positions 863, 865, 856 and 858 with their own part.
 constexpr int kTcC = 6;
 constexpr uint32_t kTcP = 64;      // P's column within a half's scores
 constexpr int kTcStagePitch = 80;  // bytes of a staged row: 64 and a pad against bank conflicts
@@ -48,7 +52,9 @@ constexpr float kTcLazy = 8.f;     // log2 of the rise that makes the output sca
 // H halves of 128 rows in a tile.  H = 2: one CTA per SM.  H = 1 (tiles of at most 128 rows):
 // two CTAs per SM, each with half of the tensor memory, whose loads, products and epilogues
 // overlap each other's: 64 trees of 20 to 128 rows on 2000 positions take 121 to 129 us, with
-// H = 2 141 to 148.
+// H = 2 141 to 148.  With more rows the second tile reads the keys again: 64 trees of 132, 240, 400
+// and 512 rows on 2000 positions take 154, 173, 315 and 322 us with H = 2, 206, 221, 409 and 420
+// with H = 1 (just above 256 rows, where H = 2 has a second tile for 4 rows, 296 against 307).
 template <int DP, int H>
 struct TcCfg {
   static constexpr int kR = kTcHalf * H;
