@@ -100,6 +100,7 @@ typedef struct {
 #define SPEC_TREE_INVALID 2  /* parent_idx / draft_tokens malformed, or depth > max_depth */
 #define SPEC_ROW_TIMEOUT 3   /* a bounded device-side wait gave up: the row's statistics are
                                 not valid (see SPEC_FLAG_TEST_STALL) */
+#define SPEC_ROW_NONE 4      /* a row number outside the rows (spec_token_logprobs) */
 
 /* Size limits checked on the host. */
 #define SPEC_MAX_NODES 4096
@@ -538,6 +539,97 @@ int spec_draft_topk_fused_lmhead(const void* features, const void* lm_head_w, in
                                  void* out_logits, int64_t logits_pitch, int32_t* out_tokens,
                                  float* out_probs, int32_t* out_status, void* workspace,
                                  size_t workspace_bytes, spec_stream_t stream);
+
+/*
+ * Block-scaled 4-bit floating point: a matrix of codes with one scale per block of a row's
+ * elements.  An element is one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign, times its block's scale.
+ *   SPEC_FP4_MX  blocks of 32, the scale 2^e with e in -127 .. 127 (MXFP4 of the OCP Microscaling
+ *                Formats specification 1.0); byte e + 127, 255 stands for NaN
+ *   SPEC_FP4_NV  blocks of 16, the scale s * tensor_scale with s an unsigned e4m3 number (up to
+ *                448; byte 127 stands for NaN) and one power of two for the whole matrix
+ * Layout: codes [rows, 16 * ceil(cols / 32) bytes]; element i of a row is the low (i even) or high
+ *   half of byte i / 2: sign bit, then the index in the list above (the sign of a zero says
+ *   nothing); elements past cols are 0.
+ *   scales: tiles of 128 rows by 4 blocks; with groups = ceil(ceil(cols / block) / 4), the scale
+ *   of row r and block b is byte 512 * ((r / 128) * groups + b / 4) + 16 * (r % 32) +
+ *   4 * (r / 32 % 4) + b % 4; padding (rows past the last, blocks past cols) is 0.
+ *   Both 16-byte aligned, spec_fp4_code_bytes and spec_fp4_scale_bytes long (0 for invalid sizes).
+ *   A slice of rows starts at a multiple of 128 of them.
+ */
+typedef enum { SPEC_FP4_MX = 0, SPEC_FP4_NV = 1 } spec_fp4_format;
+#define SPEC_FP4_MAX_DIM (1 << 24)
+
+size_t spec_fp4_code_bytes(int32_t rows, int32_t cols);
+size_t spec_fp4_scale_bytes(int32_t rows, int32_t cols, spec_fp4_format format);
+
+/*
+ * Quantise rows of `dtype` (row r at x + r * row_pitch elements) and the values that codes and
+ * scales stand for.  The scale of a block with the largest magnitude m is 2^(floor(log2 m) - 2) (MX;
+ * m = 0: 2^-127) or the e4m3 number nearest to m / (6 tensor_scale), 448 at most (NV); a code is
+ * the one nearest to x / scale, halves go to the even code, magnitudes beyond 6 to 6.  Every rounding
+ * is that of the exact quotient.  A block that holds NaN or an infinity gets the scale NaN and codes 0;
+ * a block whose scale rounds to 0 becomes zeros.
+ * The whole of codes and scales is written, padding included.  spec_fp4_dequantize rounds the
+ * product of code and scale once to `dtype` (exact but for results below its normal range); what lies
+ * between cols and row_pitch is left as it is.
+ * tensor_scale: a power of two within 2^-100 .. 2^100; 1 for MX.
+ * Bases 16-byte aligned, row_pitch * sizeof(elem) a multiple of 16.  Asynchronous on `stream`;
+ * allocates nothing.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED_DTYPE (dtype or format), SPEC_ERR_MISALIGNED,
+ * SPEC_ERR_TOO_LARGE (rows or cols above SPEC_FP4_MAX_DIM, or above 2^44 elements), SPEC_ERR_CUDA.
+ */
+int spec_fp4_quantize(const void* x, spec_dtype dtype, int32_t rows, int32_t cols,
+                      int64_t row_pitch, spec_fp4_format format, float tensor_scale, void* codes,
+                      void* scales, spec_stream_t stream);
+int spec_fp4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols,
+                        spec_fp4_format format, float tensor_scale, void* out, spec_dtype dtype,
+                        int64_t row_pitch, spec_stream_t stream);
+
+/*
+ * The product of two matrices in this form, on the tensor cores: an LM head or another linear layer
+ * kept in 4 bits.
+ *   out[r][v] = alpha * sum_k a[r][k] w[v][k],  r < R, v < V, k < K
+ * a [R, K] (activations), w [V, K] (weight), both of `format`; the scales' bytes alone enter the
+ * product, so alpha is the product of the two tensor scales (times any other factor).  Products
+ * are exact, sums fp32, the result rounded once to `dtype`; out [R, row_pitch] of which the first V
+ * elements of a row are written.  A block whose scale is NaN makes the results that use it NaN.
+ * A device-side wait that gives up (2 s) makes the results it concerns NaN.
+ * out's base and row_pitch * sizeof(elem) are multiples of 16 bytes.  Asynchronous on `stream`;
+ * allocates nothing.
+ * Errors: SPEC_ERR_INVALID_ARG (sizes, alpha not finite, null pointers),
+ * SPEC_ERR_UNSUPPORTED_DTYPE, SPEC_ERR_MISALIGNED, SPEC_ERR_TOO_LARGE, SPEC_ERR_CUDA.
+ */
+int spec_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
+                    const void* w_scales, spec_fp4_format format, int32_t R, int32_t V, int32_t K,
+                    float alpha, void* out, spec_dtype dtype, int64_t row_pitch,
+                    spec_stream_t stream);
+
+/*
+ * What a server reports of the tokens it emits: from rows of logits, the log probabilities of given
+ * tokens, the entropy and the most likely tokens of the distribution at `temperature` (softmax of
+ * z / temperature over the whole row; no top-k or top-p cut).
+ *   out_logprobs [R, G]: ln p of tokens [R, G]; a token outside [0, V) has -inf
+ *   out_entropy [R] (optional): -sum p ln p, in nats
+ *   out_top_tokens, out_top_logprobs [R, k]: the k largest logits (ties to the lower index, listed
+ *     in that order) and their ln p; 0 <= k <= 32, k <= V (k = 0: both may be NULL)
+ *   out_status [R] (optional): SPEC_TREE_OK; SPEC_ROW_NONFINITE for a row that holds NaN or +inf or is
+ *     all -inf (log probabilities and entropy NaN, tokens -1); SPEC_ROW_NONE for a row number
+ *     outside [0, n_rows) (log probabilities -inf, entropy 0, tokens -1)
+ * logits [n_rows, row_pitch] of dtype, base and row_pitch * sizeof(elem) 16-byte aligned.  rows [R]
+ *   (device): the row that result r is read from, in any order, the same one any number of times;
+ *   NULL: row r (R <= n_rows).  With the row numbers of an accepted path only those rows are
+ *   read.  tokens is int32, G >= 0 (0: NULL).
+ * temperature finite and at least SPEC_LOGPROB_MIN_TEMPERATURE.  Asynchronous on `stream`;
+ * allocates nothing.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED_DTYPE, SPEC_ERR_MISALIGNED,
+ * SPEC_ERR_TOO_LARGE (V > SPEC_MAX_VOCAB), SPEC_ERR_CUDA.
+ */
+#define SPEC_LOGPROB_MIN_TEMPERATURE 1e-37f
+int spec_token_logprobs(const void* logits, spec_dtype dtype, int32_t n_rows, int32_t V,
+                        int64_t row_pitch, const int32_t* rows, int32_t R, const int32_t* tokens,
+                        int32_t G, int32_t k, float temperature, float* out_logprobs,
+                        float* out_entropy, int32_t* out_top_tokens, float* out_top_logprobs,
+                        int32_t* out_status, spec_stream_t stream);
 
 /*
  * EAGLE-2 dynamic draft tree (EAGLE / EAGLE-2 paper translation, modelers.csdn.net,

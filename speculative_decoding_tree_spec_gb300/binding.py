@@ -12,6 +12,7 @@ import functools
 import inspect
 import os
 import threading
+import typing
 
 import torch
 
@@ -42,6 +43,11 @@ SPEC_ATTN_MAX_HEAD_DIM = 128
 SPEC_APPEND_MAX_HEAD_DIM = 1024
 SPEC_MAX_POSITIONS = 0x7FFFF000
 SPEC_ROPE_INTERLEAVED = 1
+SPEC_ROW_NONE = 4
+SPEC_FP4_MX = 0
+SPEC_FP4_NV = 1
+SPEC_FP4_MAX_DIM = 1 << 24
+SPEC_LOGPROB_MIN_TEMPERATURE = 1e-37
 ERRORS = {0: "SPEC_OK", -1: "SPEC_ERR_INVALID_ARG", -2: "SPEC_ERR_UNSUPPORTED_DTYPE",
           -3: "SPEC_ERR_MISALIGNED", -4: "SPEC_ERR_WORKSPACE", -5: "SPEC_ERR_CUDA",
           -6: "SPEC_ERR_TOO_LARGE"}
@@ -148,6 +154,21 @@ def lib():
                                                        P, ctypes.c_int64, P, P, P, P,
                                                        ctypes.c_size_t, P]
             L.spec_draft_topk_fused_lmhead.restype = ctypes.c_int
+            F = ctypes.c_float
+            L.spec_fp4_code_bytes.argtypes = [i32, i32]
+            L.spec_fp4_code_bytes.restype = ctypes.c_size_t
+            L.spec_fp4_scale_bytes.argtypes = [i32, i32, ctypes.c_int]
+            L.spec_fp4_scale_bytes.restype = ctypes.c_size_t
+            L.spec_fp4_quantize.argtypes = [P, ctypes.c_int, i32, i32, i64, ctypes.c_int, F, P, P, P]
+            L.spec_fp4_quantize.restype = ctypes.c_int
+            L.spec_fp4_dequantize.argtypes = [P, P, i32, i32, ctypes.c_int, F, P, ctypes.c_int, i64, P]
+            L.spec_fp4_dequantize.restype = ctypes.c_int
+            L.spec_fp4_linear.argtypes = [P, P, P, P, ctypes.c_int, i32, i32, i32, F, P, ctypes.c_int,
+                                          i64, P]
+            L.spec_fp4_linear.restype = ctypes.c_int
+            L.spec_token_logprobs.argtypes = [P, ctypes.c_int, i32, i32, i64, P, i32, P, i32, i32, F, P,
+                                              P, P, P, P, P]
+            L.spec_token_logprobs.restype = ctypes.c_int
             L.spec_tree_expand_topk.argtypes = [P, P, i32, i32, i32, i32, i32, P, P]
             L.spec_tree_expand_topk.restype = ctypes.c_int
             L.spec_tree_build.argtypes = [P, P, P, P, i32, i32, i32, P, P, P, P, P, P, P]
@@ -487,7 +508,7 @@ def _int32(t, shape, dev: int, what):
     if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or \
             not t.is_contiguous():
         raise TypeError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on the "
-                        "cache's device")
+                        "others' device")
     return t.data_ptr()
 
 
@@ -739,6 +760,201 @@ def draft_topk_fused_lmhead(features: torch.Tensor, weight: torch.Tensor, k: int
     if rc != 0:
         raise SpecError(rc, "spec_draft_topk_fused_lmhead")
     return out
+
+
+_FP4_FORMATS = {"mx": SPEC_FP4_MX, "nv": SPEC_FP4_NV}
+
+
+class Fp4Matrix(typing.NamedTuple):
+    """A [rows, cols] matrix in block-scaled 4-bit floating point: codes and scales (uint8, in the
+    layout of include/spec_verify.h), the format ("mx": blocks of 32, power-of-two scales; "nv":
+    blocks of 16, e4m3 scales times tensor_scale)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+    format: str
+    tensor_scale: float = 1.0
+
+
+def _float_dtype(dtype) -> int:
+    code = _PAGED_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"float32 or bfloat16 is wanted, got {dtype}")
+    return code
+
+
+def _fp4_sizes(rows: int, cols: int, fmt: str):
+    """(bytes of a row of codes, bytes of all scales)."""
+    per = 128 if fmt == "mx" else 64
+    return (cols + 31) // 32 * 16, (rows + 127) // 128 * ((cols + per - 1) // per) * 512
+
+
+def _fp4_check(m: Fp4Matrix, dev: int, what: str):
+    """The format's code and the pointers of a matrix whose tensors fit its sizes."""
+    fmt = _FP4_FORMATS.get(m.format)
+    if fmt is None:
+        raise ValueError(f"{what}: the format is 'mx' or 'nv', got {m.format!r}")
+    if m.rows < 0 or m.cols < 1:
+        raise ValueError(f"{what}: rows and cols must be positive")
+    c, s = m.codes, m.scales
+    row, scales = _fp4_sizes(m.rows, m.cols, m.format)
+    if c.dtype is not torch.uint8 or s.dtype is not torch.uint8 or c.get_device() != dev or \
+            s.get_device() != dev or not c.is_contiguous() or not s.is_contiguous():
+        raise TypeError(f"{what}: codes and scales must be contiguous uint8 tensors on one CUDA device")
+    if c.numel() != m.rows * row or s.numel() != scales:
+        raise ValueError(f"{what}: a {m.rows} x {m.cols} {m.format} matrix has {m.rows * row} bytes of "
+                         f"codes and {scales} of scales, got {c.numel()} and {s.numel()}")
+    return fmt, c.data_ptr(), s.data_ptr()
+
+
+def _padded(rows: int, cols: int, dtype, device):
+    """An empty [rows, cols] whose rows start on 16-byte boundaries."""
+    per = 16 // dtype.itemsize
+    pitch = (cols + per - 1) // per * per
+    t = torch.empty((rows, pitch), dtype=dtype, device=device)
+    return t if pitch == cols else t[:, :cols]
+
+
+def _matrix_out(out, rows: int, cols: int, dtype, dev: int):
+    if out.dim() != 2 or out.shape != (rows, cols) or out.dtype is not dtype or out.get_device() != dev:
+        raise TypeError(f"out must be a [{rows}, {cols}] tensor of {dtype} on the inputs' device")
+    if out.stride(1) != 1 and cols > 1:
+        raise ValueError("out's rows must be contiguous")
+    return out
+
+
+def _pitch(t: torch.Tensor, cols: int) -> int:
+    """Elements from row to row; what one row's stride says does not matter."""
+    per = 16 // t.element_size()
+    return t.stride(0) if t.shape[0] > 1 else (cols + per - 1) // per * per
+
+
+def fp4_quantize(x: torch.Tensor, format: str = "mx", tensor_scale: float = 1.0, *, out=None,
+                 stream=None) -> Fp4Matrix:
+    """spec_fp4_quantize: rows of x [rows, cols] (float32 or bfloat16, contiguous rows on 16-byte
+    boundaries) in block-scaled 4-bit floating point.  tensor_scale: a power of two, 1 for "mx".
+    out: an Fp4Matrix of the same sizes to write to.  `stream` as in paged_append_rope."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be on a CUDA device")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return fp4_quantize(x, format, tensor_scale, out=out)
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [rows, cols] with contiguous rows")
+    rows, cols = x.shape
+    if format not in _FP4_FORMATS:
+        raise ValueError(f"the format is 'mx' or 'nv', got {format!r}")
+    if out is None:
+        row, scales = _fp4_sizes(rows, cols, format)
+        out = Fp4Matrix(torch.empty((rows, row), dtype=torch.uint8, device=x.device),
+                        torch.empty(scales, dtype=torch.uint8, device=x.device), rows, cols, format,
+                        float(tensor_scale))
+    elif (out.rows, out.cols, out.format, out.tensor_scale) != (rows, cols, format, tensor_scale):
+        raise ValueError("out must have x's sizes, the format and the tensor scale")
+    fmt, codes, scales = _fp4_check(out, dev, "out")
+    rc = (_lib or lib()).spec_fp4_quantize(x.data_ptr(), _float_dtype(x.dtype), rows, cols,
+                                           _pitch(x, cols), fmt, tensor_scale, codes, scales,
+                                           torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        raise SpecError(rc, "spec_fp4_quantize")
+    return out
+
+
+def fp4_dequantize(m: Fp4Matrix, dtype=torch.bfloat16, *, out=None, stream=None) -> torch.Tensor:
+    """spec_fp4_dequantize: the [rows, cols] values (bfloat16 or float32) that m stands for."""
+    dev = m.codes.get_device()
+    if dev < 0:
+        raise ValueError("the matrix must be on a CUDA device")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return fp4_dequantize(m, dtype, out=out)
+    fmt, codes, scales = _fp4_check(m, dev, "the matrix")
+    code = _float_dtype(dtype)
+    if out is None:
+        out = _padded(m.rows, m.cols, dtype, m.codes.device)
+    else:
+        _matrix_out(out, m.rows, m.cols, dtype, dev)
+    rc = (_lib or lib()).spec_fp4_dequantize(codes, scales, m.rows, m.cols, fmt, m.tensor_scale,
+                                             out.data_ptr(), code, _pitch(out, m.cols),
+                                             torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        raise SpecError(rc, "spec_fp4_dequantize")
+    return out
+
+
+def fp4_linear(a: Fp4Matrix, w: Fp4Matrix, dtype=torch.bfloat16, *, alpha: float = 1.0, out=None,
+               stream=None) -> torch.Tensor:
+    """spec_fp4_linear: alpha * a w^T [a.rows, w.rows] of two matrices of one format with the same
+    number of columns, as bfloat16 or float32 (a view with padded rows where w.rows is odd).  The
+    tensor scales are taken in."""
+    dev = a.codes.get_device()
+    if dev < 0:
+        raise ValueError("the matrices must be on a CUDA device")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return fp4_linear(a, w, dtype, alpha=alpha, out=out)
+    fmt, ac, asc = _fp4_check(a, dev, "a")
+    _, wc, wsc = _fp4_check(w, dev, "w")
+    if a.format != w.format or a.cols != w.cols:
+        raise ValueError("a and w must share the format and the number of columns")
+    code = _float_dtype(dtype)
+    if out is None:
+        out = _padded(a.rows, w.rows, dtype, a.codes.device)
+    else:
+        _matrix_out(out, a.rows, w.rows, dtype, dev)
+    rc = (_lib or lib()).spec_fp4_linear(ac, asc, wc, wsc, fmt, a.rows, w.rows, a.cols,
+                                         alpha * a.tensor_scale * w.tensor_scale, out.data_ptr(), code,
+                                         _pitch(out, w.rows), torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        raise SpecError(rc, "spec_fp4_linear")
+    return out
+
+
+def token_logprobs(logits: torch.Tensor, tokens=None, k: int = 0, temperature: float = 1.0, *,
+                   rows=None, stream=None) -> dict:
+    """spec_token_logprobs on [n, V] device rows (row pitch from the tensor's stride).  tokens: the
+    given tokens [R] or [R, G] int32 (None: none); rows [R] int32: the row numbers to read (None:
+    row r for result r).  Returns logprobs (of tokens' shape), entropy [R], top_tokens and
+    top_logprobs [R, k] and status [R]; natural logarithms, float32."""
+    dev = logits.get_device()
+    if dev < 0:
+        raise ValueError("the logits must be on a CUDA device")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return token_logprobs(logits, tokens, k, temperature, rows=rows)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [n, V] with contiguous rows")
+    n, V = logits.shape
+    device = logits.device
+    if rows is not None and rows.dim() != 1:
+        raise ValueError("rows must be [R]")
+    R = n if rows is None else rows.shape[0]
+    if tokens is not None:
+        G = tokens.shape[1] if tokens.dim() == 2 else 1
+        given = _int32(tokens, (R, G) if tokens.dim() == 2 else (R,), dev, "tokens")
+        logprobs = torch.empty(tokens.shape, dtype=torch.float32, device=device)
+    else:
+        G, given = 0, None
+        logprobs = torch.empty((R, 0), dtype=torch.float32, device=device)
+    entropy = torch.empty(R, dtype=torch.float32, device=device)
+    top = torch.empty((R, max(k, 0)), dtype=torch.int32, device=device)
+    top_lp = torch.empty((R, max(k, 0)), dtype=torch.float32, device=device)
+    status = torch.empty(R, dtype=torch.int32, device=device)
+    rc = (_lib or lib()).spec_token_logprobs(
+        logits.data_ptr(), _float_dtype(logits.dtype), n, V, _pitch(logits, V),
+        _int32(rows, (R,), dev, "rows"), R, given, G, k, temperature, logprobs.data_ptr(),
+        entropy.data_ptr(), top.data_ptr(), top_lp.data_ptr(), status.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        raise SpecError(rc, "spec_token_logprobs")
+    return {"logprobs": logprobs, "entropy": entropy, "top_tokens": top, "top_logprobs": top_lp,
+            "status": status}
 
 
 @_on_stream

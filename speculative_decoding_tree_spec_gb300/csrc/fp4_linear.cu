@@ -1,0 +1,492 @@
+// fp4_linear.cu -- the product of two matrices in block-scaled 4-bit floating point,
+//   out[r][v] = alpha sum_k a[r][k] w[v][k],
+// on the fifth-generation tensor cores (tcgen05.mma with block scales): codes and scales go to the
+// tensor cores as they are stored, products are exact and summed in fp32, the result is rounded once.
+//
+// The weight's rows are the tile's M (128 per CTA), the activations' rows its N (16 to 192): a head
+// has many of the former, a decoding step any number of the latter.  Persistent CTAs, K in steps of 256
+// elements (rows of 128 bytes):
+//   warp 0      TMA producer: codes of both operands with the 128-byte swizzle and their scale tiles
+//               (512 contiguous bytes each) into a ring of stages
+//   warp 1      copies a stage's scales to tensor memory (tcgen05.cp, ordered before the products that
+//               read them) and issues four K = 64 products into one of two accumulators
+//   warps 2-5   epilogue: a thread has one weight row, reads 32 columns at a time
+// Every wait is bounded; a tile whose accumulator does not come is written as NaN.
+#include <cuda.h>
+
+#include <cuda_bf16.h>
+
+#include "fp4.cuh"
+#include "tcgen05.cuh"
+
+namespace svk {
+
+namespace {
+
+constexpr int kFlM = 128;        // weight rows of a CTA's tile
+constexpr int kFlMaxN = 192;     // activation rows of a tile
+constexpr int kFlK = 256;        // elements of a stage
+constexpr int kFlMaxStages = 10;
+constexpr int kFlThreads = 192;
+constexpr uint32_t kFlABytes = kFlM * kFlK / 2;
+constexpr uint32_t kFlSfCol = 2 * kFlMaxN;  // first tensor-memory column of the scales
+constexpr uint32_t kFlSfBuf = 64;           // columns of one of the two buffers
+constexpr uint32_t kFlSfB = 16;             // the activations' scales in a buffer
+constexpr size_t kFlSmemMax = 224 * 1024;
+
+template <spec_fp4_format F>
+struct Fmt;
+template <>
+struct Fmt<SPEC_FP4_MX> {
+  static constexpr int kGroups = 2;  // scale tiles along a stage
+};
+template <>
+struct Fmt<SPEC_FP4_NV> {
+  static constexpr int kGroups = 4;
+};
+
+// Instruction descriptor of the block-scaled 4-bit kinds: both operands e2m1 and K-major, scale
+// type (ue8m0 or ue4m3), M, N, and which of a tensor-memory word's scales the product starts at.
+template <spec_fp4_format F>
+__device__ __forceinline__ uint32_t fp4_idesc(int m, int n, int sf) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)sf << 4) | ((uint32_t)(n >> 3) << 17) |
+         ((F == SPEC_FP4_MX ? 1u : 0u) << 23) | ((uint32_t)(m >> 4) << 24) | ((uint32_t)sf << 29);
+}
+// 32 rows of 16 bytes, without a swizzle: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+  return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1u << 46);
+}
+
+template <int CG, spec_fp4_format F>
+__device__ __forceinline__ void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, bool accumulate) {
+#define SVK_FP4_MMA(GROUP, KIND)                                                               \
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"                                   \
+               " tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" \
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb),                       \
+               "r"((uint32_t)accumulate)                                                       \
+               : "memory")
+  if constexpr (F == SPEC_FP4_MX) {
+    if constexpr (CG == 1) SVK_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
+    else SVK_FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
+  } else {
+    if constexpr (CG == 1) SVK_FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    else SVK_FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  }
+#undef SVK_FP4_MMA
+}
+template <int CG>
+__device__ __forceinline__ void scales_to_tmem(uint32_t d, uint64_t desc) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(d), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(d), "l"(desc) : "memory");
+}
+// Arrives on the barrier (both CTAs' at CG 2) once the products issued so far are done.
+template <int CG>
+__device__ __forceinline__ void fp4_commit(uint64_t* bar) {
+  if constexpr (CG == 1)
+    tc05_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+        "%1;\n" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void fp4_alloc(uint32_t* smem_addr) {
+  if constexpr (CG == 1) {
+    tc05_alloc(smem_addr, 512);
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+                     smem_u32(smem_addr))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void fp4_dealloc(uint32_t tmem) {
+  if constexpr (CG == 1)
+    tc05_dealloc(tmem, 512);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+}
+// A box of a tensor map into this CTA's shared memory; its bytes count on `bar`, the address of a
+// barrier in this CTA or (CG 2) in the pair's first.
+template <int CG>
+__device__ __forceinline__ void fp4_load(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t first_cta(const void* p) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+template <int CG>
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(first_cta(bar))
+                 : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (CG == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
+                     : "memory");
+}
+
+struct LinearJob {
+  int R, V;
+  int m_tiles, n_tiles, tile_n;
+  int k_steps, last_mma;  // stages along K, products of the last one
+  int groups_a, groups_w; // scale tiles along K (the same number), rows' tiles start at groups * tile
+  int sf_chunks;          // row tiles of the activations' scales that a tile's rows touch
+  int stages;
+  uint32_t b_bytes;       // of a stage's activations in one CTA
+  float alpha;
+  void* out;
+  int64_t pitch;
+  uint64_t wait_limit_ns;
+};
+
+struct LinearShared {
+  uint64_t full[kFlMaxStages], empty[kFlMaxStages], tfull[2], tempty[2];
+  uint32_t tmem;
+};
+
+template <int CG, spec_fp4_format F, typename O>
+__global__ void __launch_bounds__(kFlThreads, 1)
+    fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                      const __grid_constant__ CUtensorMap tm_ws,
+                      const __grid_constant__ CUtensorMap tm_as, LinearJob job) {
+  constexpr int kGroups = Fmt<F>::kGroups;
+  constexpr uint32_t kSfaBytes = kGroups * kScaleTile;
+  __shared__ LinearShared sh;
+  extern __shared__ unsigned char fl_dyn[];
+  const uint32_t base = (smem_u32(fl_dyn) + 1023u) & ~1023u;
+  const uint32_t stage_bytes =
+      kFlABytes + job.b_bytes + kSfaBytes + (uint32_t)job.sf_chunks * kSfaBytes;
+  const uint32_t stage_pitch = (stage_bytes + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1u);
+  const int group = (int)blockIdx.x / CG, n_groups = (int)gridDim.x / CG;
+  const int tiles = job.m_tiles * job.n_tiles;
+  const uint64_t limit = job.wait_limit_ns;
+  const int stages = job.stages;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sh.tfull[a], 1);
+      mbar_init(&sh.tempty[a], 4 * CG);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) fp4_alloc<CG>(&sh.tmem);
+  tc05_fence_before();
+  __syncthreads();
+  if (CG > 1) group_sync<CG>();
+  tc05_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool stop = false;
+      for (int t = group; t < tiles && !stop; t += n_groups) {
+        const int nt = t % job.n_tiles, mt = t / job.n_tiles;
+        const int n0 = nt * job.tile_n;
+        const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
+        const int row_w = (mt * CG + rank) * kFlM, row_a = n0 + rank * (n / CG);
+        for (int kb = 0; kb < job.k_steps; ++kb, ++it) {
+          const int s = (int)(it % (uint32_t)stages);
+          const uint32_t ph = (it / (uint32_t)stages) & 1u;
+          if (!mbar_wait(&sh.empty[s], ph ^ 1u, limit)) {
+            stop = true;
+            break;
+          }
+          const uint32_t a = base + (uint32_t)s * stage_pitch;
+          const uint32_t bar = CG == 1 ? smem_u32(&sh.full[s]) : first_cta(&sh.full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], CG * stage_bytes);
+          fp4_load<CG>(a, &tm_w, kb * (kFlK / 2), row_w, bar);
+          fp4_load<CG>(a + kFlABytes, &tm_a, kb * (kFlK / 2), row_a, bar);
+          uint32_t sf = a + kFlABytes + job.b_bytes;
+          fp4_load<CG>(sf, &tm_ws, 0, (row_w >> 7) * job.groups_w + kb * kGroups, bar);
+          for (int j = 0; j < job.sf_chunks; ++j) {
+            sf += kSfaBytes;
+            fp4_load<CG>(sf, &tm_as, 0, ((n0 >> 7) + j) * job.groups_a + kb * kGroups, bar);
+          }
+        }
+      }
+      // the last stages' products are done, and with them their copies
+      const uint32_t first = it > (uint32_t)stages ? it - (uint32_t)stages : 0u;
+      for (uint32_t h = first; h < it; ++h)
+        if (!mbar_wait(&sh.empty[h % (uint32_t)stages], (h / (uint32_t)stages) & 1u, limit)) break;
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- products ----------------
+    uint32_t it = 0, lt = 0;
+    bool stop = false;
+    for (int t = group; t < tiles && !stop; t += n_groups, ++lt) {
+      const int acc = (int)(lt & 1u);
+      if (!__all_sync(kFull, mbar_wait(&sh.tempty[acc], ((lt >> 1) & 1u) ^ 1u, limit))) break;
+      tc05_fence_after();
+      const int n0 = (t % job.n_tiles) * job.tile_n;
+      const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
+      const uint32_t d = tmem + (uint32_t)(acc * kFlMaxN);
+      for (int kb = 0; kb < job.k_steps; ++kb, ++it) {
+        const int s = (int)(it % (uint32_t)stages);
+        if (!__all_sync(kFull, mbar_wait(&sh.full[s], (it / (uint32_t)stages) & 1u, limit))) {
+          stop = true;
+          break;
+        }
+        tc05_fence_after();
+        const uint32_t a = base + (uint32_t)s * stage_pitch;
+        const uint32_t sf = a + kFlABytes + job.b_bytes;
+        const uint32_t sfa = tmem + kFlSfCol + (it & 1u) * kFlSfBuf, sfb = sfa + kFlSfB;
+        const uint64_t adesc = sw128_tile(a, 16), bdesc = sw128_tile(a + kFlABytes, 16);
+        const int products = kb + 1 == job.k_steps ? job.last_mma : 4;
+        if (elect_one()) {
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+            scales_to_tmem<CG>(sfa + (uint32_t)g * 4, scale_desc(sf + (uint32_t)g * kScaleTile));
+          for (int j = 0; j < job.sf_chunks; ++j)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+              scales_to_tmem<CG>(sfb + (uint32_t)(g * job.sf_chunks + j) * 4,
+                                 scale_desc(sf + (uint32_t)((1 + j) * kGroups + g) * kScaleTile));
+          const uint32_t off_b = (uint32_t)(n0 & 127) >> 5;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j < products) {
+              const int g = F == SPEC_FP4_MX ? j >> 1 : j;
+              const int id = F == SPEC_FP4_MX ? (j & 1) * 2 : 0;
+              // the next 64 elements are 32 bytes further along the swizzled rows
+              fp4_mma<CG, F>(d, adesc + (uint64_t)(j * 2), bdesc + (uint64_t)(j * 2),
+                             fp4_idesc<F>(kFlM * CG, n, id), sfa + (uint32_t)g * 4,
+                             sfb + (uint32_t)(g * job.sf_chunks) * 4 + off_b, (kb | j) != 0);
+            }
+          }
+          fp4_commit<CG>(&sh.empty[s]);
+          if (kb + 1 == job.k_steps) fp4_commit<CG>(&sh.tfull[acc]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp >= 2) {
+    // ---------------- epilogue ----------------
+    const int quarter = warp & 3;  // this warp's lanes of tensor memory
+    uint32_t lt = 0;
+    bool lost = false;
+    for (int t = group; t < tiles; t += n_groups, ++lt) {
+      const int acc = (int)(lt & 1u);
+      if (!lost) lost = !__all_sync(kFull, mbar_wait(&sh.tfull[acc], (lt >> 1) & 1u, limit));
+      tc05_fence_after();
+      const int nt = t % job.n_tiles, mt = t / job.n_tiles;
+      const int n0 = nt * job.tile_n, rows = min(job.tile_n, job.R - n0);
+      const int v = (mt * CG + rank) * kFlM + quarter * 32 + lane;
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kFlMaxN);
+      O* out = static_cast<O*>(job.out) + (int64_t)n0 * job.pitch + v;
+#pragma unroll 1
+      for (int c0 = 0; c0 < rows; c0 += 16) {
+        uint32_t x[16];
+        tc05_ld16(taddr + (uint32_t)c0, x);
+        tc05_wait_ld();
+        tc05_landed16(x);
+        if (v < job.V) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c0 + i < rows) {
+              const float y = lost ? CUDART_NAN_F : __uint_as_float(x[i]) * job.alpha;
+              if constexpr (sizeof(O) == 2)
+                reinterpret_cast<__nv_bfloat16*>(out)[(int64_t)(c0 + i) * job.pitch] = __float2bfloat16_rn(y);
+              else
+                reinterpret_cast<float*>(out)[(int64_t)(c0 + i) * job.pitch] = y;
+            }
+          }
+        }
+      }
+      tc05_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_first<CG>(&sh.tempty[acc]);
+    }
+  }
+  __syncwarp();
+  tc05_fence_before();
+  __syncthreads();
+  if (CG > 1) group_sync<CG>();
+  tc05_fence_after();
+  if (warp == 1) fp4_dealloc<CG>(tmem);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  return fn;
+}
+
+// Rows of codes, boxes of 128 bytes by box_rows.
+bool code_map(CUtensorMap* map, const void* p, int rows, int64_t row_bytes, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {kFlK / 2, (cuuint32_t)box_rows};
+  const cuuint32_t one[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Scale tiles one after another, boxes of `n` of them.
+bool scale_map(CUtensorMap* map, const void* p, int64_t tiles, int n) {
+  const cuuint64_t dims[2] = {kScaleTile / 4, (cuuint64_t)tiles};
+  const cuuint64_t strides[1] = {kScaleTile};
+  const cuuint32_t box[2] = {kScaleTile / 4, (cuuint32_t)n};
+  const cuuint32_t one[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(p), dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG, spec_fp4_format F, typename O>
+cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, const void* w_scales,
+                          int K, LinearJob job, cudaStream_t s) {
+  if (!encode_fn()) return cudaErrorNotSupported;
+  constexpr int kGroups = Fmt<F>::kGroups;
+  const int64_t row_bytes = fp4_row_bytes(K);
+  job.groups_a = job.groups_w = fp4_groups(K, F);
+  job.k_steps = (int)((row_bytes * 2 + kFlK - 1) / kFlK);
+  job.last_mma = (int)((row_bytes * 2 - (int64_t)(job.k_steps - 1) * kFlK + 63) / 64);
+  job.m_tiles = (job.V + CG * kFlM - 1) / (CG * kFlM);
+  const int box_n = (job.tile_n / CG + 7) & ~7;
+  job.b_bytes = (uint32_t)box_n * (kFlK / 2);
+  const uint32_t stage = (kFlABytes + job.b_bytes + (uint32_t)((1 + job.sf_chunks) * kGroups * kScaleTile) +
+                          1023u) & ~1023u;
+  job.stages = (int)((kFlSmemMax - 1024) / stage);
+  if (job.stages > kFlMaxStages) job.stages = kFlMaxStages;
+  const size_t smem = 1024 + (size_t)job.stages * stage;
+  CUtensorMap tm_w, tm_a, tm_ws, tm_as;
+  if (!code_map(&tm_w, w, job.V, row_bytes, kFlM) || !code_map(&tm_a, a, job.R, row_bytes, box_n) ||
+      !scale_map(&tm_ws, w_scales, (int64_t)fp4_row_tiles(job.V) * job.groups_w, kGroups) ||
+      !scale_map(&tm_as, a_scales, (int64_t)fp4_row_tiles(job.R) * job.groups_a, kGroups))
+    return cudaErrorInvalidValue;
+  auto kernel = fp4_linear_kernel<CG, F, O>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFlSmemMax);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  int64_t groups = device_sm_count() / CG;
+  if (groups > (int64_t)job.m_tiles * job.n_tiles) groups = (int64_t)job.m_tiles * job.n_tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * CG));
+  cfg.blockDim = dim3(kFlThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, tm_ws, tm_as, job);
+}
+
+template <spec_fp4_format F, typename O>
+cudaError_t launch_linear_group(const void* a, const void* a_scales, const void* w, const void* w_scales,
+                                int K, LinearJob job, cudaStream_t s) {
+  if (job.R > 64) return launch_linear<2, F, O>(a, a_scales, w, w_scales, K, job, s);
+  return launch_linear<1, F, O>(a, a_scales, w, w_scales, K, job, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
+                              const void* w_scales, spec_fp4_format format, int R, int V, int K,
+                              float alpha, void* out, spec_dtype dtype, int64_t pitch, cudaStream_t s) {
+  LinearJob job{};
+  job.R = R;
+  job.V = V;
+  job.alpha = alpha;
+  job.out = out;
+  job.pitch = pitch;
+  job.wait_limit_ns = 2000000000ull;
+  // tiles of equal numbers of rows; more than one start at multiples of 64 rows, where the scales'
+  // columns in tensor memory are aligned
+  job.n_tiles = (R + kFlMaxN - 1) / kFlMaxN;
+  const int per = (R + job.n_tiles - 1) / job.n_tiles;
+  job.tile_n = job.n_tiles == 1 ? (per + 15) & ~15 : (per + 63) & ~63;
+  job.n_tiles = (R + job.tile_n - 1) / job.tile_n;
+  job.sf_chunks = job.tile_n <= 128 && (job.n_tiles == 1 || 128 % job.tile_n == 0) ? 1 : 2;
+  if (format == SPEC_FP4_MX)
+    return dtype == SPEC_BF16
+               ? launch_linear_group<SPEC_FP4_MX, uint16_t>(a_codes, a_scales, w_codes, w_scales, K, job, s)
+               : launch_linear_group<SPEC_FP4_MX, float>(a_codes, a_scales, w_codes, w_scales, K, job, s);
+  return dtype == SPEC_BF16
+             ? launch_linear_group<SPEC_FP4_NV, uint16_t>(a_codes, a_scales, w_codes, w_scales, K, job, s)
+             : launch_linear_group<SPEC_FP4_NV, float>(a_codes, a_scales, w_codes, w_scales, K, job, s);
+}
+
+}  // namespace svk
+
+using namespace svk;
+
+extern "C" int spec_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
+                               const void* w_scales, spec_fp4_format format, int32_t R, int32_t V,
+                               int32_t K, float alpha, void* out, spec_dtype dtype, int64_t row_pitch,
+                               spec_stream_t stream) {
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (format != SPEC_FP4_MX && format != SPEC_FP4_NV) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (R < 0 || V < 1 || K < 1 || row_pitch < V) return SPEC_ERR_INVALID_ARG;
+  if (!(alpha >= -3.402823466e38f && alpha <= 3.402823466e38f)) return SPEC_ERR_INVALID_ARG;
+  if (R > SPEC_FP4_MAX_DIM || V > SPEC_FP4_MAX_DIM || K > SPEC_FP4_MAX_DIM || row_pitch > INT64_MAX / 8 / SPEC_FP4_MAX_DIM ||
+      (int64_t)fp4_row_tiles(R > V ? R : V) * fp4_groups(K, format) > INT32_MAX - 8 ||
+      ((int64_t)R + 63) / 64 * (((int64_t)V + 127) / 128) > INT32_MAX)
+    return SPEC_ERR_TOO_LARGE;
+  if (R == 0) return SPEC_OK;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !out) return SPEC_ERR_INVALID_ARG;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a_codes) | reinterpret_cast<uintptr_t>(a_scales) |
+                        reinterpret_cast<uintptr_t>(w_codes) | reinterpret_cast<uintptr_t>(w_scales) |
+                        reinterpret_cast<uintptr_t>(out);
+  if ((all & 15u) || row_pitch * (dtype == SPEC_BF16 ? 2 : 4) % 16 != 0) return SPEC_ERR_MISALIGNED;
+  return launch_fp4_linear(a_codes, a_scales, w_codes, w_scales, format, R, V, K, alpha, out, dtype,
+                           row_pitch, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
