@@ -151,6 +151,84 @@ __device__ __forceinline__ void group_sync() {
                      : "memory");
 }
 
+// The epilogue takes 32 columns (activation rows) of its 32 lanes (weight rows) at a time, leaves them in shared
+// memory as 32 rows of 32 results side by side, and a bulk store takes them out, clipped to the matrix.
+template <typename O>
+__host__ __device__ constexpr uint32_t out_stage_bytes() {
+  return 32 * 32 * sizeof(O);
+}
+// bf16: pieces of 16 lanes by 8 columns, as the transposing stmatrix wants them (a register pair is two
+// columns of one lane); x[0..15] lanes 0..15, x[16..31] lanes 16..31.  fp32: a lane's 32 columns.
+template <typename O>
+__device__ __forceinline__ void load_out(uint32_t taddr, uint32_t (&x)[32]) {
+  if constexpr (sizeof(O) == 2) {
+    tc05_ld_pieces(taddr, x);
+    tc05_ld_pieces(taddr + (16u << 16), x + 16);
+  } else {
+    tc05_ld32(taddr, x);
+  }
+}
+template <typename O>
+__device__ __forceinline__ void stage_out(uint32_t buf, int lane, const uint32_t (&x)[32], float alpha,
+                                          bool lost) {
+  float y[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) y[i] = lost ? CUDART_NAN_F : __uint_as_float(x[i]) * alpha;
+  if constexpr (sizeof(O) == 2) {
+    // four 8 x 8 pieces a store: lane l gives the place of 8 weight rows (l / 8) in row l % 8; the
+    // 16-byte units of the 64-byte rows are swizzled as the bulk store's map says
+    const uint32_t at = buf + (uint32_t)(lane & 7) * 64 + (uint32_t)(((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t h[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const __nv_bfloat162 b =
+            __floats2bfloat162_rn(y[(q >> 1) * 16 + 4 * g + 2 * (q & 1)], y[(q >> 1) * 16 + 4 * g + 2 * (q & 1) + 1]);
+        h[q] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                       at + (uint32_t)g * 512),
+                   "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(buf + (uint32_t)(i * 128 + lane * 4)), "f"(y[i]) : "memory");
+  }
+}
+// Element (column i, weight row j) of a staging buffer.
+template <typename O>
+__device__ __forceinline__ O staged(uint32_t buf, int i, int j) {
+  if constexpr (sizeof(O) == 2) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];\n"
+                 : "=h"(v)
+                 : "r"(buf + (uint32_t)(i * 64 + (((j >> 3) ^ ((i >> 1) & 3)) << 4) + (j & 7) * 2))
+                 : "memory");
+    return v;
+  } else {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(buf + (uint32_t)(i * 128 + j * 4)) : "memory");
+    return v;
+  }
+}
+__device__ __forceinline__ void bulk_store(const CUtensorMap* tm, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+}
+
 struct LinearJob {
   int R, V;
   int m_tiles, n_tiles, tile_n;
@@ -174,9 +252,11 @@ template <int CG, spec_fp4_format F, typename O>
 __global__ void __launch_bounds__(kFlThreads, 1)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                       const __grid_constant__ CUtensorMap tm_ws,
-                      const __grid_constant__ CUtensorMap tm_as, LinearJob job) {
+                      const __grid_constant__ CUtensorMap tm_as,
+                      const __grid_constant__ CUtensorMap tm_out, LinearJob job) {
   constexpr int kGroups = Fmt<F>::kGroups;
   constexpr uint32_t kSfaBytes = kGroups * kScaleTile;
+  constexpr uint32_t kStageOut = out_stage_bytes<O>();
   __shared__ LinearShared sh;
   extern __shared__ unsigned char fl_dyn[];
   const uint32_t base = (smem_u32(fl_dyn) + 1023u) & ~1023u;
@@ -295,41 +375,46 @@ __global__ void __launch_bounds__(kFlThreads, 1)
     }
   } else if (warp >= 2) {
     // ---------------- epilogue ----------------
-    const int quarter = warp & 3;  // this warp's lanes of tensor memory
-    uint32_t lt = 0;
+    const int quarter = warp & 3;  // this warp's lanes of tensor memory, 32 of the tile's weight rows
+    const uint32_t staging = base + (uint32_t)stages * stage_pitch + (uint32_t)quarter * 2 * kStageOut;
+    uint32_t lt = 0, chunk = 0;
     bool lost = false;
     for (int t = group; t < tiles; t += n_groups, ++lt) {
       const int acc = (int)(lt & 1u);
       if (!lost) lost = !__all_sync(kFull, mbar_wait(&sh.tfull[acc], (lt >> 1) & 1u, limit));
       tc05_fence_after();
-      const int nt = t % job.n_tiles, mt = t / job.n_tiles;
-      const int n0 = nt * job.tile_n, rows = min(job.tile_n, job.R - n0);
-      const int v = (mt * CG + rank) * kFlM + quarter * 32 + lane;
+      const int n0 = (t % job.n_tiles) * job.tile_n, rows = min(job.tile_n, job.R - n0);
+      const int v0 = ((t / job.n_tiles) * CG + rank) * kFlM + quarter * 32;
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kFlMaxN);
-      O* out = static_cast<O*>(job.out) + (int64_t)n0 * job.pitch + v;
 #pragma unroll 1
-      for (int c0 = 0; c0 < rows; c0 += 16) {
-        uint32_t x[16];
-        tc05_ld16(taddr + (uint32_t)c0, x);
+      for (int c0 = 0; c0 < rows; c0 += 32, ++chunk) {
+        const uint32_t buf = staging + (chunk & 1u) * kStageOut;
+        if (lane == 0) bulk_store_wait_read<1>();  // the stores from this buffer have read it
+        __syncwarp();
+        uint32_t x[32];
+        load_out<O>(taddr + (uint32_t)c0, x);
         tc05_wait_ld();
-        tc05_landed16(x);
-        if (v < job.V) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (c0 + i < rows) {
-              const float y = lost ? CUDART_NAN_F : __uint_as_float(x[i]) * job.alpha;
-              if constexpr (sizeof(O) == 2)
-                reinterpret_cast<__nv_bfloat16*>(out)[(int64_t)(c0 + i) * job.pitch] = __float2bfloat16_rn(y);
-              else
-                reinterpret_cast<float*>(out)[(int64_t)(c0 + i) * job.pitch] = y;
-            }
-          }
+        tc05_landed(x);
+        if (c0 + 32 >= rows) {  // the accumulator may be written again
+          tc05_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first<CG>(&sh.tempty[acc]);
+        }
+        stage_out<O>(buf, lane, x, job.alpha, lost);
+        if (v0 + 32 <= job.V) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) bulk_store(&tm_out, buf, v0, n0 + c0);
+        } else {  // a bulk store clips to 16 bytes, the matrix may end within them
+          __syncwarp();
+          if (v0 + lane < job.V)
+            for (int i = 0; i < min(32, rows - c0); ++i)
+              static_cast<O*>(job.out)[(int64_t)(n0 + c0 + i) * job.pitch + v0 + lane] = staged<O>(buf, i, lane);
+          __syncwarp();
         }
       }
-      tc05_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_first<CG>(&sh.tempty[acc]);
     }
+    if (lane == 0) bulk_store_wait();
   }
   __syncwarp();
   tc05_fence_before();
@@ -380,6 +465,20 @@ bool scale_map(CUtensorMap* map, const void* p, int64_t tiles, int n) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The result, boxes of 32 x 32, rows of 64 bytes with that swizzle or of 128 bytes without one.
+template <typename O>
+bool out_map(CUtensorMap* map, void* p, int R, int V, int64_t pitch) {
+  constexpr bool kHalf = sizeof(O) == 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)V, (cuuint64_t)R};
+  const cuuint64_t strides[1] = {(cuuint64_t)pitch * sizeof(O)};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t one[2] = {1, 1};
+  return encode_fn()(map, kHalf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p,
+                     dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     kHalf ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int CG, spec_fp4_format F, typename O>
 cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, const void* w_scales,
                           int K, LinearJob job, cudaStream_t s) {
@@ -394,13 +493,15 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
   job.b_bytes = (uint32_t)box_n * (kFlK / 2);
   const uint32_t stage = (kFlABytes + job.b_bytes + (uint32_t)((1 + job.sf_chunks) * kGroups * kScaleTile) +
                           1023u) & ~1023u;
-  job.stages = (int)((kFlSmemMax - 1024) / stage);
+  constexpr uint32_t kStaging = 4 * 2 * out_stage_bytes<O>();  // two buffers per epilogue warp
+  job.stages = (int)((kFlSmemMax - 1024 - kStaging) / stage);
   if (job.stages > kFlMaxStages) job.stages = kFlMaxStages;
-  const size_t smem = 1024 + (size_t)job.stages * stage;
-  CUtensorMap tm_w, tm_a, tm_ws, tm_as;
+  const size_t smem = 1024 + (size_t)job.stages * stage + kStaging;
+  CUtensorMap tm_w, tm_a, tm_ws, tm_as, tm_out;
   if (!code_map(&tm_w, w, job.V, row_bytes, kFlM) || !code_map(&tm_a, a, job.R, row_bytes, box_n) ||
       !scale_map(&tm_ws, w_scales, (int64_t)fp4_row_tiles(job.V) * job.groups_w, kGroups) ||
-      !scale_map(&tm_as, a_scales, (int64_t)fp4_row_tiles(job.R) * job.groups_a, kGroups))
+      !scale_map(&tm_as, a_scales, (int64_t)fp4_row_tiles(job.R) * job.groups_a, kGroups) ||
+      !out_map<O>(&tm_out, job.out, job.R, job.V, job.pitch))
     return cudaErrorInvalidValue;
   auto kernel = fp4_linear_kernel<CG, F, O>;
   static bool configured[64] = {};
@@ -425,7 +526,7 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, tm_ws, tm_as, job);
+  return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, tm_ws, tm_as, tm_out, job);
 }
 
 template <spec_fp4_format F, typename O>

@@ -101,6 +101,14 @@ __device__ __forceinline__ void tc05_ld16(uint32_t taddr, uint32_t* r) {
                : "r"(taddr)
                : "memory");
 }
+// 32 columns of 16 lanes (from the address's lane on), as four 16 x 8 pieces: r[4 g], r[4 g + 1] columns 8 g + 2 (t % 4)
+// and the next one of lane t / 4, t the thread; r[4 g + 2], r[4 g + 3] of lane t / 4 + 8.
+__device__ __forceinline__ void tc05_ld_pieces(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 " SVK_LIST16 ", [%16];\n"
+               : SVK_R16(SVK_OUT, 0)
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tc05_landed16(uint32_t* r) {
   asm volatile("" : SVK_R16(SVK_TIE, 0));
 }
