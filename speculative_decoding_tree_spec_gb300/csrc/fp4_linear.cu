@@ -229,11 +229,32 @@ __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
 }
 
+// A bounded wait that reads the timer, which takes longer than a stage, only once the barrier has
+// been tried often.
+__device__ __forceinline__ bool fp4_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 4096; ++i)
+    if (mbar_try(bar, parity)) return true;
+  return mbar_wait(bar, parity, limit_ns);
+}
+
+// A place in the ring of stages.
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 struct LinearJob {
   int R, V;
   int m_tiles, n_tiles, tile_n;
   int k_steps, last_mma;  // stages along K, products of the last one
-  int groups_a, groups_w; // scale tiles along K (the same number), rows' tiles start at groups * tile
+  int groups;             // scale tiles along K
   int sf_chunks;          // row tiles of the activations' scales that a tile's rows touch
   int stages;
   uint32_t b_bytes;       // of a stage's activations in one CTA
@@ -263,7 +284,8 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   const uint32_t stage_bytes =
       kFlABytes + job.b_bytes + kSfaBytes + (uint32_t)job.sf_chunks * kSfaBytes;
   const uint32_t stage_pitch = (stage_bytes + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // as a uniform value, so that the roles' loops keep descriptors and addresses in uniform registers
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1u);
   const int group = (int)blockIdx.x / CG, n_groups = (int)gridDim.x / CG;
   const int tiles = job.m_tiles * job.n_tiles;
@@ -286,57 +308,58 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   __syncthreads();
   if (CG > 1) group_sync<CG>();
   tc05_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool stop = false;
-      for (int t = group; t < tiles && !stop; t += n_groups) {
-        const int nt = t % job.n_tiles, mt = t / job.n_tiles;
-        const int n0 = nt * job.tile_n;
-        const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
-        const int row_w = (mt * CG + rank) * kFlM, row_a = n0 + rank * (n / CG);
-        for (int kb = 0; kb < job.k_steps; ++kb, ++it) {
-          const int s = (int)(it % (uint32_t)stages);
-          const uint32_t ph = (it / (uint32_t)stages) & 1u;
-          if (!mbar_wait(&sh.empty[s], ph ^ 1u, limit)) {
-            stop = true;
-            break;
-          }
-          const uint32_t a = base + (uint32_t)s * stage_pitch;
-          const uint32_t bar = CG == 1 ? smem_u32(&sh.full[s]) : first_cta(&sh.full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], CG * stage_bytes);
+    Ring ring;
+    int filled = 0;
+    bool stop = false;
+    for (int t = group; t < tiles && !stop; t += n_groups) {
+      const int n0 = (t % job.n_tiles) * job.tile_n;
+      const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
+      const int row_w = ((t / job.n_tiles) * CG + rank) * kFlM, row_a = n0 + rank * (n / CG);
+      const int tile_w = (row_w >> 7) * job.groups, tile_a = (n0 >> 7) * job.groups;
+      for (int kb = 0; kb < job.k_steps; ++kb, ring.next(stages)) {
+        if (!__all_sync(kFull, fp4_wait(&sh.empty[ring.s], ring.phase ^ 1u, limit))) {
+          stop = true;
+          break;
+        }
+        filled = min(filled + 1, stages);
+        const uint32_t a = base + (uint32_t)ring.s * stage_pitch;
+        const uint32_t sf = a + kFlABytes + job.b_bytes;
+        const uint32_t bar = CG == 1 ? smem_u32(&sh.full[ring.s]) : first_cta(&sh.full[ring.s]);
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[ring.s], CG * stage_bytes);
           fp4_load<CG>(a, &tm_w, kb * (kFlK / 2), row_w, bar);
           fp4_load<CG>(a + kFlABytes, &tm_a, kb * (kFlK / 2), row_a, bar);
-          uint32_t sf = a + kFlABytes + job.b_bytes;
-          fp4_load<CG>(sf, &tm_ws, 0, (row_w >> 7) * job.groups_w + kb * kGroups, bar);
-          for (int j = 0; j < job.sf_chunks; ++j) {
-            sf += kSfaBytes;
-            fp4_load<CG>(sf, &tm_as, 0, ((n0 >> 7) + j) * job.groups_a + kb * kGroups, bar);
-          }
+          fp4_load<CG>(sf, &tm_ws, 0, tile_w + kb * kGroups, bar);
+          fp4_load<CG>(sf + kSfaBytes, &tm_as, 0, tile_a + kb * kGroups, bar);
+          if (job.sf_chunks > 1)
+            fp4_load<CG>(sf + 2 * kSfaBytes, &tm_as, 0, tile_a + job.groups + kb * kGroups, bar);
         }
+        __syncwarp();
       }
-      // the last stages' products are done, and with them their copies
-      const uint32_t first = it > (uint32_t)stages ? it - (uint32_t)stages : 0u;
-      for (uint32_t h = first; h < it; ++h)
-        if (!mbar_wait(&sh.empty[h % (uint32_t)stages], (h / (uint32_t)stages) & 1u, limit)) break;
     }
+    // the last stages' products are done, and with them their copies
+    if (filled < stages) ring = Ring();
+    for (int h = 0; h < filled; ++h, ring.next(stages))
+      if (!__all_sync(kFull, fp4_wait(&sh.empty[ring.s], filled < stages ? 0u : ring.phase ^ 1u, limit))) break;
   } else if (warp == 1 && rank == 0) {
     // ---------------- products ----------------
-    uint32_t it = 0, lt = 0;
+    Ring ring;
+    uint32_t lt = 0, it = 0;
     bool stop = false;
     for (int t = group; t < tiles && !stop; t += n_groups, ++lt) {
       const int acc = (int)(lt & 1u);
-      if (!__all_sync(kFull, mbar_wait(&sh.tempty[acc], ((lt >> 1) & 1u) ^ 1u, limit))) break;
+      if (!__all_sync(kFull, fp4_wait(&sh.tempty[acc], ((lt >> 1) & 1u) ^ 1u, limit))) break;
       tc05_fence_after();
       const int n0 = (t % job.n_tiles) * job.tile_n;
       const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
       const uint32_t d = tmem + (uint32_t)(acc * kFlMaxN);
-      for (int kb = 0; kb < job.k_steps; ++kb, ++it) {
-        const int s = (int)(it % (uint32_t)stages);
-        if (!__all_sync(kFull, mbar_wait(&sh.full[s], (it / (uint32_t)stages) & 1u, limit))) {
+      for (int kb = 0; kb < job.k_steps; ++kb, ring.next(stages), ++it) {
+        const int s = ring.s;
+        if (!__all_sync(kFull, fp4_wait(&sh.full[s], ring.phase, limit))) {
           stop = true;
           break;
         }
@@ -381,7 +404,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
     bool lost = false;
     for (int t = group; t < tiles; t += n_groups, ++lt) {
       const int acc = (int)(lt & 1u);
-      if (!lost) lost = !__all_sync(kFull, mbar_wait(&sh.tfull[acc], (lt >> 1) & 1u, limit));
+      if (!lost) lost = !__all_sync(kFull, fp4_wait(&sh.tfull[acc], (lt >> 1) & 1u, limit));
       tc05_fence_after();
       const int n0 = (t % job.n_tiles) * job.tile_n, rows = min(job.tile_n, job.R - n0);
       const int v0 = ((t / job.n_tiles) * CG + rank) * kFlM + quarter * 32;
@@ -485,7 +508,7 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
   if (!encode_fn()) return cudaErrorNotSupported;
   constexpr int kGroups = Fmt<F>::kGroups;
   const int64_t row_bytes = fp4_row_bytes(K);
-  job.groups_a = job.groups_w = fp4_groups(K, F);
+  job.groups = fp4_groups(K, F);
   job.k_steps = (int)((row_bytes * 2 + kFlK - 1) / kFlK);
   job.last_mma = (int)((row_bytes * 2 - (int64_t)(job.k_steps - 1) * kFlK + 63) / 64);
   job.m_tiles = (job.V + CG * kFlM - 1) / (CG * kFlM);
@@ -499,8 +522,8 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
   const size_t smem = 1024 + (size_t)job.stages * stage + kStaging;
   CUtensorMap tm_w, tm_a, tm_ws, tm_as, tm_out;
   if (!code_map(&tm_w, w, job.V, row_bytes, kFlM) || !code_map(&tm_a, a, job.R, row_bytes, box_n) ||
-      !scale_map(&tm_ws, w_scales, (int64_t)fp4_row_tiles(job.V) * job.groups_w, kGroups) ||
-      !scale_map(&tm_as, a_scales, (int64_t)fp4_row_tiles(job.R) * job.groups_a, kGroups) ||
+      !scale_map(&tm_ws, w_scales, (int64_t)fp4_row_tiles(job.V) * job.groups, kGroups) ||
+      !scale_map(&tm_as, a_scales, (int64_t)fp4_row_tiles(job.R) * job.groups, kGroups) ||
       !out_map<O>(&tm_out, job.out, job.R, job.V, job.pitch))
     return cudaErrorInvalidValue;
   auto kernel = fp4_linear_kernel<CG, F, O>;
