@@ -38,25 +38,42 @@ struct QuantJob {
   uint8_t* scales;
 };
 
-// Elements c .. c + 7 of a row; 0 from K on.
+// Elements c .. c + 7 of a row as they are stored; 0 from K on.
 template <typename T>
-__device__ __forceinline__ void load8(const void* row, int c, int K, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    if (c + 8 <= K) {
-      Elt<T>::unpack(__ldg(reinterpret_cast<const uint4*>(row) + c / 8), f);
-      return;
-    }
-  } else {
-    if (c + 8 <= K) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row) + c / 4);
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row) + c / 4 + 1);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-      return;
+struct Raw8 {
+  static constexpr int kUnits = sizeof(T) / 2;
+  uint4 u[kUnits];
+};
+template <typename T>
+__device__ __forceinline__ void load8(const void* row, int c, int K, Raw8<T>& x) {
+  constexpr int U = Raw8<T>::kUnits;
+  if (c + 8 <= K) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) x.u[i] = __ldcs(reinterpret_cast<const uint4*>(row) + c / 8 * U + i);
+    return;
+  }
+  uint32_t w[4 * U];
+#pragma unroll
+  for (int q = 0; q < 4 * U; ++q) {
+    if constexpr (sizeof(T) == 2) {
+      const uint16_t* p = static_cast<const uint16_t*>(row) + c + 2 * q;
+      w[q] = (c + 2 * q < K ? (uint32_t)p[0] : 0u) | (c + 2 * q + 1 < K ? (uint32_t)p[1] << 16 : 0u);
+    } else {
+      w[q] = c + q < K ? static_cast<const uint32_t*>(row)[c + q] : 0u;
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = c + e < K ? Elt<T>::at(row, c + e) : 0.f;
+  for (int i = 0; i < U; ++i) x.u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& x, float (&f)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    Elt<T>::unpack(x.u[0], f);
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(&x.u[0]), b = *reinterpret_cast<const float4*>(&x.u[1]);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
 }
 
 __device__ __forceinline__ float abs_max_nan(float a, float b) {
@@ -107,46 +124,49 @@ __device__ __forceinline__ uint32_t encode8(float (&f)[8], float top, float ts, 
 }
 
 template <typename T, spec_fp4_format F>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(QuantJob job) {
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 6 : 5) quantize_kernel(QuantJob job) {
   constexpr int kLanes = F == SPEC_FP4_MX ? 4 : 2;  // lanes of a block
+  constexpr int kRows = sizeof(T) == 2 ? kQRows : kQRows / 2;  // in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t tile = blockIdx.x / (unsigned)job.segments;
   const int c = (int)(blockIdx.x % (unsigned)job.segments) * kQTileCols + lane * 8;
   const int K = job.K;
-  const int r0 = (int)(tile * kQTileRows) + warp;
   const int g = c / (kLanes * 32);  // this lane's scale tile along the row
-  float f[kQRows][8];
+  for (int i0 = 0; i0 < kQRows; i0 += kRows) {
+    const int r0 = (int)(tile * kQTileRows) + i0 * (kQThreads / 32) + warp;
+    Raw8<T> raw[kRows];
 #pragma unroll
-  for (int i = 0; i < kQRows; ++i) {
-    const int r = r0 + i * (kQThreads / 32);
-    if (r < job.R && c < K) {
-      load8<T>(static_cast<const char*>(job.x) + (int64_t)r * job.pitch_bytes, c, K, f[i]);
-    } else {
+    for (int i = 0; i < kRows; ++i) {
+      const int r = r0 + i * (kQThreads / 32);
+      if (r < job.R && c < K) {
+        load8<T>(static_cast<const char*>(job.x) + (int64_t)r * job.pitch_bytes, c, K, raw[i]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+        for (int u = 0; u < Raw8<T>::kUnits; ++u) raw[i].u[u] = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < kQRows; ++i) {
-    const int r = r0 + i * (kQThreads / 32);
-    float top = 0.f;
+    for (int i = 0; i < kRows; ++i) {
+      const int r = r0 + i * (kQThreads / 32);
+      float f[8];
+      unpack8<T>(raw[i], f);
+      float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = abs_max_nan(top, f[i][e]);
+      for (int e = 0; e < 8; ++e) top = abs_max_nan(top, f[e]);
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) top = abs_max_nan(top, __shfl_xor_sync(kFull, top, o));
-    uint32_t byte;
-    const uint32_t codes = encode8<F>(f[i], top, job.ts, byte);
-    if (r < job.R && c < 2 * job.row_bytes)
-      *reinterpret_cast<uint32_t*>(job.codes + (int64_t)r * job.row_bytes + c / 2) = codes;
-    // the four scales of a tile's row as one word; past the row's end, and in rows past the
-    // last, they are zero
-    if (c >= K || r >= job.R) byte = 0u;
-    uint32_t word = byte;
-    word |= __shfl_down_sync(kFull, byte, kLanes) << 8;
-    word |= __shfl_down_sync(kFull, byte, 2 * kLanes) << 16;
-    word |= __shfl_down_sync(kFull, byte, 3 * kLanes) << 24;
-    if (lane % (4 * kLanes) == 0 && g < job.groups)
-      *reinterpret_cast<uint32_t*>(job.scales + fp4_scale_at(r, 4 * g, job.groups)) = word;
+      for (int o = 1; o < kLanes; o <<= 1) top = abs_max_nan(top, __shfl_xor_sync(kFull, top, o));
+      uint32_t byte;
+      const uint32_t codes = encode8<F>(f, top, job.ts, byte);
+      if (r < job.R && c < 2 * job.row_bytes)
+        *reinterpret_cast<uint32_t*>(job.codes + (int64_t)r * job.row_bytes + c / 2) = codes;
+      // the four scales of a tile's row as one word; past the row's end, and in rows past the
+      // last, they are zero
+      if (c >= K || r >= job.R) byte = 0u;
+      byte |= __shfl_down_sync(kFull, byte, kLanes) << 8;
+      byte |= __shfl_down_sync(kFull, byte, 2 * kLanes) << 16;
+      if (lane % (4 * kLanes) == 0 && g < job.groups)
+        *reinterpret_cast<uint32_t*>(job.scales + fp4_scale_at(r, 4 * g, job.groups)) = byte;
+    }
   }
 }
 
