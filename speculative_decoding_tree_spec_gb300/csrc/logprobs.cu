@@ -29,13 +29,16 @@ namespace svk {
 
 namespace {
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 256;  // at most, of a CTA of the row kernel; 1024 per SM
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpPerSm = 4;   // resident CTAs of the row kernel
-constexpr int kLpUnits = 4;   // 16-byte units per lane in a chunk
+constexpr int kLpPerSm = 3;     // CTAs of that size that fit an SM
+constexpr int kLpUnits = 4;      // 16-byte units per lane in a load
 constexpr int kLpMaxK = 32;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpSmallV = 1024;
+constexpr int kLpCand = 256;     // elements ranked by counting
+constexpr int kLpFineV = 32768;
+constexpr int kLpCount = 512;    // chunks ranked by counting
 
 struct LogprobJob {
   const void* base;
@@ -150,13 +153,13 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-// The lane's units of a chunk; what lies past the row is -inf.
+// The lane's units of the row's `at`-th load (2 KB of a warp); what lies past the row is -inf.
 template <typename T>
-__device__ __forceinline__ void load_chunk(const void* row, int V, int chunk, int lane,
+__device__ __forceinline__ void load_units(const void* row, int V, int at, int lane,
                                            uint4 (&raw)[kLpUnits]) {
   constexpr int E = Elt<T>::kPerUnit;
   constexpr uint32_t kNegInf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-  const int u0 = chunk * (32 * kLpUnits);
+  const int u0 = at * (32 * kLpUnits);
   const int full = V / E;
   if (u0 + 32 * kLpUnits <= full) {
 #pragma unroll
@@ -188,24 +191,26 @@ __device__ __forceinline__ void load_chunk(const void* row, int V, int chunk, in
   }
 }
 
-// NaN-propagating maximum of the lane's units.
+// NaN-propagating maximum of `n` of the lane's units from j0 on (constants where it is called).
 template <typename T>
-__device__ __forceinline__ float chunk_max(const uint4 (&raw)[kLpUnits]) {
+__device__ __forceinline__ float units_max(const uint4 (&raw)[kLpUnits], int j0, int n) {
   if constexpr (sizeof(T) == 2) {
-    __nv_bfloat162 m2 = *reinterpret_cast<const __nv_bfloat162*>(&raw[0].x);
+    uint32_t none = 0xFF80FF80u;
+    __nv_bfloat162 m2 = *reinterpret_cast<const __nv_bfloat162*>(&none);
 #pragma unroll
     for (int j = 0; j < kLpUnits; ++j) {
+      if (j < j0 || j >= j0 + n) continue;
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-      for (int q = (j == 0 ? 1 : 0); q < 4; ++q)
-        m2 = __hmax2_nan(m2, *reinterpret_cast<const __nv_bfloat162*>(&w[q]));
+      for (int q = 0; q < 4; ++q) m2 = __hmax2_nan(m2, *reinterpret_cast<const __nv_bfloat162*>(&w[q]));
     }
     const float lo = __low2float(m2), hi = __high2float(m2);
     return (lo != lo || hi != hi) ? CUDART_NAN_F : fmaxf(lo, hi);
   } else {
-    float m = __uint_as_float(raw[0].x);
+    float m = -CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < kLpUnits; ++j) {
+      if (j < j0 || j >= j0 + n) continue;
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -218,7 +223,7 @@ __device__ __forceinline__ float chunk_max(const uint4 (&raw)[kLpUnits]) {
 // Sums of 2^a and a 2^a over the lane's units, a = (z - m) c.  Weights that vanish (z = -inf)
 // would make the second sum NaN: kMasked bounds a from below, which leaves those weights 0.
 template <typename T, bool kMasked>
-__device__ __forceinline__ void chunk_sums(const uint4 (&raw)[kLpUnits], float m, float c, float& s,
+__device__ __forceinline__ void units_sums(const uint4 (&raw)[kLpUnits], float m, float c, float& s,
                                            float& aw) {
   constexpr int E = Elt<T>::kPerUnit;
   const float2 nm = make_float2(-m, -m), c2 = make_float2(c, c);
@@ -247,57 +252,85 @@ __device__ __forceinline__ void chunk_sums(const uint4 (&raw)[kLpUnits], float m
   aw = a0.x + a0.y;
 }
 
-template <typename T>
+// One key of a chunk per load of it (kSub 1) or per 512 bytes (kSub kLpUnits).
+template <typename T, int kSub>
 __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(LogprobJob job) {
   constexpr int E = Elt<T>::kPerUnit;
-  extern __shared__ uint32_t s_key[];  // [n_chunks] order key of each chunk's largest logit
+  constexpr int kKeyUnits = kLpUnits / kSub;  // units per lane that share a key
+  extern __shared__ __align__(16) uint32_t s_key[];  // [n_chunks kSub, rounded up to 4] order key of each
+                                                     // chunk's largest logit
   __shared__ Part s_part[kLpMaxCluster * kLpWarps];
   __shared__ uint32_t s_bad;
-  __shared__ uint64_t s_list[kLpWarps][32];
-  __shared__ int s_sel[kLpMaxK];
+  __shared__ uint64_t s_list[kLpCand];  // candidates, or a list of 32 per warp
+  __shared__ int s_sel[kLpMaxK], s_count;
   __shared__ uint32_t s_tau;
   __shared__ float s_m, s_log;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int C = job.cluster;
+  const int C = job.cluster, W = (int)blockDim.x >> 5;
   const int rank = blockIdx.x % C, r = blockIdx.x / C;
   const int n = row_of(job, r);
   if (n < 0) {  // the whole cluster agrees
-    if (rank == 0) write_nothing(job, r, threadIdx.x, kLpThreads, -CUDART_INF_F, 0.f, SPEC_ROW_NONE);
+    if (rank == 0) write_nothing(job, r, threadIdx.x, blockDim.x, -CUDART_INF_F, 0.f, SPEC_ROW_NONE);
     return;
   }
   const void* row = static_cast<const char*>(job.base) + (int64_t)n * job.pitch_bytes;
   const int V = job.V, k = job.k;
   const float c = job.c;
-  const int step = C * kLpWarps;
-  int ch = rank * kLpWarps + warp;
+  // loads of a chunk: 1024 logits
+  constexpr int loads = kSub > 1 ? 1 : 1024 / (32 * kLpUnits * E);
+  const int n_loads = job.n_chunks * loads;
+  // this warp's loads: chunk by chunk, C W chunks apart
+  int at = (rank * W + warp) * loads;
+  [[maybe_unused]] int left = loads;
+  const int skip = (C * W - 1) * loads;
 
   uint4 nxt[kLpUnits];
-  if (ch < job.n_chunks) load_chunk<T>(row, V, ch, lane, nxt);
-  if (threadIdx.x == 0) s_bad = 0u;
-  if (C > 1) cluster_arrive();  // the first CTA is there, its word cleared
+  if (at < n_loads) load_units<T>(row, V, at, lane, nxt);
+  if (threadIdx.x == 0) {
+    s_bad = 0u;
+    s_count = 0;
+  }
+  if (C > 1) cluster_arrive();  // the first CTA is there, its words cleared
   else __syncthreads();
   bool arrived = C > 1;
 
   float m = -CUDART_INF_F;
   Kahan S, A;
   int bad = 0;
+  uint32_t top = 0u;
   const uint32_t key0 = C > 1 ? cluster_addr(s_key, 0) : 0u;
-  for (; ch < job.n_chunks; ch += step) {
+  while (at < n_loads) {
     uint4 raw[kLpUnits];
 #pragma unroll
     for (int j = 0; j < kLpUnits; ++j) raw[j] = nxt[j];
-    if (ch + step < job.n_chunks) load_chunk<T>(row, V, ch + step, lane, nxt);
-    const float um = chunk_max<T>(raw);
+    const int done = at;
+    ++at;
+    bool last = true;  // of its chunk
+    if constexpr (loads > 1) last = --left == 0;
+    if (last) {
+      at += skip;
+      left = loads;
+    }
+    if (at < n_loads) load_units<T>(row, V, at, lane, nxt);
+    const float um = units_max<T>(raw, 0, kLpUnits);
     bad |= (um != um);
     if (k > 0) {
-      const uint32_t top = __reduce_max_sync(kFull, order_key(um));
       if (arrived) {
         cluster_wait();
         arrived = false;
       }
-      if (lane == 0) {
-        if (C > 1) cluster_put(key0 + 4u * (uint32_t)ch, top);
-        else s_key[ch] = top;
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) {
+        top = max(top, order_key(kSub == 1 ? um : units_max<T>(raw, j * kKeyUnits, kKeyUnits)));
+        if (kSub > 1 || last) {
+          top = __reduce_max_sync(kFull, top);
+          const int i = kSub > 1 ? done * kSub + j : done / loads;
+          if (lane == 0) {
+            if (C > 1) cluster_put(key0 + 4u * (uint32_t)i, top);
+            else s_key[i] = top;
+          }
+          top = 0u;
+        }
       }
     }
     if (um > m) {
@@ -314,8 +347,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     }
     if (m != -CUDART_INF_F) {
       float s, a;
-      chunk_sums<T, false>(raw, m, c, s, a);
-      if (a != a) chunk_sums<T, true>(raw, m, c, s, a);
+      units_sums<T, false>(raw, m, c, s, a);
+      if (a != a) units_sums<T, true>(raw, m, c, s, a);
       S.add(s);
       A.add(a);
     }
@@ -332,35 +365,78 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
   p = warp_join(p, c);
   bad = __any_sync(kFull, bad);
   if (lane == 0) {
-    const int at = rank * kLpWarps + warp;
+    const int i = rank * W + warp;
     if (C > 1) {
-      const uint32_t d = cluster_addr(&s_part[at], 0);
+      const uint32_t d = cluster_addr(&s_part[i], 0);
       cluster_put(d, __float_as_uint(p.m));
       cluster_put(d + 4, __float_as_uint(p.s_hi));
       cluster_put(d + 8, __float_as_uint(p.s_lo));
       cluster_put(d + 12, __float_as_uint(p.a));
       if (bad) cluster_put(cluster_addr(&s_bad, 0), 1u);
     } else {
-      s_part[at] = p;
+      s_part[i] = p;
       if (bad) s_bad = 1u;
     }
   }
   if (C > 1) {
     cluster_arrive();
-    if (rank != 0) {
-      cluster_wait();
-      return;
-    }
     cluster_wait();
+    if (rank != 0) return;
   } else {
     __syncthreads();
   }
 
-  // warp 0: the row's sums; warp 1: the k chunks with the largest maxima, in that order
-  const int kk = min(k, job.n_chunks);
+  // the k chunks with the largest maxima, in that order
+  const int n_keys = job.n_chunks * kSub, kk = min(k, n_keys);
+  if (kk > 0 && n_keys <= kLpCount) {
+    // a chunk's place is the number of chunks before it: larger ones, and equal ones to its left
+    for (int i = threadIdx.x; i < n_keys; i += blockDim.x) {
+      const uint32_t mine = s_key[i];
+      int before = 0;
+      for (int j = 0; j < n_keys; j += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&s_key[j]);
+        // of four chunks to the left an equal one counts, of four to the right it does not
+        const uint32_t than = j + 3 < i ? mine - 1u : mine;
+        before += (o.x > than) + (j + 1 < n_keys && o.y > than) + (j + 2 < n_keys && o.z > than) +
+                  (j + 3 < n_keys && o.w > than);
+      }
+      // the four around it
+      for (int j = i & ~3; j < i; ++j) before += s_key[j] == mine;
+      if (before < kk) {
+        s_sel[before] = i;
+        if (before == kk - 1) s_tau = kk == k ? mine : 0u;  // with fewer chunks than k, every element counts
+      }
+    }
+  } else if (kk > 0 && warp == W - 1) {
+    uint32_t best = 0u;
+    int where = INT_MAX;
+    auto look = [&]() {
+      best = 0u;
+      where = INT_MAX;
+      for (int i = lane; i < n_keys; i += 32)
+        if (s_key[i] > best) {
+          best = s_key[i];
+          where = i;
+        }
+    };
+    look();
+    uint32_t most = 0u;
+    for (int j = 0; j < kk; ++j) {
+      most = __reduce_max_sync(kFull, best);
+      const int i = __reduce_min_sync(kFull, best == most ? where : INT_MAX);
+      if (lane == 0) s_sel[j] = i;
+      if (where == i) {
+        s_key[i] = 0u;
+        look();
+      }
+    }
+    if (lane == 0) s_tau = kk == k ? most : 0u;
+  }
+  // the row's sums
   if (warp == 0) {
-    Part q = lane < step ? s_part[lane] : part_none();
-    if (lane + 32 < step) {
+    const int parts = C * W;
+    Part q = lane < parts ? s_part[lane] : part_none();
+    if (lane + 32 < parts) {
       Part o = s_part[lane + 32];
       const float M = fmaxf(q.m, o.m);
       part_raise(q, M, c);
@@ -385,65 +461,87 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
         if (job.out_status) job.out_status[r] = SPEC_TREE_OK;
       }
     }
-  } else if (warp == 1 && kk > 0) {
-    uint32_t best = 0u;
-    int at = INT_MAX;
-    auto look = [&]() {
-      best = 0u;
-      at = INT_MAX;
-      for (int i = lane; i < job.n_chunks; i += 32)
-        if (s_key[i] > best) {
-          best = s_key[i];
-          at = i;
-        }
-    };
-    look();
-    uint32_t top = 0u;
-    for (int j = 0; j < kk; ++j) {
-      top = __reduce_max_sync(kFull, best);
-      const int i = __reduce_min_sync(kFull, best == top ? at : INT_MAX);
-      if (lane == 0) s_sel[j] = i;
-      if (at == i) {
-        s_key[i] = 0u;
-        look();
-      }
-    }
-    if (lane == 0) s_tau = kk == k ? top : 0u;  // with fewer chunks than k, every element counts
   }
   __syncthreads();
   const float M = s_m, log_s = s_log;
   if (log_s != log_s) {
-    write_nothing(job, r, threadIdx.x, kLpThreads, CUDART_NAN_F, CUDART_NAN_F, SPEC_ROW_NONFINITE);
+    write_nothing(job, r, threadIdx.x, blockDim.x, CUDART_NAN_F, CUDART_NAN_F, SPEC_ROW_NONFINITE);
     return;
   }
-  write_given<T>(job, row, r, threadIdx.x, kLpThreads, M, log_s);
-  if (k == 0) return;
+  if (k == 0) {
+    write_given<T>(job, row, r, threadIdx.x, blockDim.x, M, log_s);
+    return;
+  }
 
-  // the selected chunks' elements at or above the last one's maximum, into a list per warp
+  // the elements at or above the k-th chunk's maximum, of the k chunks
   const uint32_t tau = s_tau;
+  const int key_loads = kSub > 1 ? 1 : loads;
+  const int total = kk * key_loads;
+  auto look_at = [&](int i) {  // the i-th piece of the selected chunks: its load
+    const int sel = s_sel[i / key_loads];
+    return kSub > 1 ? sel / kSub : sel * loads + i % key_loads;
+  };
+  if (warp < total) load_units<T>(row, V, look_at(warp), lane, nxt);
+  write_given<T>(job, row, r, threadIdx.x, blockDim.x, M, log_s);
+  for (int i = warp; i < total; i += W) {
+    uint4 raw[kLpUnits];
+#pragma unroll
+    for (int j = 0; j < kLpUnits; ++j) raw[j] = nxt[j];
+    const int l = look_at(i);
+    if (i + W < total) load_units<T>(row, V, look_at(i + W), lane, nxt);
+    const int only = kSub > 1 ? s_sel[i] % kSub : 0;
+#pragma unroll
+    for (int j = 0; j < kLpUnits; ++j) {
+      if (kSub > 1 && j != only) continue;  // kSub is kLpUnits: one unit per key
+      if (order_key(units_max<T>(raw, j, 1)) < tau) continue;
+      float f[E];
+      Elt<T>::unpack(raw[j], f);
+      const int i0 = (l * (32 * kLpUnits) + j * 32 + lane) * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (order_key(f[e]) >= tau && i0 + e < V) {
+          const int slot = atomicAdd(&s_count, 1);
+          if (slot < kLpCand)
+            s_list[slot] = ((uint64_t)order_key(f[e]) << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)(i0 + e));
+        }
+    }
+  }
+  __syncthreads();
+  const int found = s_count;
+  if (found <= kLpCand) {  // a candidate's place is the number of larger ones
+    for (int i = threadIdx.x; i < found; i += blockDim.x) {
+      const uint64_t mine = s_list[i];
+      int before = 0;
+      for (int j = 0; j < found; ++j) before += s_list[j] > mine;
+      if (before < k) {
+        const float z = key_value((uint32_t)(mine >> 32));
+        job.out_top[(int64_t)r * k + before] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
+        job.out_top_lp[(int64_t)r * k + before] = (z - M) * job.inv_t - log_s;
+      }
+    }
+    return;
+  }
+
+  // many equal ones: each warp keeps a list of its k largest
+  __syncthreads();
   uint64_t L = 0ull;
-  for (int j = warp; j < kk; j += kLpWarps) {
-    const int chunk = s_sel[j];
-    load_chunk<T>(row, V, chunk, lane, nxt);
+  for (int i = warp; i < total; i += W) {
+    const int l = look_at(i), only = kSub > 1 ? s_sel[i] % kSub : -1;
+    load_units<T>(row, V, l, lane, nxt);
 #pragma unroll 1
     for (int u = 0; u < kLpUnits; ++u) {
+      if (only >= 0 && u != only) continue;
       const uint4 x = u == 0 ? nxt[0] : u == 1 ? nxt[1] : u == 2 ? nxt[2] : nxt[3];
       float f[E];
       Elt<T>::unpack(x, f);
-      float um = f[0];
-#pragma unroll
-      for (int e = 1; e < E; ++e) um = fmaxf(um, f[e]);
-      if (!__any_sync(kFull, order_key(um) >= tau)) continue;
-      const int i0 = (chunk * (32 * kLpUnits) + u * 32 + lane) * E;
+      const int i0 = (l * (32 * kLpUnits) + u * 32 + lane) * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const uint32_t o = order_key(f[e]);
         const uint64_t key = ((uint64_t)o << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)(i0 + e));
-        uint32_t who = __ballot_sync(kFull, o >= tau && i0 + e < V);
-        if (who == 0u) continue;
         const uint64_t lk = __shfl_sync(kFull, L, k - 1);
-        const bool in = ((who >> lane) & 1u) && key > lk;
-        who = __ballot_sync(kFull, in);
+        const bool in = o >= tau && i0 + e < V && key > lk;
+        uint32_t who = __ballot_sync(kFull, in);
         if (__popc(who) <= 6) {
           while (who) {
             const int src = __ffs(who) - 1;
@@ -456,10 +554,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
       }
     }
   }
-  s_list[warp][lane] = L;
+  s_list[warp * 32 + lane] = L;
   __syncthreads();
   if (warp == 0) {
-    for (int w = 1; w < min(kLpWarps, kk); ++w) L = list_merge(L, s_list[w][lane], lane);
+    for (int w = 1; w < W; ++w) L = list_merge(L, s_list[w * 32 + lane], lane);
     if (lane < k) {
       const float z = key_value((uint32_t)(L >> 32));
       job.out_top[(int64_t)r * k + lane] = (int32_t)(0xFFFFFFFFu - (uint32_t)L);
@@ -560,17 +658,23 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
     else logprob_small_kernel<T, 32><<<blocks, kLpThreads, 0, s>>>(job);
     return cudaGetLastError();
   }
-  const int per_chunk = 32 * kLpUnits * Elt<T>::kPerUnit;
+  const int per_load = 32 * kLpUnits * Elt<T>::kPerUnit;
+  // a chunk is 1024 logits; a key per 512 bytes where that leaves few chunks
+  const bool fine = job.V <= kLpFineV;
+  const int per_chunk = fine ? per_load : 1024;
   job.n_chunks = (job.V + per_chunk - 1) / per_chunk;
-  // as many CTAs per row as leave every row resident at once and each warp a chunk
-  const int room = device_sm_count() * kLpPerSm;
-  int C = 1;
-  while (C < kLpMaxCluster && (int64_t)job.R * C * 2 <= room && C * kLpWarps < job.n_chunks) C *= 2;
+  const int n_keys = job.n_chunks * (fine ? kLpUnits : 1);
+  // warps per row that leave every row resident at once
+  const int room = device_sm_count() * kLpPerSm * kLpWarps;
+  int W = 1, C = 1;
+  while (W < kLpWarps && (int64_t)job.R * W * 2 <= room && W < job.n_chunks) W *= 2;
+  while (C < kLpMaxCluster && (int64_t)job.R * W * C * 2 <= room && C * W < job.n_chunks) C *= 2;
+  int threads = 32 * W;
   job.cluster = C;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(job.R * C));
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.dynamicSmemBytes = job.k > 0 ? (size_t)job.n_chunks * 4 : 0;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = job.k > 0 ? ((size_t)n_keys + 3) / 4 * 16 : 0;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -578,7 +682,7 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, logprob_rows_kernel<T>, job);
+  return cudaLaunchKernelEx(&cfg, fine ? logprob_rows_kernel<T, kLpUnits> : logprob_rows_kernel<T, 1>, job);
 }
 
 }  // namespace
