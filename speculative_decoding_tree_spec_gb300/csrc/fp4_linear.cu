@@ -52,19 +52,22 @@ __device__ __forceinline__ uint32_t fp4_idesc(int m, int n, int sf) {
   return (1u << 7) | (1u << 10) | ((uint32_t)sf << 4) | ((uint32_t)(n >> 3) << 17) |
          ((F == SPEC_FP4_MX ? 1u : 0u) << 23) | ((uint32_t)(m >> 4) << 24) | ((uint32_t)sf << 29);
 }
-// 32 rows of 16 bytes, without a swizzle: 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
-  return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1u << 46);
-}
+// Shared-memory descriptors, of which the low word changes from one to the next (by bytes / 16): scales,
+// 32 rows of 16 bytes without a swizzle, 8-row groups 128 bytes apart; codes, rows of 128 bytes with
+// that swizzle (sw128_tile).
+constexpr uint32_t kScaleDescHigh = (128u >> 4) | (1u << 14);
+constexpr uint32_t kCodeDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kCodeDescLow = (16u >> 4) << 16;
 
 template <int CG, spec_fp4_format F>
-__device__ __forceinline__ void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void fp4_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                         uint32_t sfa, uint32_t sfb, bool accumulate) {
 #define SVK_FP4_MMA(GROUP, KIND)                                                               \
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"                                   \
-               " tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" \
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb),                       \
-               "r"((uint32_t)accumulate)                                                       \
+  asm volatile("{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n"                \
+               " mov.b64 x, {%1, %7};\n mov.b64 y, {%2, %7};\n"                               \
+               " tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], x, y, %3, [%4], [%5], p;\n}\n" \
+               ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb),                       \
+               "r"((uint32_t)accumulate), "n"(kCodeDescHigh)                                   \
                : "memory")
   if constexpr (F == SPEC_FP4_MX) {
     if constexpr (CG == 1) SVK_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
@@ -76,11 +79,15 @@ __device__ __forceinline__ void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint
 #undef SVK_FP4_MMA
 }
 template <int CG>
-__device__ __forceinline__ void scales_to_tmem(uint32_t d, uint64_t desc) {
+__device__ __forceinline__ void scales_to_tmem(uint32_t d, uint32_t desc) {
   if constexpr (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(d), "l"(desc) : "memory");
+    asm volatile("{\n .reg .b64 x;\n mov.b64 x, {%1, %2};\n tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], x;\n}\n" ::"r"(d),
+                 "r"(desc), "n"(kScaleDescHigh)
+                 : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(d), "l"(desc) : "memory");
+    asm volatile("{\n .reg .b64 x;\n mov.b64 x, {%1, %2};\n tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], x;\n}\n" ::"r"(d),
+                 "r"(desc), "n"(kScaleDescHigh)
+                 : "memory");
 }
 // Arrives on the barrier (both CTAs' at CG 2) once the products issued so far are done.
 template <int CG>
@@ -349,6 +356,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
     // ---------------- products ----------------
     Ring ring;
     uint32_t lt = 0, it = 0;
+    const uint32_t sf_col = tmem + kFlSfCol;  // a multiple of both buffers
     bool stop = false;
     for (int t = group; t < tiles && !stop; t += n_groups, ++lt) {
       const int acc = (int)(lt & 1u);
@@ -357,6 +365,23 @@ __global__ void __launch_bounds__(kFlThreads, 1)
       const int n0 = (t % job.n_tiles) * job.tile_n;
       const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
       const uint32_t d = tmem + (uint32_t)(acc * kFlMaxN);
+      const uint32_t off_b = (uint32_t)(n0 & 127) >> 5;
+      const uint32_t idesc0 = fp4_idesc<F>(kFlM * CG, n, 0), idesc2 = fp4_idesc<F>(kFlM * CG, n, 2);
+      // the products of a stage; of the last one those that K reaches.  `step`: columns of a group's
+      // activation scales.  The next 64 elements are 32 bytes further along the swizzled rows.
+      auto issue = [&](uint32_t d, uint32_t a, uint32_t sfa, uint32_t sfb, int step, int kb) {
+        const uint32_t b = a + (kFlABytes >> 4);
+        const int products = kb + 1 == job.k_steps ? job.last_mma : 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < products) {
+            const int g = F == SPEC_FP4_MX ? j >> 1 : j;
+            fp4_mma<CG, F>(d, (a + j * 2) | kCodeDescLow, (b + j * 2) | kCodeDescLow,
+                           F == SPEC_FP4_MX && (j & 1) ? idesc2 : idesc0, sfa + g * 4, sfb + g * step,
+                           (kb | j) != 0);
+          }
+        }
+      };
       for (int kb = 0; kb < job.k_steps; ++kb, ring.next(stages), ++it) {
         const int s = ring.s;
         if (!__all_sync(kFull, fp4_wait(&sh.full[s], ring.phase, limit))) {
@@ -364,31 +389,24 @@ __global__ void __launch_bounds__(kFlThreads, 1)
           break;
         }
         tc05_fence_after();
-        const uint32_t a = base + (uint32_t)s * stage_pitch;
-        const uint32_t sf = a + kFlABytes + job.b_bytes;
-        const uint32_t sfa = tmem + kFlSfCol + (it & 1u) * kFlSfBuf, sfb = sfa + kFlSfB;
-        const uint64_t adesc = sw128_tile(a, 16), bdesc = sw128_tile(a + kFlABytes, 16);
-        const int products = kb + 1 == job.k_steps ? job.last_mma : 4;
+        const uint32_t a = (base + (uint32_t)s * stage_pitch) >> 4;
+        const uint32_t sf = a + ((kFlABytes + job.b_bytes) >> 4);
+        const uint32_t sfa = sf_col ^ ((it & 1u) * kFlSfBuf), sfb = sfa + kFlSfB;
         if (elect_one()) {
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g)
-            scales_to_tmem<CG>(sfa + (uint32_t)g * 4, scale_desc(sf + (uint32_t)g * kScaleTile));
-          for (int j = 0; j < job.sf_chunks; ++j)
+          for (int g = 0; g < kGroups; ++g) scales_to_tmem<CG>(sfa + g * 4, sf + g * (kScaleTile >> 4));
+          if (job.sf_chunks == 1) {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
-              scales_to_tmem<CG>(sfb + (uint32_t)(g * job.sf_chunks + j) * 4,
-                                 scale_desc(sf + (uint32_t)((1 + j) * kGroups + g) * kScaleTile));
-          const uint32_t off_b = (uint32_t)(n0 & 127) >> 5;
+              scales_to_tmem<CG>(sfb + g * 4, sf + (kGroups + g) * (kScaleTile >> 4));
+            issue(d, a, sfa, sfb + off_b, 4, kb);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j < products) {
-              const int g = F == SPEC_FP4_MX ? j >> 1 : j;
-              const int id = F == SPEC_FP4_MX ? (j & 1) * 2 : 0;
-              // the next 64 elements are 32 bytes further along the swizzled rows
-              fp4_mma<CG, F>(d, adesc + (uint64_t)(j * 2), bdesc + (uint64_t)(j * 2),
-                             fp4_idesc<F>(kFlM * CG, n, id), sfa + (uint32_t)g * 4,
-                             sfb + (uint32_t)(g * job.sf_chunks) * 4 + off_b, (kb | j) != 0);
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int g = 0; g < kGroups; ++g)
+                scales_to_tmem<CG>(sfb + (g * 2 + j) * 4, sf + ((1 + j) * kGroups + g) * (kScaleTile >> 4));
+            issue(d, a, sfa, sfb + off_b, 8, kb);
           }
           fp4_commit<CG>(&sh.empty[s]);
           if (kb + 1 == job.k_steps) fp4_commit<CG>(&sh.tfull[acc]);
