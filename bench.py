@@ -71,6 +71,9 @@ def parse_args():
     ap.add_argument("--fused", action="store_true",
                     help="with --op draft: the draft LM head + top-k in one call (features x "
                          "weight on the tensor cores, then the ranking kernel)")
+    ap.add_argument("--head", choices=["bf16", "mx", "nv"], default="bf16",
+                    help="with --op draft --fused: the draft head's format, bf16 or one of the "
+                         "block-scaled 4-bit formats")
     ap.add_argument("--per-request", action="store_true",
                     help="per-request sampling parameters: the trees cycle through greedy, the "
                          "workload's own setting, top-k 50 at T=1 and top-p 0.8 at T=0.5 "
@@ -920,17 +923,30 @@ def run_draft_fused(args):
     g.manual_seed(shard_seed(args.seed, rank))
     feats = torch.randn((R, d), generator=g, device=dev).to(torch.bfloat16)
     weight = (torch.randn((V, d), generator=g, device=dev) * 0.02).to(torch.bfloat16)
-    ws = torch.empty(int(binding.lib().spec_draft_fused_workspace_size(R, V, k)), dtype=torch.uint8,
-                     device=dev)
+    if args.head == "bf16":
+        size = int(binding.lib().spec_draft_fused_workspace_size(R, V, k))
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+
+        def call(f):
+            return binding.draft_topk_fused_lmhead(f, weight, k, 1.0, workspace=ws)
+    else:
+        scales = (2.0 ** -4, 2.0 ** -10) if args.head == "nv" else (1.0, 1.0)
+        weight = binding.fp4_quantize(weight, args.head, scales[1])
+        fmt = binding.SPEC_FP4_NV if args.head == "nv" else binding.SPEC_FP4_MX
+        size = int(binding.lib().spec_draft_fused_fp4_workspace_size(R, V, d, k, fmt))
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+
+        def call(f):
+            return binding.draft_topk_fused_fp4(f, weight, k, 1.0, scales[0], workspace=ws)
     stream = torch.cuda.current_stream()
     for _ in range(args.warmup):
-        binding.draft_topk_fused_lmhead(feats, weight, k, 1.0, workspace=ws)
+        call(feats)
     torch.cuda.synchronize()
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     barrier(world)
     e0.record(stream)
     for _ in range(args.steps):
-        binding.draft_topk_fused_lmhead(feats, weight, k, 1.0, workspace=ws)
+        call(feats)
     e1.record(stream)
     torch.cuda.synchronize()
     ms = max_over_ranks(e0.elapsed_time(e1), world, dev) / args.steps
@@ -942,7 +958,7 @@ def run_draft_fused(args):
 
     def e2e_step():
         dbuf.copy_(host, non_blocking=True)
-        out = binding.draft_topk_fused_lmhead(dbuf, weight, k, 1.0, workspace=ws)
+        out = call(dbuf)
         return {a: v.to("cpu", non_blocking=True) for a, v in out.items()}
 
     for _ in range(2):
@@ -964,7 +980,8 @@ def run_draft_fused(args):
     line = {"metric": "draft LM head + top-k drafting in one call: expanded-node rows per second",
             "value": world * R / (ms / 1e3), "unit": "rows/s", "n_gpus": world,
             "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms,
-            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+            "dtype": "bf16" if args.head == "bf16" else f"fp4 ({args.head})",
             "data": "synthetic",
             "config": {"workload": f"draft_lmhead_topk_r{R}_v{V}_d{d}_k{k}", "rows": R, "V": V,
                        "d": d, "k": k, "temperature": 1.0,
@@ -977,6 +994,10 @@ def run_draft_fused(args):
             "e2e": {"value": world * R / (e2e_ms / 1e3), "unit": "rows/s",
                     "h2d_bytes_per_step": h2d, "d2h_bytes_per_step": d2h},
             "gpu_launches": args.steps * 2}
+    if args.head != "bf16":
+        line["config"]["head"] = f"4 bits ({args.head}), features quantised in the call"
+        line["roofline"].update(kernel="quantize_kernel + fp4_linear_kernel + draft_topk_kernel (whole call)")
+        line["gpu_launches"] = args.steps * 3
     if rank == 0:
         print(json.dumps(line), flush=True)
 

@@ -605,6 +605,26 @@ int spec_fp4_linear(const void* a_codes, const void* a_scales, const void* w_cod
                     spec_stream_t stream);
 
 /*
+ * spec_draft_topk_fused_lmhead with a draft LM head kept in 4 bits: the features F [R, d] (bf16,
+ * row-major, device) are quantised with tensor scale feature_scale, multiplied with the head [V, d]
+ * (w_codes, w_scales, weight_scale, both of `format`) and the bf16 logits ranked as there: the same
+ * children as spec_fp4_quantize, spec_fp4_linear and spec_draft_topk give one after the other.
+ * workspace: device, 256-byte aligned, spec_draft_fused_fp4_workspace_size bytes (the features in 4
+ * bits and, unless out_logits is given, the logits; about 2 R V bytes; 0 for invalid sizes).
+ * Scales as in spec_fp4_quantize; d a multiple of 8, bases 16-byte aligned.  Other arguments, outputs
+ * and errors as spec_draft_topk_fused_lmhead; SPEC_ERR_UNSUPPORTED_DTYPE for another format.  A device
+ * wait that gave up makes the logits it concerns NaN, and their rows SPEC_ROW_NONFINITE.
+ */
+size_t spec_draft_fused_fp4_workspace_size(int32_t R, int32_t V, int32_t d, int32_t k,
+                                           spec_fp4_format format);
+int spec_draft_topk_fused_fp4(const void* features, float feature_scale, const void* w_codes,
+                              const void* w_scales, spec_fp4_format format, float weight_scale,
+                              int32_t d, int32_t R, int32_t V, int32_t k, float temperature,
+                              void* out_logits, int64_t logits_pitch, int32_t* out_tokens,
+                              float* out_probs, int32_t* out_status, void* workspace,
+                              size_t workspace_bytes, spec_stream_t stream);
+
+/*
  * What a server reports of the tokens it emits: from rows of logits, the log probabilities of given
  * tokens, the entropy and the most likely tokens of the distribution at `temperature` (softmax of
  * z / temperature over the whole row; no top-k or top-p cut).

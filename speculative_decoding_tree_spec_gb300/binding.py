@@ -166,6 +166,11 @@ def lib():
             L.spec_fp4_linear.argtypes = [P, P, P, P, ctypes.c_int, i32, i32, i32, F, P, ctypes.c_int,
                                           i64, P]
             L.spec_fp4_linear.restype = ctypes.c_int
+            L.spec_draft_fused_fp4_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.c_int]
+            L.spec_draft_fused_fp4_workspace_size.restype = ctypes.c_size_t
+            L.spec_draft_topk_fused_fp4.argtypes = [P, F, P, P, ctypes.c_int, F, i32, i32, i32, i32, F, P,
+                                                    i64, P, P, P, P, ctypes.c_size_t, P]
+            L.spec_draft_topk_fused_fp4.restype = ctypes.c_int
             L.spec_token_logprobs.argtypes = [P, ctypes.c_int, i32, i32, i64, P, i32, P, i32, i32, F, P,
                                               P, P, P, P, P]
             L.spec_token_logprobs.restype = ctypes.c_int
@@ -792,18 +797,18 @@ def _fp4_sizes(rows: int, cols: int, fmt: str):
 
 def _fp4_check(m: Fp4Matrix, dev: int, what: str):
     """The format's code and the pointers of a matrix whose tensors fit its sizes."""
-    fmt = _FP4_FORMATS.get(m.format)
+    c, s, rows, cols, name, _ = m
+    fmt = _FP4_FORMATS.get(name)
     if fmt is None:
-        raise ValueError(f"{what}: the format is 'mx' or 'nv', got {m.format!r}")
-    if m.rows < 0 or m.cols < 1:
+        raise ValueError(f"{what}: the format is 'mx' or 'nv', got {name!r}")
+    if rows < 0 or cols < 1:
         raise ValueError(f"{what}: rows and cols must be positive")
-    c, s = m.codes, m.scales
-    row, scales = _fp4_sizes(m.rows, m.cols, m.format)
+    row, scales = _fp4_sizes(rows, cols, name)
     if c.dtype is not torch.uint8 or s.dtype is not torch.uint8 or c.get_device() != dev or \
             s.get_device() != dev or not c.is_contiguous() or not s.is_contiguous():
         raise TypeError(f"{what}: codes and scales must be contiguous uint8 tensors on one CUDA device")
-    if c.numel() != m.rows * row or s.numel() != scales:
-        raise ValueError(f"{what}: a {m.rows} x {m.cols} {m.format} matrix has {m.rows * row} bytes of "
+    if c.numel() != rows * row or s.numel() != scales:
+        raise ValueError(f"{what}: a {rows} x {cols} {name} matrix has {rows * row} bytes of "
                          f"codes and {scales} of scales, got {c.numel()} and {s.numel()}")
     return fmt, c.data_ptr(), s.data_ptr()
 
@@ -826,8 +831,10 @@ def _matrix_out(out, rows: int, cols: int, dtype, dev: int):
 
 def _pitch(t: torch.Tensor, cols: int) -> int:
     """Elements from row to row; what one row's stride says does not matter."""
+    if t.shape[0] > 1:
+        return t.stride(0)
     per = 16 // t.element_size()
-    return t.stride(0) if t.shape[0] > 1 else (cols + per - 1) // per * per
+    return (cols + per - 1) // per * per
 
 
 def fp4_quantize(x: torch.Tensor, format: str = "mx", tensor_scale: float = 1.0, *, out=None,
@@ -847,16 +854,20 @@ def fp4_quantize(x: torch.Tensor, format: str = "mx", tensor_scale: float = 1.0,
     rows, cols = x.shape
     if format not in _FP4_FORMATS:
         raise ValueError(f"the format is 'mx' or 'nv', got {format!r}")
+    dtype = _float_dtype(x.dtype)
     if out is None:
-        row, scales = _fp4_sizes(rows, cols, format)
-        out = Fp4Matrix(torch.empty((rows, row), dtype=torch.uint8, device=x.device),
-                        torch.empty(scales, dtype=torch.uint8, device=x.device), rows, cols, format,
-                        float(tensor_scale))
-    elif (out.rows, out.cols, out.format, out.tensor_scale) != (rows, cols, format, tensor_scale):
-        raise ValueError("out must have x's sizes, the format and the tensor scale")
-    fmt, codes, scales = _fp4_check(out, dev, "out")
-    rc = (_lib or lib()).spec_fp4_quantize(x.data_ptr(), _float_dtype(x.dtype), rows, cols,
-                                           _pitch(x, cols), fmt, tensor_scale, codes, scales,
+        row, size = _fp4_sizes(rows, cols, format)
+        device = x.device
+        codes = torch.empty((rows, row), dtype=torch.uint8, device=device)
+        scales = torch.empty(size, dtype=torch.uint8, device=device)
+        out = Fp4Matrix(codes, scales, rows, cols, format, tensor_scale)
+        fmt, codes, scales = _FP4_FORMATS[format], codes.data_ptr(), scales.data_ptr()
+    else:
+        if (out.rows, out.cols, out.format, out.tensor_scale) != (rows, cols, format, tensor_scale):
+            raise ValueError("out must have x's sizes, the format and the tensor scale")
+        fmt, codes, scales = _fp4_check(out, dev, "out")
+    rc = (_lib or lib()).spec_fp4_quantize(x.data_ptr(), dtype, rows, cols, _pitch(x, cols), fmt,
+                                           tensor_scale, codes, scales,
                                            torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise SpecError(rc, "spec_fp4_quantize")
@@ -912,6 +923,49 @@ def fp4_linear(a: Fp4Matrix, w: Fp4Matrix, dtype=torch.bfloat16, *, alpha: float
                                          _pitch(out, w.rows), torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise SpecError(rc, "spec_fp4_linear")
+    return out
+
+
+def draft_topk_fused_fp4(features: torch.Tensor, weight: Fp4Matrix, k: int, temperature: float = 1.0,
+                         feature_scale: float = 1.0, want_logits: bool = False, workspace=None,
+                         stream=None) -> dict:
+    """spec_draft_topk_fused_fp4: draft_topk_fused_lmhead with a head [V, d] kept in 4 bits; features
+    [R, d] bf16 (device, contiguous), quantised with the tensor scale feature_scale.  Returns tokens
+    [R, k], probs [R, k], status [R] and, if asked, the bf16 logits [R, V] (a padded-pitch view)."""
+    dev = features.get_device()
+    if dev < 0:
+        raise ValueError("the features must be on a CUDA device")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return draft_topk_fused_fp4(features, weight, k, temperature, feature_scale, want_logits,
+                                        workspace)
+    if features.dim() != 2 or features.dtype is not torch.bfloat16 or features.shape[1] != weight.cols:
+        raise TypeError("features [R, d] must be bf16 with the weight's d")
+    if not features.is_contiguous():
+        raise ValueError("features must be contiguous")
+    fmt, codes, scales = _fp4_check(weight, dev, "weight")
+    R, d = features.shape
+    V, device = weight.rows, features.device
+    out = {"tokens": torch.empty((R, k), dtype=torch.int32, device=device),
+           "probs": torch.empty((R, k), dtype=torch.float32, device=device),
+           "status": torch.empty(R, dtype=torch.int32, device=device)}
+    logits = None
+    if want_logits:
+        logits = out["logits"] = _padded(R, V, torch.bfloat16, device)
+    if workspace is None:
+        ws = (_lib or lib()).spec_draft_fused_fp4_workspace_size(R, V, d, k, fmt)
+        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on the features' device")
+    rc = (_lib or lib()).spec_draft_topk_fused_fp4(
+        features.data_ptr(), feature_scale, codes, scales, fmt, weight.tensor_scale, d, R, V, k,
+        temperature, None if logits is None else logits.data_ptr(),
+        0 if logits is None else _pitch(logits, V), out["tokens"].data_ptr(), out["probs"].data_ptr(),
+        out["status"].data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        raise SpecError(rc, "spec_draft_topk_fused_fp4")
     return out
 
 

@@ -47,4 +47,12 @@ __device__ __forceinline__ uint32_t fp4_codes(const float (&y)[8]) {
   return d;
 }
 
+// The launches behind the entry points, arguments checked (quantize.cu, fp4_linear.cu).
+cudaError_t launch_fp4_quantize(const void* x, spec_dtype dtype, int rows, int cols,
+                                int64_t row_pitch, spec_fp4_format format, float tensor_scale,
+                                void* codes, void* scales, cudaStream_t s);
+cudaError_t launch_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
+                              const void* w_scales, spec_fp4_format format, int R, int V, int K,
+                              float alpha, void* out, spec_dtype dtype, int64_t pitch, cudaStream_t s);
+
 }  // namespace svk

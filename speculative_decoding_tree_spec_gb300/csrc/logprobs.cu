@@ -664,11 +664,25 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   const int per_chunk = fine ? per_load : 1024;
   job.n_chunks = (job.V + per_chunk - 1) / per_chunk;
   const int n_keys = job.n_chunks * (fine ? kLpUnits : 1);
-  // warps per row that leave every row resident at once
-  const int room = device_sm_count() * kLpPerSm * kLpWarps;
+  // Warps per row: a wave of rows takes as long as a warp's loads and what finishing a row costs, about 8
+  // loads' time, in a cluster 12.  Measured (us, bf16 rows of 128256, k = 5): 8 rows 8.0 with 64
+  // warps, 9.1 with 32, 14.5 with 8; 152 rows 13.3 with 16, 15.1 with 8, 18.7 with 32; 640 rows 40.2 with
+  // 4, 41.8 with 8, 53.7 with 2; 3840 rows 188 with 8, 191 with 4, 207 with 2.
+  const int64_t room = (int64_t)device_sm_count() * kLpPerSm * kLpWarps;
+  const int64_t n_loads = ((int64_t)job.V + per_load - 1) / per_load;
   int W = 1, C = 1;
-  while (W < kLpWarps && (int64_t)job.R * W * 2 <= room && W < job.n_chunks) W *= 2;
-  while (C < kLpMaxCluster && (int64_t)job.R * W * C * 2 <= room && C * W < job.n_chunks) C *= 2;
+  int64_t least = INT64_MAX;
+  for (int w = 1; w <= kLpWarps * kLpMaxCluster; w *= 2) {
+    const bool cluster = w > kLpWarps;
+    const int64_t waves = ((int64_t)job.R * w + room - 1) / room;
+    if (w > 1 && (w > job.n_chunks || (cluster && waves > 1))) break;
+    const int64_t cost = waves * ((n_loads + w - 1) / w + (cluster ? 12 : 8));
+    if (cost <= least) {
+      least = cost;
+      W = w < kLpWarps ? w : kLpWarps;
+      C = w / W;
+    }
+  }
   int threads = 32 * W;
   job.cluster = C;
   cudaLaunchConfig_t cfg = {};

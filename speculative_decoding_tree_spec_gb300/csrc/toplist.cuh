@@ -7,13 +7,6 @@
 
 namespace svk {
 
-// The key of element idx of a row: its logit's order bits, then the complement of idx.
-template <typename T>
-__device__ __forceinline__ uint64_t element_key(const void* row, int idx) {
-  const float z = Elt<T>::at(row, idx);
-  return ((uint64_t)order_key(z) << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)idx);
-}
-
 // 64-bit keys held one per lane, sorted descending by a bitonic network (blocks of
 // size s alternate direction so that each pair forms a bitonic sequence; size 32 is
 // descending).
@@ -50,21 +43,6 @@ __device__ __forceinline__ uint64_t list_merge(uint64_t L, uint64_t x, int lane)
   for (int stride = 16; stride > 0; stride >>= 1) {
     const uint64_t o = __shfl_xor_sync(kFull, L, stride);
     L = ((lane & stride) == 0) == (L > o) ? L : o;
-  }
-  return L;
-}
-
-// The list merged with n keys of a candidate buffer by one whole warp, 32 keys at a time: a few
-// are inserted one by one, more are sorted and merged.  Returns the merged list.
-static __device__ uint64_t merge_into_list(uint64_t L, const uint64_t* buf, int n, int k_out,
-                                           int lane) {
-  for (int c = 0; c < n; c += 32) {
-    const int m = min(32, n - c);
-    if (m <= 6) {
-      for (int i = 0; i < m; ++i) L = list_insert(L, buf[c + i], k_out, lane);
-    } else {
-      L = list_merge(L, warp_sort_desc(lane < m ? buf[c + lane] : 0ull, lane), lane);
-    }
   }
   return L;
 }

@@ -104,6 +104,42 @@ LOGPROBS = [
     (dict(pitch=1 << 61), -6),
 ]
 
+FUSED = [
+    (dict(R=0), 0),
+    (dict(format=2), -2),
+    (dict(R=-1), -1),
+    (dict(V=0), -1),
+    (dict(d=0), -1),
+    (dict(k=0), -1),
+    (dict(k=33), -1),
+    (dict(k=5, V=4), -1),
+    (dict(T=0.0), -1),
+    (dict(T=NAN), -1),
+    (dict(feature_scale=0.3, format=1), -1),
+    (dict(weight_scale=0.0, format=1), -1),
+    (dict(feature_scale=2.0), -1),
+    (dict(weight_scale=0.5), -1),
+    (dict(feature_scale=2.0 ** 100, weight_scale=2.0 ** 100, format=1), -1),
+    (dict(features=None), -1),
+    (dict(w=None), -1),
+    (dict(w_scales=None), -1),
+    (dict(tokens=None), -1),
+    (dict(probs=None), -1),
+    (dict(ws=None), -1),
+    (dict(features=FAKE + 8), -3),
+    (dict(w=FAKE + 8), -3),
+    (dict(w_scales=FAKE + 4), -3),
+    (dict(d=60), -3),
+    (dict(logits=FAKE, pitch=63), -1),
+    (dict(logits=FAKE, pitch=68), -3),
+    (dict(logits=FAKE + 2, pitch=64), -3),
+    (dict(ws_bytes=100), -4),
+    (dict(ws=FAKE + 16), -4),
+    (dict(V=(1 << 21) + 1), -6),
+    (dict(R=BIG), -6),
+    (dict(d=BIG + 7), -6),
+]
+
 
 def quantize(L, back, x=FAKE, dtype=0, rows=4, cols=64, pitch=64, format=0, scale=1.0, codes=FAKE, scales=FAKE):
     if back:
@@ -122,10 +158,17 @@ def logprobs(L, logits=FAKE, dtype=0, n=4, V=64, pitch=64, rows=FAKE, R=4, token
                                  status, None)
 
 
+def fused(L, features=FAKE, feature_scale=1.0, w=FAKE, w_scales=FAKE, format=0, weight_scale=1.0, d=64, R=4, V=64, k=2,
+          T=1.0, logits=None, pitch=0, tokens=FAKE, probs=FAKE, status=FAKE, ws=FAKE, ws_bytes=1 << 40):
+    return L.spec_draft_topk_fused_fp4(features, feature_scale, w, w_scales, format, weight_scale, d, R, V, k, T,
+                                       logits, pitch, tokens, probs, status, ws, ws_bytes, None)
+
+
 def main():
     L = binding.lib()
     json.dump({"quantize": [quantize(L, False, **kw) for kw, _ in QUANTIZE],
                "dequantize": [quantize(L, True, **kw) for kw, _ in QUANTIZE],
+               "fused": [fused(L, **kw) for kw, _ in FUSED],
                "linear": [linear(L, **kw) for kw, _ in LINEAR],
                "logprobs": [logprobs(L, **kw) for kw, _ in LOGPROBS]}, sys.stdout)
 

@@ -31,7 +31,7 @@ def codes():
 
 
 @pytest.mark.parametrize("name,cases", [("quantize", hv.QUANTIZE), ("dequantize", hv.QUANTIZE),
-                                        ("linear", hv.LINEAR), ("logprobs", hv.LOGPROBS)])
+                                        ("linear", hv.LINEAR), ("fused", hv.FUSED), ("logprobs", hv.LOGPROBS)])
 def test_host_validation(codes, name, cases):
     for (kw, want), got in zip(cases, codes[name]):
         assert got == want, (name, kw)
@@ -47,6 +47,12 @@ def test_sizes():
     for bad in ((-1, 4), (4, 0), ((1 << 24) + 1, 4), (4, (1 << 24) + 1)):
         assert L.spec_fp4_code_bytes(*bad) == 0 and L.spec_fp4_scale_bytes(*bad, 0) == 0
     assert L.spec_fp4_scale_bytes(4, 4, 2) == 0
+    size = L.spec_draft_fused_fp4_workspace_size
+    assert size(640, 1001, 200, 10, 0) % 256 == 0
+    assert size(640, 1001, 200, 10, 0) >= 640 * 1008 * 2 + 640 * 112 + 5 * 2 * 512
+    for bad in ((0, 9, 9, 1, 0), (1, 0, 9, 1, 0), (1, 9, 0, 1, 0), (1, 9, 9, 0, 0), (1, 9, 9, 10, 0), (1, 9, 9, 1, 2),
+                (1, (1 << 21) + 1, 9, 1, 0), ((1 << 24) + 1, 9, 9, 1, 0)):
+        assert size(*bad) == 0
 
 
 class Tensor(FakeTensor):
@@ -67,11 +73,16 @@ class Torch(FakeTorch):
         return self.cuda.made[-1]
 
 
+class Lib(FakeLib):
+    def __getattr__(self, name):
+        return (lambda *a: 1024) if "workspace_size" in name else super().__getattr__(name)
+
+
 @pytest.fixture
 def fake(monkeypatch):
     t = Torch()
     monkeypatch.setattr(binding, "torch", t)
-    monkeypatch.setattr(binding, "_lib", FakeLib(t.cuda))
+    monkeypatch.setattr(binding, "_lib", Lib(t.cuda))
     return t.cuda
 
 
@@ -90,10 +101,11 @@ def _calls(dev):
     return {"quantize": lambda s=None: binding.fp4_quantize(x, stream=s),
             "dequantize": lambda s=None: binding.fp4_dequantize(a, stream=s),
             "linear": lambda s=None: binding.fp4_linear(a, w, stream=s),
+            "fused": lambda s=None: binding.draft_topk_fused_fp4(x, w, 3, stream=s),
             "logprobs": lambda s=None: binding.token_logprobs(logits, T((5,), I32, dev), 3, stream=s)}
 
 
-CALLS = ["quantize", "dequantize", "linear", "logprobs"]
+CALLS = ["quantize", "dequantize", "linear", "fused", "logprobs"]
 
 
 class OtherStream:  # not one of torch's
@@ -149,6 +161,11 @@ BAD = {
     "a result elsewhere": lambda: binding.fp4_linear(matrix(5, 64), matrix(16, 64), out=T((5, 16), BF, 1)),
     "a result of another size": lambda: binding.fp4_linear(matrix(5, 64), matrix(16, 64), out=T((16, 5), BF)),
     "a result of half precision": lambda: binding.fp4_linear(matrix(5, 64), matrix(16, 64), torch.float16),
+    "fp32 features": lambda: binding.draft_topk_fused_fp4(T((5, 64), F32), matrix(16, 64), 2),
+    "features of another length": lambda: binding.draft_topk_fused_fp4(T((5, 32), BF), matrix(16, 64), 2),
+    "a head elsewhere": lambda: binding.draft_topk_fused_fp4(T((5, 64), BF), matrix(16, 64, dev=1), 2),
+    "a workspace elsewhere": lambda: binding.draft_topk_fused_fp4(T((5, 64), BF), matrix(16, 64), 2,
+                                                                  workspace=T((4096,), U8, 1)),
     "logits of half precision": lambda: binding.token_logprobs(T((5, 64), torch.float16), None, 1),
     "logits of three dimensions": lambda: binding.token_logprobs(T((5, 2, 64), BF), None, 1),
     "logits in columns": lambda: binding.token_logprobs(T((5, 64), BF, strides=(1, 8)), None, 1),
