@@ -33,10 +33,13 @@ constexpr int kLpThreads = 256;  // at most, of a CTA of the row kernel; 1024 pe
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpPerSm = 3;     // CTAs of that size that fit an SM
 constexpr int kLpUnits = 4;      // 16-byte units per lane in a load
+constexpr int kLpStages = 4;     // loads of a warp in flight
 constexpr int kLpMaxK = 32;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpSmallV = 1024;
 constexpr int kLpCand = 256;     // elements ranked by counting
+constexpr size_t kLpRing = kLpStages * kLpUnits * 32 * 16;  // bytes of a warp
+constexpr int kLpMaxShared = (int)(kLpWarps * kLpRing) + SPEC_MAX_VOCAB / 1024 * 4;
 constexpr int kLpFineV = 32768;
 constexpr int kLpCount = 512;    // chunks ranked by counting
 
@@ -191,6 +194,23 @@ __device__ __forceinline__ void load_units(const void* row, int V, int at, int l
   }
 }
 
+// The same on its way to shared memory, `slot` this lane's place (units 32 places apart).  A lane
+// reads back only what it copied itself, so its own wait is all it needs.
+template <typename T>
+__device__ __forceinline__ void copy_units(const void* row, int V, int at, int lane, uint4* slot) {
+  const int u0 = at * (32 * kLpUnits);
+  if (u0 + 32 * kLpUnits <= V / Elt<T>::kPerUnit) {
+#pragma unroll
+    for (int j = 0; j < kLpUnits; ++j)
+      cp_async16(slot + j * 32, reinterpret_cast<const uint4*>(row) + u0 + j * 32 + lane);
+  } else {
+    uint4 raw[kLpUnits];
+    load_units<T>(row, V, at, lane, raw);
+#pragma unroll
+    for (int j = 0; j < kLpUnits; ++j) slot[j * 32] = raw[j];
+  }
+}
+
 // NaN-propagating maximum of `n` of the lane's units from j0 on (constants where it is called).
 template <typename T>
 __device__ __forceinline__ float units_max(const uint4 (&raw)[kLpUnits], int j0, int n) {
@@ -257,8 +277,7 @@ template <typename T, int kSub>
 __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(LogprobJob job) {
   constexpr int E = Elt<T>::kPerUnit;
   constexpr int kKeyUnits = kLpUnits / kSub;  // units per lane that share a key
-  extern __shared__ __align__(16) uint32_t s_key[];  // [n_chunks kSub, rounded up to 4] order key of each
-                                                     // chunk's largest logit
+  extern __shared__ __align__(16) uint4 s_ring[];  // [warps][kLpStages][kLpUnits][32]
   __shared__ Part s_part[kLpMaxCluster * kLpWarps];
   __shared__ uint32_t s_bad;
   __shared__ uint64_t s_list[kLpCand];  // candidates, or a list of 32 per warp
@@ -267,6 +286,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
   __shared__ float s_m, s_log;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int C = job.cluster, W = (int)blockDim.x >> 5;
+  // [n_chunks kSub, rounded up to 4] order key of each chunk's largest logit
+  uint32_t* const s_key = reinterpret_cast<uint32_t*>(s_ring + W * (kLpStages * kLpUnits * 32));
+  uint4* const ring = s_ring + warp * (kLpStages * kLpUnits * 32) + lane;
   const int rank = blockIdx.x % C, r = blockIdx.x / C;
   const int n = row_of(job, r);
   if (n < 0) {  // the whole cluster agrees
@@ -279,13 +301,19 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
   // loads of a chunk: 1024 logits
   constexpr int loads = kSub > 1 ? 1 : 1024 / (32 * kLpUnits * E);
   const int n_loads = job.n_chunks * loads;
-  // this warp's loads: chunk by chunk, C W chunks apart
-  int at = (rank * W + warp) * loads;
-  [[maybe_unused]] int left = loads;
+  // this warp's loads: chunk by chunk, C W chunks apart; `ahead` is the next one to copy
   const int skip = (C * W - 1) * loads;
-
-  uint4 nxt[kLpUnits];
-  if (at < n_loads) load_units<T>(row, V, at, lane, nxt);
+  auto next = [&](int& at) {
+    ++at;
+    if (loads == 1 || at % loads == 0) at += skip;
+  };
+  int at = (rank * W + warp) * loads, ahead = at;
+#pragma unroll
+  for (int i = 0; i < kLpStages; ++i) {
+    if (ahead < n_loads) copy_units<T>(row, V, ahead, lane, ring + i * (kLpUnits * 32));
+    cp_async_commit();
+    next(ahead);
+  }
   if (threadIdx.x == 0) {
     s_bad = 0u;
     s_count = 0;
@@ -299,19 +327,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
   int bad = 0;
   uint32_t top = 0u;
   const uint32_t key0 = C > 1 ? cluster_addr(s_key, 0) : 0u;
+  int stage = 0;
   while (at < n_loads) {
+    uint4* const slot = ring + stage * (kLpUnits * 32);
+    stage = (stage + 1) % kLpStages;
+    cp_async_wait<kLpStages - 1>();
     uint4 raw[kLpUnits];
 #pragma unroll
-    for (int j = 0; j < kLpUnits; ++j) raw[j] = nxt[j];
+    for (int j = 0; j < kLpUnits; ++j) raw[j] = slot[j * 32];
     const int done = at;
-    ++at;
-    bool last = true;  // of its chunk
-    if constexpr (loads > 1) last = --left == 0;
-    if (last) {
-      at += skip;
-      left = loads;
-    }
-    if (at < n_loads) load_units<T>(row, V, at, lane, nxt);
+    next(at);
+    const bool last = loads == 1 || at % loads == 0;  // of its chunk
     const float um = units_max<T>(raw, 0, kLpUnits);
     bad |= (um != um);
     if (k > 0) {
@@ -352,6 +378,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
       S.add(s);
       A.add(a);
     }
+    // the registers hold what the slot held
+    if (ahead < n_loads) copy_units<T>(row, V, ahead, lane, slot);
+    cp_async_commit();
+    next(ahead);
   }
   if (arrived) cluster_wait();
 
@@ -481,6 +511,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     const int sel = s_sel[i / key_loads];
     return kSub > 1 ? sel / kSub : sel * loads + i % key_loads;
   };
+  uint4 nxt[kLpUnits];
   if (warp < total) load_units<T>(row, V, look_at(warp), lane, nxt);
   write_given<T>(job, row, r, threadIdx.x, blockDim.x, M, log_s);
   for (int i = warp; i < total; i += W) {
@@ -688,7 +719,7 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(job.R * C));
   cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = job.k > 0 ? ((size_t)n_keys + 3) / 4 * 16 : 0;
+  cfg.dynamicSmemBytes = (size_t)W * kLpRing + (job.k > 0 ? ((size_t)n_keys + 3) / 4 * 16 : 0);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -696,7 +727,17 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fine ? logprob_rows_kernel<T, kLpUnits> : logprob_rows_kernel<T, 1>, job);
+  auto kernel = fine ? logprob_rows_kernel<T, kLpUnits> : logprob_rows_kernel<T, 1>;
+  static bool configured[64][2] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !configured[dev][fine]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpMaxShared);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev][fine] = true;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, job);
 }
 
 }  // namespace
