@@ -4,20 +4,21 @@
 // One pass over the row: each lane keeps its running maximum m and, referred to it, the sums of
 // w = 2^a and of a w, a = (z - m) log2(e) / T.  When m grows by d (in units of a) both are carried
 // over: w' = w 2^-d, a' = a - d.  Subtracting before multiplying keeps the weight of the maximum
-// exactly 1; a chunk's sums (16 or 32 weights of a lane) are fp32 and join compensated sums, so that
+// exactly 1; the sums of a load (16 or 32 weights of a lane) are fp32 and join compensated sums, so that
 // ln S is accurate to the weights' own rounding, and where one token holds nearly everything it
 // lacks at most what that token's lane adds beside it.
 //
-// The most likely tokens without a list in the loop: a row is read in contiguous chunks of 2 KB, one
-// warp each, and of a chunk only its largest logit is kept (one warp reduction a chunk).  Among
-// contiguous chunks, ordered by (largest logit, then lower place), the k tokens wanted lie in the first
-// k: a token in a later one has k better tokens before it.  So only those k chunks are read
-// again (out of the L2 cache mostly), and only their elements at or above the k-th chunk's maximum are
-// ranked.
+// The most likely tokens without a list in the loop: of each contiguous 512 bytes of the row (a piece) only
+// the largest logit is kept, one warp reduction a piece.  Among contiguous pieces, ordered by
+// (largest logit, then lower place), the k tokens wanted lie in the first k: a token in a later one has
+// k better tokens before it.  The same holds for groups of pieces, so the first k groups are
+// found by counting, then the first k pieces in them, and only those are read again; their elements at
+// or above the k-th piece's maximum are ranked by counting.  Ties by the hundred go through a sorted
+// list per warp instead.
 //
-// One CTA per row, four per SM.  A launch of fewer rows than that puts a cluster of 2, 4 or 8 CTAs on
-// each row; they leave their chunks' maxima and sums in the first CTA's shared memory, which
-// finishes the row.  Rows of up to 1024 logits take one warp each, the row in registers.
+// A CTA of 1 to 8 warps per row, or a cluster of up to 8 CTAs where rows are few (launch_logprobs
+// chooses); they leave their pieces' maxima and sums in the first CTA's shared memory, which finishes the
+// row.  Loads go through a ring in shared memory, four of 2 KB in flight per warp.  Rows of up to 1024 logits take one warp each, the row in registers.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -29,19 +30,19 @@ namespace svk {
 
 namespace {
 
-constexpr int kLpThreads = 256;  // at most, of a CTA of the row kernel; 1024 per SM
+constexpr int kLpThreads = 256;  // at most, of a CTA of the row kernel
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpPerSm = 3;     // CTAs of that size that fit an SM
-constexpr int kLpUnits = 4;      // 16-byte units per lane in a load
+constexpr int kLpPerSm = 3;      // CTAs of that size that fit an SM
+constexpr int kLpUnits = 4;      // 16-byte units per lane in a load; a unit of a warp is a piece
 constexpr int kLpStages = 4;     // loads of a warp in flight
+constexpr size_t kLpRing = kLpStages * kLpUnits * 32 * 16;  // their bytes
 constexpr int kLpMaxK = 32;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpSmallV = 1024;
-constexpr int kLpCand = 256;     // elements ranked by counting
-constexpr size_t kLpRing = kLpStages * kLpUnits * 32 * 16;  // bytes of a warp
-constexpr int kLpMaxShared = (int)(kLpWarps * kLpRing) + SPEC_MAX_VOCAB / 1024 * 4;
-constexpr int kLpFineV = 32768;
-constexpr int kLpCount = 512;    // chunks ranked by counting
+// the ring of eight warps and the maxima of the widest fp32 row
+constexpr int kLpMaxShared = (int)(kLpWarps * kLpRing) + SPEC_MAX_VOCAB / 32;
+constexpr int kLpCand = 256;     // candidates ranked by counting
+constexpr int kLpGroups = 128;   // groups ranked by counting
 
 struct LogprobJob {
   const void* base;
@@ -56,7 +57,9 @@ struct LogprobJob {
   int32_t* out_top;
   float* out_top_lp;
   int32_t* out_status;
-  int cluster, n_chunks;
+  int cluster, n_loads;  // CTAs per row, loads of a row
+  int n_pieces, group;   // pieces of a row, and of a group
+  int refine;            // the pieces of the chosen groups are ranked, too, before they are read
 };
 
 // Sums of 2^a and a 2^a over some elements, referred to their maximum m (in logits).
@@ -156,41 +159,38 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-// The lane's units of the row's `at`-th load (2 KB of a warp); what lies past the row is -inf.
+// Unit u of a row; what lies past the row is -inf.
+template <typename T>
+__device__ __forceinline__ uint4 load_unit_padded(const void* row, int V, int u) {
+  constexpr int E = Elt<T>::kPerUnit;
+  constexpr uint32_t kNegInf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+  if (u < V / E) return __ldg(reinterpret_cast<const uint4*>(row) + u);
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (sizeof(T) == 2) {
+      const unsigned short* p = static_cast<const unsigned short*>(row);
+      const int i = u * E + 2 * q;
+      w[q] = (i < V ? (uint32_t)p[i] : 0xFF80u) | ((i + 1 < V ? (uint32_t)p[i + 1] : 0xFF80u) << 16);
+    } else {
+      const int i = u * E + q;
+      w[q] = i < V ? static_cast<const uint32_t*>(row)[i] : kNegInf;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The lane's units of the row's `at`-th load (2 KB of a warp).
 template <typename T>
 __device__ __forceinline__ void load_units(const void* row, int V, int at, int lane,
                                            uint4 (&raw)[kLpUnits]) {
-  constexpr int E = Elt<T>::kPerUnit;
-  constexpr uint32_t kNegInf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
   const int u0 = at * (32 * kLpUnits);
-  const int full = V / E;
-  if (u0 + 32 * kLpUnits <= full) {
+  if (u0 + 32 * kLpUnits <= V / Elt<T>::kPerUnit) {
 #pragma unroll
     for (int j = 0; j < kLpUnits; ++j)
       raw[j] = __ldg(reinterpret_cast<const uint4*>(row) + u0 + j * 32 + lane);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < kLpUnits; ++j) {
-    const int u = u0 + j * 32 + lane;
-    raw[j] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
-    if (u < full) {
-      raw[j] = __ldg(reinterpret_cast<const uint4*>(row) + u);
-    } else if (u * E < V) {
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if constexpr (sizeof(T) == 2) {
-          const unsigned short* p = static_cast<const unsigned short*>(row);
-          const int i = u * E + 2 * q;
-          w[q] = (i < V ? (uint32_t)p[i] : 0xFF80u) | ((i + 1 < V ? (uint32_t)p[i + 1] : 0xFF80u) << 16);
-        } else {
-          const int i = u * E + q;
-          w[q] = i < V ? static_cast<const uint32_t*>(row)[i] : kNegInf;
-        }
-      }
-      raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    for (int j = 0; j < kLpUnits; ++j) raw[j] = load_unit_padded<T>(row, V, u0 + j * 32 + lane);
   }
 }
 
@@ -211,32 +211,29 @@ __device__ __forceinline__ void copy_units(const void* row, int V, int at, int l
   }
 }
 
-// NaN-propagating maximum of `n` of the lane's units from j0 on (constants where it is called).
+// NaN-propagating maxima.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float warp_max_nan(float a) {
+  float d;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;\n" : "=f"(d) : "f"(a));
+  return d;
+}
 template <typename T>
-__device__ __forceinline__ float units_max(const uint4 (&raw)[kLpUnits], int j0, int n) {
+__device__ __forceinline__ float unit_max(const uint4& u) {
   if constexpr (sizeof(T) == 2) {
-    uint32_t none = 0xFF80FF80u;
-    __nv_bfloat162 m2 = *reinterpret_cast<const __nv_bfloat162*>(&none);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    __nv_bfloat162 m2 = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
 #pragma unroll
-    for (int j = 0; j < kLpUnits; ++j) {
-      if (j < j0 || j >= j0 + n) continue;
-      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) m2 = __hmax2_nan(m2, *reinterpret_cast<const __nv_bfloat162*>(&w[q]));
-    }
-    const float lo = __low2float(m2), hi = __high2float(m2);
-    return (lo != lo || hi != hi) ? CUDART_NAN_F : fmaxf(lo, hi);
+    for (int q = 1; q < 4; ++q) m2 = __hmax2_nan(m2, *reinterpret_cast<const __nv_bfloat162*>(&w[q]));
+    const uint32_t b = *reinterpret_cast<const uint32_t*>(&m2);
+    return max_nan(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
   } else {
-    float m = -CUDART_INF_F;
-#pragma unroll
-    for (int j = 0; j < kLpUnits; ++j) {
-      if (j < j0 || j >= j0 + n) continue;
-      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(m) : "f"(__uint_as_float(w[q])));
-    }
-    return m;
+    return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
+                   max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
   }
 }
 
@@ -272,22 +269,26 @@ __device__ __forceinline__ void units_sums(const uint4 (&raw)[kLpUnits], float m
   aw = a0.x + a0.y;
 }
 
-// One key of a chunk per load of it (kSub 1) or per 512 bytes (kSub kLpUnits).
-template <typename T, int kSub>
+// The key of element i with value z.
+__device__ __forceinline__ uint64_t key_of(float z, int i) {
+  return ((uint64_t)order_key(z) << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)i);
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(LogprobJob job) {
   constexpr int E = Elt<T>::kPerUnit;
-  constexpr int kKeyUnits = kLpUnits / kSub;  // units per lane that share a key
   extern __shared__ __align__(16) uint4 s_ring[];  // [warps][kLpStages][kLpUnits][32]
   __shared__ Part s_part[kLpMaxCluster * kLpWarps];
-  __shared__ uint32_t s_bad;
-  __shared__ uint64_t s_list[kLpCand];  // candidates, or a list of 32 per warp
-  __shared__ int s_sel[kLpMaxK], s_count;
-  __shared__ uint32_t s_tau;
+  __shared__ __align__(16) uint32_t s_group[kLpGroups];  // each group's largest, as order keys
+  __shared__ uint64_t s_list[kLpCand];                 // candidates, or a list of 32 per warp
+  __shared__ int s_sel[kLpMaxK], s_piece[kLpMaxK];     // the chosen groups and pieces
+  __shared__ int s_count, s_found;
+  __shared__ uint32_t s_bad, s_tau, s_tau2;
   __shared__ float s_m, s_log;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int C = job.cluster, W = (int)blockDim.x >> 5;
-  // [n_chunks kSub, rounded up to 4] order key of each chunk's largest logit
-  uint32_t* const s_key = reinterpret_cast<uint32_t*>(s_ring + W * (kLpStages * kLpUnits * 32));
+  // [4 n_loads] each piece's largest logit
+  float* const s_top = reinterpret_cast<float*>(s_ring + W * (kLpStages * kLpUnits * 32));
   uint4* const ring = s_ring + warp * (kLpStages * kLpUnits * 32) + lane;
   const int rank = blockIdx.x % C, r = blockIdx.x / C;
   const int n = row_of(job, r);
@@ -296,27 +297,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     return;
   }
   const void* row = static_cast<const char*>(job.base) + (int64_t)n * job.pitch_bytes;
-  const int V = job.V, k = job.k;
+  const int V = job.V, k = job.k, n_loads = job.n_loads;
   const float c = job.c;
-  // loads of a chunk: 1024 logits
-  constexpr int loads = kSub > 1 ? 1 : 1024 / (32 * kLpUnits * E);
-  const int n_loads = job.n_chunks * loads;
-  // this warp's loads: chunk by chunk, C W chunks apart; `ahead` is the next one to copy
-  const int skip = (C * W - 1) * loads;
-  auto next = [&](int& at) {
-    ++at;
-    if (loads == 1 || at % loads == 0) at += skip;
-  };
-  int at = (rank * W + warp) * loads, ahead = at;
+  const int first = rank * W + warp, step = C * W;
+  int ahead = first;
 #pragma unroll
-  for (int i = 0; i < kLpStages; ++i) {
+  for (int i = 0; i < kLpStages; ++i, ahead += step) {
     if (ahead < n_loads) copy_units<T>(row, V, ahead, lane, ring + i * (kLpUnits * 32));
     cp_async_commit();
-    next(ahead);
   }
+  const uint32_t top0 = C > 1 ? cluster_addr(s_top, 0) : 0u;
+  const uint32_t group0 = C > 1 ? cluster_addr(s_group, 0) : 0u;
   if (threadIdx.x == 0) {
     s_bad = 0u;
-    s_count = 0;
+    s_count = s_found = 0;
   }
   if (C > 1) cluster_arrive();  // the first CTA is there, its words cleared
   else __syncthreads();
@@ -324,38 +318,36 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
 
   float m = -CUDART_INF_F;
   Kahan S, A;
-  int bad = 0;
-  uint32_t top = 0u;
-  const uint32_t key0 = C > 1 ? cluster_addr(s_key, 0) : 0u;
-  int stage = 0;
-  while (at < n_loads) {
+  int bad = 0, stage = 0;
+  for (int at = first; at < n_loads; at += step, ahead += step) {
     uint4* const slot = ring + stage * (kLpUnits * 32);
     stage = (stage + 1) % kLpStages;
     cp_async_wait<kLpStages - 1>();
     uint4 raw[kLpUnits];
 #pragma unroll
     for (int j = 0; j < kLpUnits; ++j) raw[j] = slot[j * 32];
-    const int done = at;
-    next(at);
-    const bool last = loads == 1 || at % loads == 0;  // of its chunk
-    const float um = units_max<T>(raw, 0, kLpUnits);
+    float um4[kLpUnits];
+#pragma unroll
+    for (int j = 0; j < kLpUnits; ++j) um4[j] = unit_max<T>(raw[j]);
+    const float um = max_nan(max_nan(um4[0], um4[1]), max_nan(um4[2], um4[3]));
     bad |= (um != um);
     if (k > 0) {
+#pragma unroll
+      for (int j = 0; j < kLpUnits; ++j) um4[j] = warp_max_nan(um4[j]);
       if (arrived) {
         cluster_wait();
         arrived = false;
       }
-#pragma unroll
-      for (int j = 0; j < kSub; ++j) {
-        top = max(top, order_key(kSub == 1 ? um : units_max<T>(raw, j * kKeyUnits, kKeyUnits)));
-        if (kSub > 1 || last) {
-          top = __reduce_max_sync(kFull, top);
-          const int i = kSub > 1 ? done * kSub + j : done / loads;
-          if (lane == 0) {
-            if (C > 1) cluster_put(key0 + 4u * (uint32_t)i, top);
-            else s_key[i] = top;
-          }
-          top = 0u;
+      if (lane == 0) {
+        const uint32_t most = order_key(max_nan(max_nan(um4[0], um4[1]), max_nan(um4[2], um4[3])));
+        if (C > 1) {
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(top0 + 16u * (uint32_t)at),
+                       "f"(um4[0]), "f"(um4[1]), "f"(um4[2]), "f"(um4[3])
+                       : "memory");
+          if (!job.refine) cluster_put(group0 + 4u * (uint32_t)at, most);
+        } else {
+          *reinterpret_cast<float4*>(&s_top[4 * at]) = make_float4(um4[0], um4[1], um4[2], um4[3]);
+          if (!job.refine) s_group[at] = most;
         }
       }
     }
@@ -381,7 +373,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     // the registers hold what the slot held
     if (ahead < n_loads) copy_units<T>(row, V, ahead, lane, slot);
     cp_async_commit();
-    next(ahead);
   }
   if (arrived) cluster_wait();
 
@@ -395,16 +386,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
   p = warp_join(p, c);
   bad = __any_sync(kFull, bad);
   if (lane == 0) {
-    const int i = rank * W + warp;
     if (C > 1) {
-      const uint32_t d = cluster_addr(&s_part[i], 0);
+      const uint32_t d = cluster_addr(&s_part[first], 0);
       cluster_put(d, __float_as_uint(p.m));
       cluster_put(d + 4, __float_as_uint(p.s_hi));
       cluster_put(d + 8, __float_as_uint(p.s_lo));
       cluster_put(d + 12, __float_as_uint(p.a));
       if (bad) cluster_put(cluster_addr(&s_bad, 0), 1u);
     } else {
-      s_part[i] = p;
+      s_part[first] = p;
       if (bad) s_bad = 1u;
     }
   }
@@ -416,57 +406,38 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     __syncthreads();
   }
 
-  // the k chunks with the largest maxima, in that order
-  const int n_keys = job.n_chunks * kSub, kk = min(k, n_keys);
-  if (kk > 0 && n_keys <= kLpCount) {
-    // a chunk's place is the number of chunks before it: larger ones, and equal ones to its left
-    for (int i = threadIdx.x; i < n_keys; i += blockDim.x) {
-      const uint32_t mine = s_key[i];
+  const int G = job.group, n_groups = (job.n_pieces + G - 1) / G, kg = min(k, n_groups);
+  if (k > 0) {
+    if (job.refine) {  // each group's largest piece
+      for (int i = threadIdx.x; i < n_groups; i += blockDim.x) {
+        uint32_t top = 0u;
+        for (int j = i * G; j < min((i + 1) * G, job.n_pieces); ++j) top = max(top, order_key(s_top[j]));
+        s_group[i] = top;
+      }
+      __syncthreads();
+    }
+    // a group's place is the number of groups before it: larger ones, and equal ones to its left
+    for (int i = threadIdx.x; i < n_groups; i += blockDim.x) {
+      const uint32_t mine = s_group[i];
       int before = 0;
-      for (int j = 0; j < n_keys; j += 4) {
-        const uint4 o = *reinterpret_cast<const uint4*>(&s_key[j]);
-        // of four chunks to the left an equal one counts, of four to the right it does not
+      for (int j = 0; j < n_groups; j += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&s_group[j]);
+        // of four groups to the left an equal one counts, of four to the right it does not
         const uint32_t than = j + 3 < i ? mine - 1u : mine;
-        before += (o.x > than) + (j + 1 < n_keys && o.y > than) + (j + 2 < n_keys && o.z > than) +
-                  (j + 3 < n_keys && o.w > than);
+        before += (o.x > than) + (j + 1 < n_groups && o.y > than) + (j + 2 < n_groups && o.z > than) +
+                  (j + 3 < n_groups && o.w > than);
       }
-      // the four around it
-      for (int j = i & ~3; j < i; ++j) before += s_key[j] == mine;
-      if (before < kk) {
+      for (int j = i & ~3; j < i; ++j) before += s_group[j] == mine;  // of the four around it
+      if (before < kg) {
         s_sel[before] = i;
-        if (before == kk - 1) s_tau = kk == k ? mine : 0u;  // with fewer chunks than k, every element counts
+        if (before == kg - 1) s_tau = kg == k ? mine : 0u;  // fewer groups than k: every piece counts
       }
     }
-  } else if (kk > 0 && warp == W - 1) {
-    uint32_t best = 0u;
-    int where = INT_MAX;
-    auto look = [&]() {
-      best = 0u;
-      where = INT_MAX;
-      for (int i = lane; i < n_keys; i += 32)
-        if (s_key[i] > best) {
-          best = s_key[i];
-          where = i;
-        }
-    };
-    look();
-    uint32_t most = 0u;
-    for (int j = 0; j < kk; ++j) {
-      most = __reduce_max_sync(kFull, best);
-      const int i = __reduce_min_sync(kFull, best == most ? where : INT_MAX);
-      if (lane == 0) s_sel[j] = i;
-      if (where == i) {
-        s_key[i] = 0u;
-        look();
-      }
-    }
-    if (lane == 0) s_tau = kk == k ? most : 0u;
   }
   // the row's sums
   if (warp == 0) {
-    const int parts = C * W;
-    Part q = lane < parts ? s_part[lane] : part_none();
-    if (lane + 32 < parts) {
+    Part q = lane < step ? s_part[lane] : part_none();
+    if (lane + 32 < step) {
       Part o = s_part[lane + 32];
       const float M = fmaxf(q.m, o.m);
       part_raise(q, M, c);
@@ -498,90 +469,106 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     write_nothing(job, r, threadIdx.x, blockDim.x, CUDART_NAN_F, CUDART_NAN_F, SPEC_ROW_NONFINITE);
     return;
   }
-  if (k == 0) {
-    write_given<T>(job, row, r, threadIdx.x, blockDim.x, M, log_s);
-    return;
-  }
-
-  // the elements at or above the k-th chunk's maximum, of the k chunks
-  const uint32_t tau = s_tau;
-  const int key_loads = kSub > 1 ? 1 : loads;
-  const int total = kk * key_loads;
-  auto look_at = [&](int i) {  // the i-th piece of the selected chunks: its load
-    const int sel = s_sel[i / key_loads];
-    return kSub > 1 ? sel / kSub : sel * loads + i % key_loads;
-  };
-  uint4 nxt[kLpUnits];
-  if (warp < total) load_units<T>(row, V, look_at(warp), lane, nxt);
   write_given<T>(job, row, r, threadIdx.x, blockDim.x, M, log_s);
-  for (int i = warp; i < total; i += W) {
-    uint4 raw[kLpUnits];
-#pragma unroll
-    for (int j = 0; j < kLpUnits; ++j) raw[j] = nxt[j];
-    const int l = look_at(i);
-    if (i + W < total) load_units<T>(row, V, look_at(i + W), lane, nxt);
-    const int only = kSub > 1 ? s_sel[i] % kSub : 0;
-#pragma unroll
-    for (int j = 0; j < kLpUnits; ++j) {
-      if (kSub > 1 && j != only) continue;  // kSub is kLpUnits: one unit per key
-      if (order_key(units_max<T>(raw, j, 1)) < tau) continue;
-      float f[E];
-      Elt<T>::unpack(raw[j], f);
-      const int i0 = (l * (32 * kLpUnits) + j * 32 + lane) * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (order_key(f[e]) >= tau && i0 + e < V) {
-          const int slot = atomicAdd(&s_count, 1);
-          if (slot < kLpCand)
-            s_list[slot] = ((uint64_t)order_key(f[e]) << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)(i0 + e));
-        }
-    }
-  }
-  __syncthreads();
-  const int found = s_count;
-  if (found <= kLpCand) {  // a candidate's place is the number of larger ones
-    for (int i = threadIdx.x; i < found; i += blockDim.x) {
-      const uint64_t mine = s_list[i];
-      int before = 0;
-      for (int j = 0; j < found; ++j) before += s_list[j] > mine;
-      if (before < k) {
-        const float z = key_value((uint32_t)(mine >> 32));
-        job.out_top[(int64_t)r * k + before] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
-        job.out_top_lp[(int64_t)r * k + before] = (z - M) * job.inv_t - log_s;
+  if (k == 0) return;
+
+  // the pieces of those groups at or above the k-th group's largest, by their places
+  const uint32_t tau = s_tau;
+  const bool refine = job.refine != 0;
+  int kp = kg * kLpUnits;
+  uint32_t tau2 = tau;
+  bool some = true;
+  if (refine) {
+    for (int i = threadIdx.x; i < kg * G; i += blockDim.x) {
+      const int piece = s_sel[i / G] * G + i % G;
+      if (piece < job.n_pieces && order_key(s_top[piece]) >= tau) {
+        const int slot = atomicAdd(&s_count, 1);
+        if (slot < kLpCand) s_list[slot] = key_of(s_top[piece], piece);
       }
     }
-    return;
+    __syncthreads();
+    const int count = s_count;
+    some = count <= kLpCand;
+    if (some) {
+      kp = min(k, count);
+      for (int i = threadIdx.x; i < count; i += blockDim.x) {
+        const uint64_t mine = s_list[i];
+        int before = 0;
+        for (int j = 0; j < count; ++j) before += s_list[j] > mine;
+        if (before < kp) {
+          s_piece[before] = (int)(0xFFFFFFFFu - (uint32_t)mine);
+          if (before == kp - 1) s_tau2 = kp == k ? (uint32_t)(mine >> 32) : 0u;
+        }
+      }
+      __syncthreads();
+      tau2 = s_tau2;
+    }
+  }
+  if (some) {
+    // their elements at or above the k-th piece's largest
+    auto piece_at = [&](int i) { return refine ? s_piece[i] : s_sel[i / kLpUnits] * kLpUnits + i % kLpUnits; };
+    for (int i0 = warp * kLpUnits; i0 < kp; i0 += W * kLpUnits) {
+      uint4 u[kLpUnits];
+#pragma unroll
+      for (int j = 0; j < kLpUnits; ++j)
+        if (i0 + j < kp) u[j] = load_unit_padded<T>(row, V, piece_at(i0 + j) * 32 + lane);
+#pragma unroll
+      for (int j = 0; j < kLpUnits; ++j) {
+        if (i0 + j >= kp || order_key(unit_max<T>(u[j])) < tau2) continue;
+        float f[E];
+        Elt<T>::unpack(u[j], f);
+        const int e0 = (piece_at(i0 + j) * 32 + lane) * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (order_key(f[e]) >= tau2 && e0 + e < V) {
+            const int slot = atomicAdd(&s_found, 1);
+            if (slot < kLpCand) s_list[slot] = key_of(f[e], e0 + e);
+          }
+      }
+    }
+    __syncthreads();
+    const int found = s_found;
+    if (found <= kLpCand) {
+      for (int i = threadIdx.x; i < found; i += blockDim.x) {
+        const uint64_t mine = s_list[i];
+        int before = 0;
+        for (int j = 0; j < found; ++j) before += s_list[j] > mine;
+        if (before < k) {
+          const float z = key_value((uint32_t)(mine >> 32));
+          job.out_top[(int64_t)r * k + before] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
+          job.out_top_lp[(int64_t)r * k + before] = (z - M) * job.inv_t - log_s;
+        }
+      }
+      return;
+    }
   }
 
-  // many equal ones: each warp keeps a list of its k largest
+  // many equal ones: each warp keeps a sorted list of its largest
   __syncthreads();
   uint64_t L = 0ull;
-  for (int i = warp; i < total; i += W) {
-    const int l = look_at(i), only = kSub > 1 ? s_sel[i] % kSub : -1;
-    load_units<T>(row, V, l, lane, nxt);
+  for (int i = warp; i < kg * G; i += W) {
+    const int piece = s_sel[i / G] * G + i % G;
+    if (piece >= job.n_pieces || order_key(s_top[piece]) < tau) continue;
+    const uint4 u = load_unit_padded<T>(row, V, piece * 32 + lane);
+    float f[E];
+    Elt<T>::unpack(u, f);
+    const int e0 = (piece * 32 + lane) * E;
 #pragma unroll 1
-    for (int u = 0; u < kLpUnits; ++u) {
-      if (only >= 0 && u != only) continue;
-      const uint4 x = u == 0 ? nxt[0] : u == 1 ? nxt[1] : u == 2 ? nxt[2] : nxt[3];
-      float f[E];
-      Elt<T>::unpack(x, f);
-      const int i0 = (l * (32 * kLpUnits) + u * 32 + lane) * E;
+    for (int e = 0; e < E; ++e) {
+      float z = f[0];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t o = order_key(f[e]);
-        const uint64_t key = ((uint64_t)o << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)(i0 + e));
-        const uint64_t lk = __shfl_sync(kFull, L, k - 1);
-        const bool in = o >= tau && i0 + e < V && key > lk;
-        uint32_t who = __ballot_sync(kFull, in);
-        if (__popc(who) <= 6) {
-          while (who) {
-            const int src = __ffs(who) - 1;
-            who &= who - 1;
-            L = list_insert(L, __shfl_sync(kFull, key, src), k, lane);
-          }
-        } else {
-          L = list_merge(L, warp_sort_desc(in ? key : 0ull, lane), lane);
+      for (int q = 1; q < E; ++q) z = e == q ? f[q] : z;
+      const uint64_t key = key_of(z, e0 + e), lk = __shfl_sync(kFull, L, k - 1);
+      const bool in = order_key(z) >= tau && e0 + e < V && key > lk;
+      uint32_t who = __ballot_sync(kFull, in);
+      if (__popc(who) <= 6) {
+        while (who) {
+          const int src = __ffs(who) - 1;
+          who &= who - 1;
+          L = list_insert(L, __shfl_sync(kFull, key, src), k, lane);
         }
+      } else {
+        L = list_merge(L, warp_sort_desc(in ? key : 0ull, lane), lane);
       }
     }
   }
@@ -689,37 +676,49 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
     else logprob_small_kernel<T, 32><<<blocks, kLpThreads, 0, s>>>(job);
     return cudaGetLastError();
   }
-  const int per_load = 32 * kLpUnits * Elt<T>::kPerUnit;
-  // a chunk is 1024 logits; a key per 512 bytes where that leaves few chunks
-  const bool fine = job.V <= kLpFineV;
-  const int per_chunk = fine ? per_load : 1024;
-  job.n_chunks = (job.V + per_chunk - 1) / per_chunk;
-  const int n_keys = job.n_chunks * (fine ? kLpUnits : 1);
+  const int per_piece = 32 * Elt<T>::kPerUnit;
+  job.n_pieces = (job.V + per_piece - 1) / per_piece;
+  job.n_loads = (job.n_pieces + kLpUnits - 1) / kLpUnits;
   // Warps per row: a wave of rows takes as long as a warp's loads and what finishing a row costs, about 8
-  // loads' time, in a cluster 12.  Measured (us, bf16 rows of 128256, k = 5): 8 rows 8.0 with 64
-  // warps, 9.1 with 32, 14.5 with 8; 152 rows 13.3 with 16, 15.1 with 8, 18.7 with 32; 640 rows 40.2 with
-  // 4, 41.8 with 8, 53.7 with 2; 3840 rows 188 with 8, 191 with 4, 207 with 2.
-  const int64_t room = (int64_t)device_sm_count() * kLpPerSm * kLpWarps;
-  const int64_t n_loads = ((int64_t)job.V + per_load - 1) / per_load;
+  // loads' time, in a cluster 12.  Measured (us, bf16 rows of 128256, k = 5): 8 rows 8.3 with 64
+  // warps, 9.6 with 32, 15.3 with 8; 152 rows 14.5 with 16, 16.1 with 8, 19.8 with 32; 640 rows 43 with
+  // 4 and with 8, 52 with 2; 3840 rows 180 with 2, 182 with 4, 188 with 8.
   int W = 1, C = 1;
-  int64_t least = INT64_MAX;
+  int64_t least = INT64_MAX, waves_of = 1;
   for (int w = 1; w <= kLpWarps * kLpMaxCluster; w *= 2) {
     const bool cluster = w > kLpWarps;
-    const int64_t waves = ((int64_t)job.R * w + room - 1) / room;
-    if (w > 1 && (w > job.n_chunks || (cluster && waves > 1))) break;
-    const int64_t cost = waves * ((n_loads + w - 1) / w + (cluster ? 12 : 8));
+    const int cta = cluster ? kLpWarps : w;
+    // what fits an SM: registers, and the rings and maxima in shared memory
+    int per_sm = kLpPerSm * kLpWarps / cta;
+    const int shared = (int)(cta * kLpRing) + job.n_loads * 16 + 7 * 1024;
+    if (per_sm > 227 * 1024 / shared) per_sm = 227 * 1024 / shared;
+    const int64_t room = (int64_t)device_sm_count() * per_sm;
+    const int64_t waves = ((int64_t)job.R * (w / cta) + room - 1) / room;
+    if (w > 1 && (w > job.n_loads || (cluster && waves > 1))) break;
+    const int64_t cost = waves * ((job.n_loads + w - 1) / w + (cluster ? 12 : 8));
     if (cost <= least) {
       least = cost;
-      W = w < kLpWarps ? w : kLpWarps;
-      C = w / W;
+      waves_of = waves;
+      W = cta;
+      C = w / cta;
     }
   }
-  int threads = 32 * W;
   job.cluster = C;
+  // Groups: counting takes the square of their number, ranking the pieces in them little, so the largest
+  // that leave 48 of them (k is at most 32).  1664 fp32 rows of 152064, k = 20: 156 us with 149 groups,
+  // 174 with 297.  Where the rows are one wave, time is latency: a load is a group then, and the chosen
+  // ones are read whole.  One bf16 row of 128256: 8.1 instead of 9.5 us.
+  job.refine = waves_of > 1 || job.n_loads > kLpGroups;
+  job.group = kLpUnits;
+  if (job.refine) {
+    job.group = 1;
+    while (job.n_pieces >= job.group * 2 * 48) job.group *= 2;
+  }
+  const int threads = 32 * W;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(job.R * C));
   cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)W * kLpRing + (job.k > 0 ? ((size_t)n_keys + 3) / 4 * 16 : 0);
+  cfg.dynamicSmemBytes = (size_t)W * kLpRing + (job.k > 0 ? (size_t)job.n_loads * 16 : 0);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -727,15 +726,15 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  auto kernel = fine ? logprob_rows_kernel<T, kLpUnits> : logprob_rows_kernel<T, 1>;
-  static bool configured[64][2] = {};
+  auto kernel = logprob_rows_kernel<T>;
+  static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !configured[dev][fine]) {
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpMaxShared);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured[dev][fine] = true;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   return cudaLaunchKernelEx(&cfg, kernel, job);
 }
