@@ -12,8 +12,8 @@
 // are fp32 numbers themselves.
 //
 // Memory-bound: 8 elements per thread, 16-byte loads and 4-byte stores side by side, rows in
-// groups of four loads in flight.  Blocks share their maximum over 4 (nv: 2) lanes, the four scales of a
-// tile's row go out as one word.
+// groups of four loads in flight.  Blocks share their maximum over 4 (nv: 2) lanes; the scales of four blocks
+// in four rows are transposed over lanes and go out as four words.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -124,30 +124,35 @@ __device__ __forceinline__ uint32_t encode8(float (&f)[8], float top, float ts, 
 }
 
 template <typename T, spec_fp4_format F>
-__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 6 : 5) quantize_kernel(QuantJob job) {
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 && F == SPEC_FP4_MX ? 6 : 5) quantize_kernel(QuantJob job) {
   constexpr int kLanes = F == SPEC_FP4_MX ? 4 : 2;  // lanes of a block
   constexpr int kRows = sizeof(T) == 2 ? kQRows : kQRows / 2;  // in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t tile = blockIdx.x / (unsigned)job.segments;
   const int c = (int)(blockIdx.x % (unsigned)job.segments) * kQTileCols + lane * 8;
   const int K = job.K;
-  const int g = c / (kLanes * 32);  // this lane's scale tile along the row
+  const int r0 = (int)(tile * kQTileRows) + warp;
+  constexpr int kStep = kQThreads / 32;  // between this warp's rows
+  const char* x = static_cast<const char*>(job.x) + (int64_t)r0 * job.pitch_bytes;
+  uint8_t* out = job.codes + (int64_t)r0 * job.row_bytes + c / 2;
+  const bool in_row = c < K, in_codes = c < 2 * job.row_bytes;
+  uint32_t bytes = 0u;  // this lane's block's scale in each of the rows
+#pragma unroll
   for (int i0 = 0; i0 < kQRows; i0 += kRows) {
-    const int r0 = (int)(tile * kQTileRows) + i0 * (kQThreads / 32) + warp;
     Raw8<T> raw[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int r = r0 + i * (kQThreads / 32);
-      if (r < job.R && c < K) {
-        load8<T>(static_cast<const char*>(job.x) + (int64_t)r * job.pitch_bytes, c, K, raw[i]);
+      if (in_row && r0 + (i0 + i) * kStep < job.R) {
+        load8<T>(x, c, K, raw[i]);
       } else {
 #pragma unroll
         for (int u = 0; u < Raw8<T>::kUnits; ++u) raw[i].u[u] = make_uint4(0u, 0u, 0u, 0u);
       }
+      x += kStep * job.pitch_bytes;
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int r = r0 + i * (kQThreads / 32);
+      const bool real = r0 + (i0 + i) * kStep < job.R;
       float f[8];
       unpack8<T>(raw[i], f);
       float top = 0.f;
@@ -157,17 +162,23 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 6 : 5) quantize_ke
       for (int o = 1; o < kLanes; o <<= 1) top = abs_max_nan(top, __shfl_xor_sync(kFull, top, o));
       uint32_t byte;
       const uint32_t codes = encode8<F>(f, top, job.ts, byte);
-      if (r < job.R && c < 2 * job.row_bytes)
-        *reinterpret_cast<uint32_t*>(job.codes + (int64_t)r * job.row_bytes + c / 2) = codes;
-      // the four scales of a tile's row as one word; past the row's end, and in rows past the
-      // last, they are zero
-      if (c >= K || r >= job.R) byte = 0u;
-      byte |= __shfl_down_sync(kFull, byte, kLanes) << 8;
-      byte |= __shfl_down_sync(kFull, byte, 2 * kLanes) << 16;
-      if (lane % (4 * kLanes) == 0 && g < job.groups)
-        *reinterpret_cast<uint32_t*>(job.scales + fp4_scale_at(r, 4 * g, job.groups)) = byte;
+      if (real && in_codes) *reinterpret_cast<uint32_t*>(out) = codes;
+      // past the row's end, and in rows past the last, scales are zero
+      if (in_row && real) bytes |= byte << (8 * (i0 + i));
+      out += kStep * job.row_bytes;
     }
   }
+  // the four scales of a tile's row as one word: of the lanes of four blocks the first four each take
+  // one of the rows
+  constexpr int kSpan = 4 * kLanes;
+  const int mine = lane & (kSpan - 1), from = lane & ~(kSpan - 1), g = c / (kLanes * 32);
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = __shfl_sync(kFull, bytes, from + q * kLanes);
+  const uint32_t pick = (uint32_t)(mine & 3) * 0x11u + 0x40u;  // this row's byte of two words
+  const uint32_t word = __byte_perm(__byte_perm(w[0], w[1], pick), __byte_perm(w[2], w[3], pick), 0x5410u);
+  if (mine < 4 && g < job.groups)
+    *reinterpret_cast<uint32_t*>(job.scales + fp4_scale_at(r0 + mine * kStep, 4 * g, job.groups)) = word;
 }
 
 struct DequantJob {
