@@ -4,14 +4,25 @@
 // tensor cores as they are stored, products are exact and summed in fp32, the result is rounded once.
 //
 // The weight's rows are the tile's M (128 per CTA), the activations' rows its N (16 to 192): a head
-// has many of the former, a decoding step any number of the latter.  Persistent CTAs, K in steps of 256
-// elements (rows of 128 bytes):
+// has many of the former, a decoding step any number of the latter.  Above 128 activation rows two CTAs
+// share a 256-row tile (cta_group::2), each with its half of both operands.  Persistent CTAs, K in steps
+// of 256 elements (rows of 128 bytes, four products):
 //   warp 0      TMA producer: codes of both operands with the 128-byte swizzle and their scale tiles
-//               (512 contiguous bytes each) into a ring of stages
+//               (512 contiguous bytes each) into a ring of 4 to 10 stages
 //   warp 1      copies a stage's scales to tensor memory (tcgen05.cp, ordered before the products that
-//               read them) and issues four K = 64 products into one of two accumulators
-//   warps 2-5   epilogue: a thread has one weight row, reads 32 columns at a time
+//               read them) and issues the products into one of two accumulators of 192 columns
+//   warps 2-5   epilogue: 32 weight rows a warp, 32 activation rows at a time, transposed in shared memory
+//               (stmatrix) and stored in bulk
+// Where weight rows are few, clusters share a tile's K instead and join in shared memory (kSplit).
 // Every wait is bounded; a tile whose accumulator does not come is written as NaN.
+//
+// What bounds it (GB300, 128256 x 4096): up to 128 rows the weight's bytes (one row nv, 295 MB: 48 us, 6.1
+// TB/s, 90 % of the copy bandwidth; 128 rows mx 51 us), from there the tensor cores: 3840 rows mx 576 us,
+// 7.0 PFLOP/s, the tensor pipe 67 % active on 16384 weight rows.  What it took: the issuing warp whole and
+// its descriptors in uniform registers (issuing a stage took 500 cycles, its products take 390), low words of
+// descriptors computed once a stage (nv 99 -> 86 us at 3840 x 16384 x 4096), the transposed epilogue
+// (two-byte stores by lane: 1152 us instead of 983 then).  No gain: scales copied a stage ahead of the
+// products (124 us instead of 99), peeking at the next stage's barrier, longer suspensions in waits.
 #include <cuda.h>
 
 #include <cuda_bf16.h>
@@ -28,6 +39,8 @@ constexpr int kFlMaxN = 192;     // activation rows of a tile
 constexpr int kFlK = 256;        // elements of a stage
 constexpr int kFlMaxStages = 10;
 constexpr int kFlThreads = 192;
+constexpr int kFlMaxSplit = 8;
+constexpr int kFlSplitCtas = 128;  // in clusters of eight, as whole clusters fit the chip's GPCs
 constexpr uint32_t kFlABytes = kFlM * kFlK / 2;
 constexpr uint32_t kFlSfCol = 2 * kFlMaxN;  // first tensor-memory column of the scales
 constexpr uint32_t kFlSfBuf = 64;           // columns of one of the two buffers
@@ -257,9 +270,30 @@ struct Ring {
   }
 };
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// Four floats at a shared-memory address of CTA `cta` of the cluster, and of this one.
+__device__ __forceinline__ void put_four(uint32_t addr, uint32_t cta, const uint32_t* x) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(addr), "r"(cta));
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3])
+               : "memory");
+}
+__device__ __forceinline__ float4 get_four(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+
 struct LinearJob {
   int R, V;
   int m_tiles, n_tiles, tile_n;
+  int split;              // CTAs of a cluster that share a tile's K (kSplit)
   int k_steps, last_mma;  // stages along K, products of the last one
   int groups;             // scale tiles along K
   int sf_chunks;          // row tiles of the activations' scales that a tile's rows touch
@@ -276,7 +310,7 @@ struct LinearShared {
   uint32_t tmem;
 };
 
-template <int CG, spec_fp4_format F, typename O>
+template <int CG, spec_fp4_format F, typename O, bool kSplit>
 __global__ void __launch_bounds__(kFlThreads, 1)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                       const __grid_constant__ CUtensorMap tm_ws,
@@ -294,7 +328,12 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   // as a uniform value, so that the roles' loops keep descriptors and addresses in uniform registers
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1u);
-  const int group = (int)blockIdx.x / CG, n_groups = (int)gridDim.x / CG;
+  const int share = kSplit ? job.split : CG;  // CTAs of a tile
+  const int group = (int)blockIdx.x / share, n_groups = (int)gridDim.x / share;
+  // the stages along K that this CTA takes
+  const int part = kSplit ? (int)blockIdx.x % job.split : 0;
+  const int k0 = kSplit ? job.k_steps * part / job.split : 0;
+  const int k1 = kSplit ? job.k_steps * (part + 1) / job.split : job.k_steps;
   const int tiles = job.m_tiles * job.n_tiles;
   const uint64_t limit = job.wait_limit_ns;
   const int stages = job.stages;
@@ -327,7 +366,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
       const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
       const int row_w = ((t / job.n_tiles) * CG + rank) * kFlM, row_a = n0 + rank * (n / CG);
       const int tile_w = (row_w >> 7) * job.groups, tile_a = (n0 >> 7) * job.groups;
-      for (int kb = 0; kb < job.k_steps; ++kb, ring.next(stages)) {
+      for (int kb = k0; kb < k1; ++kb, ring.next(stages)) {
         if (!__all_sync(kFull, fp4_wait(&sh.empty[ring.s], ring.phase ^ 1u, limit))) {
           stop = true;
           break;
@@ -378,11 +417,11 @@ __global__ void __launch_bounds__(kFlThreads, 1)
             const int g = F == SPEC_FP4_MX ? j >> 1 : j;
             fp4_mma<CG, F>(d, (a + j * 2) | kCodeDescLow, (b + j * 2) | kCodeDescLow,
                            F == SPEC_FP4_MX && (j & 1) ? idesc2 : idesc0, sfa + g * 4, sfb + g * step,
-                           (kb | j) != 0);
+                           kb != k0 || j != 0);
           }
         }
       };
-      for (int kb = 0; kb < job.k_steps; ++kb, ring.next(stages), ++it) {
+      for (int kb = k0; kb < k1; ++kb, ring.next(stages), ++it) {
         const int s = ring.s;
         if (!__all_sync(kFull, fp4_wait(&sh.full[s], ring.phase, limit))) {
           stop = true;
@@ -409,12 +448,12 @@ __global__ void __launch_bounds__(kFlThreads, 1)
             issue(d, a, sfa, sfb + off_b, 8, kb);
           }
           fp4_commit<CG>(&sh.empty[s]);
-          if (kb + 1 == job.k_steps) fp4_commit<CG>(&sh.tfull[acc]);
+          if (kb + 1 == k1) fp4_commit<CG>(&sh.tfull[acc]);
         }
         __syncwarp();
       }
     }
-  } else if (warp >= 2) {
+  } else if (warp >= 2 && !kSplit) {
     // ---------------- epilogue ----------------
     const int quarter = warp & 3;  // this warp's lanes of tensor memory, 32 of the tile's weight rows
     const uint32_t staging = base + (uint32_t)stages * stage_pitch + (uint32_t)quarter * 2 * kStageOut;
@@ -456,6 +495,66 @@ __global__ void __launch_bounds__(kFlThreads, 1)
       }
     }
     if (lane == 0) bulk_store_wait();
+  }
+  if constexpr (kSplit) {
+    // The parts of a tile along K are joined in shared memory, which the stages no longer need: every CTA of
+    // the cluster owns an equal run of the activations' rows, in fours, and gets the others' parts of them.
+    // One tile per cluster.
+    const int quarter = warp & 3, n = job.R, own = (n + 4 * job.split - 1) / (4 * job.split);  // fours
+    const int lane_v = quarter * 32 + lane, v = group * kFlM + lane_v;
+    bool lost = false;
+    __syncwarp();
+    if (warp >= 2) lost = !__all_sync(kFull, fp4_wait(&sh.tfull[0], 0u, limit));
+    cluster_sync();  // all products of the tile are done
+    if (warp >= 2) {
+      tc05_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < n; c0 += 32) {
+        uint32_t x[32];
+        tc05_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c0, x);
+        tc05_wait_ld();
+        tc05_landed(x);
+        int owner = c0 / 4 / own, four = c0 / 4 % own;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (c0 + 4 * i < n) {
+            if (lost) x[4 * i] = x[4 * i + 1] = x[4 * i + 2] = x[4 * i + 3] = 0x7fffffffu;
+            put_four(base + (uint32_t)((part * own + four) * kFlM + lane_v) * 16, (uint32_t)owner, x + 4 * i);
+            if (++four == own) {
+              four = 0;
+              ++owner;
+            }
+          }
+        }
+      }
+      tc05_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();  // the parts are there
+    if (warp >= 2 && v < job.V) {
+      const int row0 = part * own * 4;
+      for (int four = 0; four < own && row0 + four * 4 < n; ++four) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < job.split; ++q) {
+          const float4 x = get_four(base + (uint32_t)((q * own + four) * kFlM + lane_v) * 16);
+          y.x += x.x;
+          y.y += x.y;
+          y.z += x.z;
+          y.w += x.w;
+        }
+        const float z[4] = {y.x, y.y, y.z, y.w};
+        O* out = static_cast<O*>(job.out) + (int64_t)(row0 + four * 4) * job.pitch + v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (row0 + four * 4 + i < n) {
+            if constexpr (sizeof(O) == 2)
+              reinterpret_cast<__nv_bfloat16*>(out)[i * job.pitch] = __float2bfloat16_rn(z[i] * job.alpha);
+            else
+              out[i * job.pitch] = z[i] * job.alpha;
+          }
+        }
+      }
+    }
   }
   __syncwarp();
   tc05_fence_before();
@@ -520,7 +619,7 @@ bool out_map(CUtensorMap* map, void* p, int R, int V, int64_t pitch) {
                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, spec_fp4_format F, typename O>
+template <int CG, spec_fp4_format F, typename O, bool kSplit = false>
 cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, const void* w_scales,
                           int K, LinearJob job, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
@@ -544,7 +643,7 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
       !scale_map(&tm_as, a_scales, (int64_t)fp4_row_tiles(job.R) * job.groups, kGroups) ||
       !out_map<O>(&tm_out, job.out, job.R, job.V, job.pitch))
     return cudaErrorInvalidValue;
-  auto kernel = fp4_linear_kernel<CG, F, O>;
+  auto kernel = fp4_linear_kernel<CG, F, O, kSplit>;
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -556,24 +655,40 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
   }
   int64_t groups = device_sm_count() / CG;
   if (groups > (int64_t)job.m_tiles * job.n_tiles) groups = (int64_t)job.m_tiles * job.n_tiles;
+  const int cluster = kSplit ? job.split : CG;
+  if (kSplit) groups = job.m_tiles;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * CG));
+  cfg.gridDim = dim3((unsigned)(groups * cluster));
   cfg.blockDim = dim3(kFlThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.x = (unsigned)cluster;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, tm_ws, tm_as, tm_out, job);
 }
 
 template <spec_fp4_format F, typename O>
 cudaError_t launch_linear_group(const void* a, const void* a_scales, const void* w, const void* w_scales,
                                 int K, LinearJob job, cudaStream_t s) {
-  if (job.R > 64) return launch_linear<2, F, O>(a, a_scales, w, w_scales, K, job, s);
+  // Few weight rows: clusters of up to eight CTAs share a tile's K, two stages each at least, where that many
+  // are resident at once and what it saves, a quarter of a microsecond a stage, is more than the join
+  // costs, one and a thirtieth per activation row.  Measured (us, mx, shared and not): 1 x 4096 x 4096 5.1
+  // and 6.6, 60 x 4096 x 8192 7.9 and 10.7, 1 x 4096 x 14336 7.5 and 15.4, 192 x 4096 x 14336 14.6 and
+  // 18.3; but 128 x 4096 x 4096 9.2 and 8.6, 64 x 8192 x 4096 8.2 and 7.2.
+  const int tiles = (job.V + kFlM - 1) / kFlM, steps = (int)((fp4_row_bytes(K) * 2 + kFlK - 1) / kFlK);
+  job.split = 1;
+  while (job.split < kFlMaxSplit && tiles * job.split * 2 <= kFlSplitCtas && steps >= job.split * 4)
+    job.split *= 2;
+  if (job.n_tiles == 1 && 7 * (int64_t)steps * (job.split - 1) >= (int64_t)job.split * (30 + job.R))
+    return launch_linear<1, F, O, true>(a, a_scales, w, w_scales, K, job, s);
+  // Pairs of CTAs halve the reads of the activations; below, the weight's bytes bound both and single CTAs start
+  // sooner.  Measured on 128256 x 4096 (us, mx, pairs and not): 60 rows 51.3 and 48.0, 128 rows 52.1 and
+  // 51.4, 192 rows 54.8 and 57.9, 3840 rows 576 and 710.
+  if (job.R > 128) return launch_linear<2, F, O>(a, a_scales, w, w_scales, K, job, s);
   return launch_linear<1, F, O>(a, a_scales, w, w_scales, K, job, s);
 }
 
@@ -617,7 +732,7 @@ extern "C" int spec_fp4_linear(const void* a_codes, const void* a_scales, const 
   if (format != SPEC_FP4_MX && format != SPEC_FP4_NV) return SPEC_ERR_UNSUPPORTED_DTYPE;
   if (R < 0 || V < 1 || K < 1 || row_pitch < V) return SPEC_ERR_INVALID_ARG;
   if (!(alpha >= -3.402823466e38f && alpha <= 3.402823466e38f)) return SPEC_ERR_INVALID_ARG;
-  if (R > SPEC_FP4_MAX_DIM || V > SPEC_FP4_MAX_DIM || K > SPEC_FP4_MAX_DIM || row_pitch > INT64_MAX / 8 / SPEC_FP4_MAX_DIM ||
+  if (R > SPEC_FP4_MAX_DIM || V > SPEC_FP4_MAX_DIM || K > SPEC_FP4_MAX_DIM || row_pitch >= (int64_t)1 << 37 ||
       (int64_t)fp4_row_tiles(R > V ? R : V) * fp4_groups(K, format) > INT32_MAX - 8 ||
       ((int64_t)R + 63) / 64 * (((int64_t)V + 127) / 128) > INT32_MAX)
     return SPEC_ERR_TOO_LARGE;

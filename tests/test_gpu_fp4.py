@@ -199,6 +199,32 @@ def test_linear_long(fmt, R, V, K):
     _check_exact(R, V, K, fmt, F32, spread=0 if K > 1000 else 1)
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("R,V,K", [(1, 128, 1024), (1, 1, 2048), (2, 4096, 1024), (5, 200, 2080), (7, 515, 4096), (31, 640, 1100),
+                                   (64, 1000, 1500), (65, 130, 2047), (130, 300, 1500), (192, 700, 1056),
+                                   (33, 4100, 777)])
+def test_linear_of_few_weight_rows(fmt, R, V, K):
+    """Tiles whose K several CTAs share: exact whatever the order, in both types."""
+    _check_exact(R, V, K, fmt, F32, spread=0)
+    _check_exact(R, V, K, fmt, BF, alpha=2.0, spread=0)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_linear_of_extreme_scales(fmt):
+    """The smallest scale of one operand against the largest of the other: products that fp32 holds."""
+    if fmt == "mx":  # 2^-127 and 2^127; 2^-64 and 2^64
+        pairs = [(0, 254), (254, 0), (63, 191), (1, 253)]
+    else:  # the smallest subnormal, the largest subnormal, 448
+        pairs = [(1, 126), (126, 1), (7, 7), (8, 120), (3, 64)]
+    for sa, sw in pairs:
+        a, w = _random(20, 192, fmt, sa), _random(150, 192, fmt, sw + 300)
+        a[1][:], w[1][:] = sa, sw
+        want, _ = oracle_fp4.linear(oracle_fp4.values(*a, fmt), oracle_fp4.values(*w, fmt))
+        got = binding.fp4_linear(_matrix(*a, fmt), _matrix(*w, fmt), F32)
+        # one scale for all: a multiple of a quarter of it, at most 36 * 192 of them
+        np.testing.assert_array_equal(_host(got), want.astype(np.float32))
+
+
 def test_linear_takes_the_tensor_scales():
     a, w = _random(5, 64, "nv", 1), _random(70, 64, "nv", 2)
     want, _ = oracle_fp4.linear(oracle_fp4.values(*a, "nv", 0.25), oracle_fp4.values(*w, "nv", 2.0 ** -10), 3.0)
