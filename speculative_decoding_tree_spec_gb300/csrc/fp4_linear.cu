@@ -355,6 +355,8 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   if (CG > 1) group_sync<CG>();
   tc05_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
+  // up to here the launch may overlap the end of the one before it, whose results are read from here on
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -662,12 +664,14 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
   cfg.blockDim = dim3(kFlThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, tm_ws, tm_as, tm_out, job);
 }
 

@@ -41,6 +41,7 @@ constexpr int kLpMaxCluster = 8;
 constexpr int kLpSmallV = 1024;
 // the ring of eight warps and the maxima of the widest fp32 row
 constexpr int kLpMaxShared = (int)(kLpWarps * kLpRing) + SPEC_MAX_VOCAB / 32;
+constexpr size_t kLpTwoPerSm = 96 * 1024;  // shared memory that leaves room for two CTAs
 constexpr int kLpCand = 256;     // candidates ranked by counting
 constexpr int kLpGroups = 128;   // groups ranked by counting
 
@@ -132,16 +133,19 @@ __device__ __forceinline__ int row_of(const LogprobJob& job, int r) {
   return (unsigned)n < (unsigned)job.n_rows ? n : -1;
 }
 
-// The given tokens' log probabilities; a token outside the vocabulary has none.
+// A given token's log probability; one outside the vocabulary has none.
+template <typename T>
+__device__ __forceinline__ float given_logprob(const LogprobJob& job, const void* row, int tok, float M,
+                                               float log_s) {
+  return (unsigned)tok < (unsigned)job.V ? (Elt<T>::at(row, tok) - M) * job.inv_t - log_s : -CUDART_INF_F;
+}
+// Those of the tokens from t on, `step` apart.
 template <typename T>
 __device__ __forceinline__ void write_given(const LogprobJob& job, const void* row, int r, int t,
                                             int step, float M, float log_s) {
-  for (int g = t; g < job.G; g += step) {
-    const int tok = job.tokens[(int64_t)r * job.G + g];
-    float lp = -CUDART_INF_F;
-    if ((unsigned)tok < (unsigned)job.V) lp = (Elt<T>::at(row, tok) - M) * job.inv_t - log_s;
-    job.out_lp[(int64_t)r * job.G + g] = lp;
-  }
+  for (int g = t; g < job.G; g += step)
+    job.out_lp[(int64_t)r * job.G + g] =
+        given_logprob<T>(job, row, job.tokens[(int64_t)r * job.G + g], M, log_s);
 }
 
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
@@ -598,6 +602,8 @@ __global__ void __launch_bounds__(kLpThreads) logprob_small_kernel(LogprobJob jo
   }
   const void* row = static_cast<const char*>(job.base) + (int64_t)n * job.pitch_bytes;
   const int V = job.V, k = job.k;
+  // the first given tokens, while the row is on its way
+  const int tok = lane < job.G ? job.tokens[(int64_t)r * job.G + lane] : -1;
   float z[kE];
   float m = -CUDART_INF_F;
   bool nan = false;
@@ -629,7 +635,8 @@ __global__ void __launch_bounds__(kLpThreads) logprob_small_kernel(LogprobJob jo
   p.s_lo = s.lo;
   p.a = warp_sum_f(p.a);
   const float log_s = part_log(p);
-  write_given<T>(job, row, r, lane, 32, M, log_s);
+  if (lane < job.G) job.out_lp[(int64_t)r * job.G + lane] = given_logprob<T>(job, row, tok, M, log_s);
+  write_given<T>(job, row, r, lane + 32, 32, M, log_s);
   if (lane == 0) {
     if (job.out_entropy) job.out_entropy[r] = part_entropy(p, log_s);
     if (job.out_status) job.out_status[r] = SPEC_TREE_OK;
@@ -719,6 +726,12 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(job.R * C));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)W * kLpRing + (job.k > 0 ? (size_t)job.n_loads * 16 : 0);
+  // Given row numbers, some of them name no row (behind the ends of accepted paths): two CTAs of eight warps
+  // per SM then, so that those to come take the places of those without a row, instead of three, all at
+  // once, which leaves three rows on some SMs and none on others.  448 bf16 rows of 128256: 21 us instead
+  // of 27 where 253 of them are rows, 34 instead of 28 where all are.
+  if (job.rows && C == 1 && W == kLpWarps && job.R > 2 * device_sm_count() && cfg.dynamicSmemBytes < kLpTwoPerSm)
+    cfg.dynamicSmemBytes = kLpTwoPerSm;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -127,6 +127,7 @@ template <typename T, spec_fp4_format F>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 && F == SPEC_FP4_MX ? 6 : 5) quantize_kernel(QuantJob job) {
   constexpr int kLanes = F == SPEC_FP4_MX ? 4 : 2;  // lanes of a block
   constexpr int kRows = sizeof(T) == 2 ? kQRows : kQRows / 2;  // in flight
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // a product may line up
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t tile = blockIdx.x / (unsigned)job.segments;
   const int c = (int)(blockIdx.x % (unsigned)job.segments) * kQTileCols + lane * 8;
