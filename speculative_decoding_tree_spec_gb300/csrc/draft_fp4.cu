@@ -1,6 +1,6 @@
-// draft_fp4.cu -- the draft LM head kept in 4 bits and the ranking of its logits in one call: the features are
-// quantised (quantize.cu), multiplied (fp4_linear.cu) and the bf16 logits ranked (draft.cu).  The head is
-// what such a call reads: 0.28 GB instead of 1.05 GB for 128256 x 4096.
+// draft_fp4.cu -- the draft LM head kept in 4 bits and the ranking of its logits in one call: the
+// features are quantised (quantize.cu), multiplied (fp4_linear.cu) and the bf16 logits ranked
+// (draft.cu).  The head is what such a call reads: 0.28 GB instead of 1.05 GB for 128256 x 4096.
 #include "fp4.cuh"
 
 namespace svk {

@@ -1,12 +1,13 @@
 // fp4_linear.cu -- the product of two matrices in block-scaled 4-bit floating point,
 //   out[r][v] = alpha sum_k a[r][k] w[v][k],
 // on the fifth-generation tensor cores (tcgen05.mma with block scales): codes and scales go to the
-// tensor cores as they are stored, products are exact and summed in fp32, the result is rounded once.
+// tensor cores as they are stored, products are exact and summed in fp32, the result is rounded
+// once.
 //
 // The weight's rows are the tile's M (128 per CTA), the activations' rows its N (16 to 192): a head
-// has many of the former, a decoding step any number of the latter.  Above 128 activation rows two CTAs
-// share a 256-row tile (cta_group::2), each with its half of both operands.  Persistent CTAs, K in steps
-// of 256 elements (rows of 128 bytes, four products):
+// has many of the former, a decoding step any number of the latter.  Above 128 activation rows two
+// CTAs share a 256-row tile (cta_group::2), each with its half of both operands.  Persistent CTAs,
+// K in steps of 256 elements (rows of 128 bytes, four products):
 //   warp 0      TMA producer: codes of both operands with the 128-byte swizzle and their scale tiles
 //               (512 contiguous bytes each) into a ring of 4 to 10 stages
 //   warp 1      copies a stage's scales to tensor memory (tcgen05.cp, ordered before the products that
@@ -16,13 +17,14 @@
 // Where weight rows are few, clusters share a tile's K instead and join in shared memory (kSplit).
 // Every wait is bounded; a tile whose accumulator does not come is written as NaN.
 //
-// What bounds it (GB300, 128256 x 4096): up to 128 rows the weight's bytes (one row nv, 295 MB: 48 us, 6.1
-// TB/s, 90 % of the copy bandwidth; 128 rows mx 51 us), from there the tensor cores: 3840 rows mx 576 us,
-// 7.0 PFLOP/s, the tensor pipe 67 % active on 16384 weight rows.  What it took: the issuing warp whole and
-// its descriptors in uniform registers (issuing a stage took 500 cycles, its products take 390), low words of
-// descriptors computed once a stage (nv 99 -> 86 us at 3840 x 16384 x 4096), the transposed epilogue
-// (two-byte stores by lane: 1152 us instead of 983 then).  No gain: scales copied a stage ahead of the
-// products (124 us instead of 99), peeking at the next stage's barrier, longer suspensions in waits.
+// What bounds it (GB300, 128256 x 4096): up to 128 rows the weight's bytes (one row nv, 295 MB: 48
+// us, 6.1 TB/s, 90 % of the copy bandwidth; 128 rows mx 51 us), from there the tensor cores: 3840
+// rows mx 576 us, 7.0 PFLOP/s, the tensor pipe 67 % active on 16384 weight rows.  What it took: the
+// issuing warp whole and its descriptors in uniform registers (issuing a stage took 500 cycles, its
+// products take 390), low words of descriptors computed once a stage (nv 99 -> 86 us at 3840 x
+// 16384 x 4096), the transposed epilogue (two-byte stores by lane: 1152 us instead of 983 then).
+// No gain: scales copied a stage ahead of the products (124 us instead of 99), peeking at the next
+// stage's barrier, longer suspensions in waits.
 #include <cuda.h>
 
 #include <cuda_bf16.h>
@@ -65,9 +67,9 @@ __device__ __forceinline__ uint32_t fp4_idesc(int m, int n, int sf) {
   return (1u << 7) | (1u << 10) | ((uint32_t)sf << 4) | ((uint32_t)(n >> 3) << 17) |
          ((F == SPEC_FP4_MX ? 1u : 0u) << 23) | ((uint32_t)(m >> 4) << 24) | ((uint32_t)sf << 29);
 }
-// Shared-memory descriptors, of which the low word changes from one to the next (by bytes / 16): scales,
-// 32 rows of 16 bytes without a swizzle, 8-row groups 128 bytes apart; codes, rows of 128 bytes with
-// that swizzle (sw128_tile).
+// Shared-memory descriptors, of which the low word changes from one to the next (by bytes / 16):
+// scales, 32 rows of 16 bytes without a swizzle, 8-row groups 128 bytes apart; codes, rows of 128
+// bytes with that swizzle (sw128_tile).
 constexpr uint32_t kScaleDescHigh = (128u >> 4) | (1u << 14);
 constexpr uint32_t kCodeDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kCodeDescLow = (16u >> 4) << 16;
@@ -171,14 +173,16 @@ __device__ __forceinline__ void group_sync() {
                      : "memory");
 }
 
-// The epilogue takes 32 columns (activation rows) of its 32 lanes (weight rows) at a time, leaves them in shared
-// memory as 32 rows of 32 results side by side, and a bulk store takes them out, clipped to the matrix.
+// The epilogue takes 32 columns (activation rows) of its 32 lanes (weight rows) at a time, leaves
+// them in shared memory as 32 rows of 32 results side by side, and a bulk store takes them out,
+// clipped to the matrix.
 template <typename O>
 __host__ __device__ constexpr uint32_t out_stage_bytes() {
   return 32 * 32 * sizeof(O);
 }
-// bf16: pieces of 16 lanes by 8 columns, as the transposing stmatrix wants them (a register pair is two
-// columns of one lane); x[0..15] lanes 0..15, x[16..31] lanes 16..31.  fp32: a lane's 32 columns.
+// bf16: pieces of 16 lanes by 8 columns, as the transposing stmatrix wants them (a register pair is
+// two columns of one lane); x[0..15] lanes 0..15, x[16..31] lanes 16..31.  fp32: a lane's 32
+// columns.
 template <typename O>
 __device__ __forceinline__ void load_out(uint32_t taddr, uint32_t (&x)[32]) {
   if constexpr (sizeof(O) == 2) {
@@ -325,7 +329,8 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   const uint32_t stage_bytes =
       kFlABytes + job.b_bytes + kSfaBytes + (uint32_t)job.sf_chunks * kSfaBytes;
   const uint32_t stage_pitch = (stage_bytes + 1023u) & ~1023u;
-  // as a uniform value, so that the roles' loops keep descriptors and addresses in uniform registers
+  // as a uniform value, so that the roles' loops keep descriptors and addresses in uniform
+  // registers
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = CG == 1 ? 0 : (int)(blockIdx.x & 1u);
   const int share = kSplit ? job.split : CG;  // CTAs of a tile
@@ -355,7 +360,8 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   if (CG > 1) group_sync<CG>();
   tc05_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
-  // up to here the launch may overlap the end of the one before it, whose results are read from here on
+  // up to here the launch may overlap the end of the one before it, whose results are read from
+  // here on
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   if (warp == 0) {
@@ -408,8 +414,9 @@ __global__ void __launch_bounds__(kFlThreads, 1)
       const uint32_t d = tmem + (uint32_t)(acc * kFlMaxN);
       const uint32_t off_b = (uint32_t)(n0 & 127) >> 5;
       const uint32_t idesc0 = fp4_idesc<F>(kFlM * CG, n, 0), idesc2 = fp4_idesc<F>(kFlM * CG, n, 2);
-      // the products of a stage; of the last one those that K reaches.  `step`: columns of a group's
-      // activation scales.  The next 64 elements are 32 bytes further along the swizzled rows.
+      // the products of a stage; of the last one those that K reaches.  `step`: columns of a
+      // group's activation scales.  The next 64 elements are 32 bytes further along the swizzled
+      // rows.
       auto issue = [&](uint32_t d, uint32_t a, uint32_t sfa, uint32_t sfb, int step, int kb) {
         const uint32_t b = a + (kFlABytes >> 4);
         const int products = kb + 1 == job.k_steps ? job.last_mma : 4;
@@ -499,9 +506,9 @@ __global__ void __launch_bounds__(kFlThreads, 1)
     if (lane == 0) bulk_store_wait();
   }
   if constexpr (kSplit) {
-    // The parts of a tile along K are joined in shared memory, which the stages no longer need: every CTA of
-    // the cluster owns an equal run of the activations' rows, in fours, and gets the others' parts of them.
-    // One tile per cluster.
+    // The parts of a tile along K are joined in shared memory, which the stages no longer need:
+    // every CTA of the cluster owns an equal run of the activations' rows, in fours, and gets the
+    // others' parts of them. One tile per cluster.
     const int quarter = warp & 3, n = job.R, own = (n + 4 * job.split - 1) / (4 * job.split);  // fours
     const int lane_v = quarter * 32 + lane, v = group * kFlM + lane_v;
     bool lost = false;
@@ -678,20 +685,21 @@ cudaError_t launch_linear(const void* a, const void* a_scales, const void* w, co
 template <spec_fp4_format F, typename O>
 cudaError_t launch_linear_group(const void* a, const void* a_scales, const void* w, const void* w_scales,
                                 int K, LinearJob job, cudaStream_t s) {
-  // Few weight rows: clusters of up to eight CTAs share a tile's K, two stages each at least, where that many
-  // are resident at once and what it saves, a quarter of a microsecond a stage, is more than the join
-  // costs, one and a thirtieth per activation row.  Measured (us, mx, shared and not): 1 x 4096 x 4096 5.1
-  // and 6.6, 60 x 4096 x 8192 7.9 and 10.7, 1 x 4096 x 14336 7.5 and 15.4, 192 x 4096 x 14336 14.6 and
-  // 18.3; but 128 x 4096 x 4096 9.2 and 8.6, 64 x 8192 x 4096 8.2 and 7.2.
+  // Few weight rows: clusters of up to eight CTAs share a tile's K, two stages each at least, where
+  // that many are resident at once and what it saves, a quarter of a microsecond a stage, is more
+  // than the join costs, one and a thirtieth per activation row.  Measured (us, mx, shared and
+  // not): 1 x 4096 x 4096 5.1 and 6.6, 60 x 4096 x 8192 7.9 and 10.7, 1 x 4096 x 14336 7.5 and
+  // 15.4, 192 x 4096 x 14336 14.6 and 18.3; but 128 x 4096 x 4096 9.2 and 8.6, 64 x 8192 x 4096 8.2
+  // and 7.2.
   const int tiles = (job.V + kFlM - 1) / kFlM, steps = (int)((fp4_row_bytes(K) * 2 + kFlK - 1) / kFlK);
   job.split = 1;
   while (job.split < kFlMaxSplit && tiles * job.split * 2 <= kFlSplitCtas && steps >= job.split * 4)
     job.split *= 2;
   if (job.n_tiles == 1 && 7 * (int64_t)steps * (job.split - 1) >= (int64_t)job.split * (30 + job.R))
     return launch_linear<1, F, O, true>(a, a_scales, w, w_scales, K, job, s);
-  // Pairs of CTAs halve the reads of the activations; below, the weight's bytes bound both and single CTAs start
-  // sooner.  Measured on 128256 x 4096 (us, mx, pairs and not): 60 rows 51.3 and 48.0, 128 rows 52.1 and
-  // 51.4, 192 rows 54.8 and 57.9, 3840 rows 576 and 710.
+  // Pairs of CTAs halve the reads of the activations; below, the weight's bytes bound both and
+  // single CTAs start sooner.  Measured on 128256 x 4096 (us, mx, pairs and not): 60 rows 51.3 and
+  // 48.0, 128 rows 52.1 and 51.4, 192 rows 54.8 and 57.9, 3840 rows 576 and 710.
   if (job.R > 128) return launch_linear<2, F, O>(a, a_scales, w, w_scales, K, job, s);
   return launch_linear<1, F, O>(a, a_scales, w, w_scales, K, job, s);
 }

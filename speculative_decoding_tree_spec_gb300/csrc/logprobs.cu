@@ -1,24 +1,25 @@
 // logprobs.cu -- what a server reports of a row of logits: the log probabilities of given tokens,
 // the entropy of the distribution and its most likely tokens.
 //   x = (z - max) / T,  S = sum e^x,  log p_t = x_t - ln S,  H = ln S - (sum x e^x) / S
-// One pass over the row: each lane keeps its running maximum m and, referred to it, the sums of
-// w = 2^a and of a w, a = (z - m) log2(e) / T.  When m grows by d (in units of a) both are carried
+// One pass over the row: each lane keeps its running maximum m and, referred to it, the sums of w =
+// 2^a and of a w, a = (z - m) log2(e) / T.  When m grows by d (in units of a) both are carried
 // over: w' = w 2^-d, a' = a - d.  Subtracting before multiplying keeps the weight of the maximum
-// exactly 1; the sums of a load (16 or 32 weights of a lane) are fp32 and join compensated sums, so that
-// ln S is accurate to the weights' own rounding, and where one token holds nearly everything it
-// lacks at most what that token's lane adds beside it.
+// exactly 1; the sums of a load (16 or 32 weights of a lane) are fp32 and join compensated sums, so
+// that ln S is accurate to the weights' own rounding, and where one token holds nearly everything
+// it lacks at most what that token's lane adds beside it.
 //
-// The most likely tokens without a list in the loop: of each contiguous 512 bytes of the row (a piece) only
-// the largest logit is kept, one warp reduction a piece.  Among contiguous pieces, ordered by
-// (largest logit, then lower place), the k tokens wanted lie in the first k: a token in a later one has
-// k better tokens before it.  The same holds for groups of pieces, so the first k groups are
-// found by counting, then the first k pieces in them, and only those are read again; their elements at
-// or above the k-th piece's maximum are ranked by counting.  Ties by the hundred go through a sorted
-// list per warp instead.
+// The most likely tokens without a list in the loop: of each contiguous 512 bytes of the row (a
+// piece) only the largest logit is kept, one warp reduction a piece.  Among contiguous pieces,
+// ordered by (largest logit, then lower place), the k tokens wanted lie in the first k: a token in
+// a later one has k better tokens before it.  The same holds for groups of pieces, so the first k
+// groups are found by counting, then the first k pieces in them, and only those are read again;
+// their elements at or above the k-th piece's maximum are ranked by counting.  Ties by the hundred
+// go through a sorted list per warp instead.
 //
 // A CTA of 1 to 8 warps per row, or a cluster of up to 8 CTAs where rows are few (launch_logprobs
-// chooses); they leave their pieces' maxima and sums in the first CTA's shared memory, which finishes the
-// row.  Loads go through a ring in shared memory, four of 2 KB in flight per warp.  Rows of up to 1024 logits take one warp each, the row in registers.
+// chooses); they leave their pieces' maxima and sums in the first CTA's shared memory, which
+// finishes the row.  Loads go through a ring in shared memory, four of 2 KB in flight per warp.
+// Rows of up to 1024 logits take one warp each, the row in registers.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -686,10 +687,10 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   const int per_piece = 32 * Elt<T>::kPerUnit;
   job.n_pieces = (job.V + per_piece - 1) / per_piece;
   job.n_loads = (job.n_pieces + kLpUnits - 1) / kLpUnits;
-  // Warps per row: a wave of rows takes as long as a warp's loads and what finishing a row costs, about 8
-  // loads' time, in a cluster 12.  Measured (us, bf16 rows of 128256, k = 5): 8 rows 8.3 with 64
-  // warps, 9.6 with 32, 15.3 with 8; 152 rows 14.5 with 16, 16.1 with 8, 19.8 with 32; 640 rows 43 with
-  // 4 and with 8, 52 with 2; 3840 rows 180 with 2, 182 with 4, 188 with 8.
+  // Warps per row: a wave of rows takes as long as a warp's loads and what finishing a row costs,
+  // about 8 loads' time, in a cluster 12.  Measured (us, bf16 rows of 128256, k = 5): 8 rows 8.3
+  // with 64 warps, 9.6 with 32, 15.3 with 8; 152 rows 14.5 with 16, 16.1 with 8, 19.8 with 32; 640
+  // rows 43 with 4 and with 8, 52 with 2; 3840 rows 180 with 2, 182 with 4, 188 with 8.
   int W = 1, C = 1;
   int64_t least = INT64_MAX, waves_of = 1;
   for (int w = 1; w <= kLpWarps * kLpMaxCluster; w *= 2) {
@@ -711,10 +712,10 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
     }
   }
   job.cluster = C;
-  // Groups: counting takes the square of their number, ranking the pieces in them little, so the largest
-  // that leave 48 of them (k is at most 32).  1664 fp32 rows of 152064, k = 20: 156 us with 149 groups,
-  // 174 with 297.  Where the rows are one wave, time is latency: a load is a group then, and the chosen
-  // ones are read whole.  One bf16 row of 128256: 8.1 instead of 9.5 us.
+  // Groups: counting takes the square of their number, ranking the pieces in them little, so the
+  // largest that leave 48 of them (k is at most 32).  1664 fp32 rows of 152064, k = 20: 156 us with
+  // 149 groups, 174 with 297.  Where the rows are one wave, time is latency: a load is a group
+  // then, and the chosen ones are read whole.  One bf16 row of 128256: 8.1 instead of 9.5 us.
   job.refine = waves_of > 1 || job.n_loads > kLpGroups;
   job.group = kLpUnits;
   if (job.refine) {
@@ -726,10 +727,10 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(job.R * C));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)W * kLpRing + (job.k > 0 ? (size_t)job.n_loads * 16 : 0);
-  // Given row numbers, some of them name no row (behind the ends of accepted paths): two CTAs of eight warps
-  // per SM then, so that those to come take the places of those without a row, instead of three, all at
-  // once, which leaves three rows on some SMs and none on others.  448 bf16 rows of 128256: 21 us instead
-  // of 27 where 253 of them are rows, 34 instead of 28 where all are.
+  // Given row numbers, some of them name no row (behind the ends of accepted paths): two CTAs of
+  // eight warps per SM then, so that those to come take the places of those without a row, instead
+  // of three, all at once, which leaves three rows on some SMs and none on others.  448 bf16 rows
+  // of 128256: 21 us instead of 27 where 253 of them are rows, 34 instead of 28 where all are.
   if (job.rows && C == 1 && W == kLpWarps && job.R > 2 * device_sm_count() && cfg.dynamicSmemBytes < kLpTwoPerSm)
     cfg.dynamicSmemBytes = kLpTwoPerSm;
   cfg.stream = s;

@@ -7,13 +7,13 @@
 // significant bits: ts is a power of two, and max|x| / 6 is rounded to odd before it is rounded to
 // e4m3.  x / S is the product with 1 / S, corrected by its exact remainder (the quotient's
 // correction of Markstein, IBM Journal of Research and Development 34, 1990), which is the fp32
-// number nearest to the quotient; and no quotient of a 24-bit number by a 4-bit one lies so near
-// to a midpoint between two codes that rounding it to fp32 first would take it there: the midpoints times S
-// are fp32 numbers themselves.
+// number nearest to the quotient; and no quotient of a 24-bit number by a 4-bit one lies so near to
+// a midpoint between two codes that rounding it to fp32 first would take it there: the midpoints
+// times S are fp32 numbers themselves.
 //
-// Memory-bound: 8 elements per thread, 16-byte loads and 4-byte stores side by side, rows in
-// groups of four loads in flight.  Blocks share their maximum over 4 (nv: 2) lanes; the scales of four blocks
-// in four rows are transposed over lanes and go out as four words.
+// Memory-bound: 8 elements per thread, 16-byte loads and 4-byte stores side by side, rows in groups
+// of four loads in flight.  Blocks share their maximum over 4 (nv: 2) lanes; the scales of four
+// blocks in four rows are transposed over lanes and go out as four words.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 && F == SPEC_FP4_MX 
       out += kStep * job.row_bytes;
     }
   }
-  // the four scales of a tile's row as one word: of the lanes of four blocks the first four each take
-  // one of the rows
+  // the four scales of a tile's row as one word: of the lanes of four blocks the first four each
+  // take one of the rows
   constexpr int kSpan = 4 * kLanes;
   const int mine = lane & (kSpan - 1), from = lane & ~(kSpan - 1), g = c / (kLanes * 32);
   uint32_t w[4];
