@@ -45,6 +45,7 @@ constexpr int kLpMaxShared = (int)(kLpWarps * kLpRing) + SPEC_MAX_VOCAB / 32;
 constexpr size_t kLpTwoPerSm = 96 * 1024;  // shared memory that leaves room for two CTAs
 constexpr int kLpCand = 256;     // candidates ranked by counting
 constexpr int kLpGroups = 128;   // groups ranked by counting
+constexpr int kLpSmallCand = 96; // candidates of a row of up to 1024 logits that are sorted
 
 struct LogprobJob {
   const void* base;
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
   const uint32_t top0 = C > 1 ? cluster_addr(s_top, 0) : 0u;
   const uint32_t group0 = C > 1 ? cluster_addr(s_group, 0) : 0u;
   if (threadIdx.x == 0) {
-    s_bad = 0u;
+    s_bad = s_tau = 0u;
     s_count = s_found = 0;
   }
   if (C > 1) cluster_arrive();  // the first CTA is there, its words cleared
@@ -435,8 +436,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
       for (int j = i & ~3; j < i; ++j) before += s_group[j] == mine;  // of the four around it
       if (before < kg) {
         s_sel[before] = i;
-        if (before == kg - 1) s_tau = kg == k ? mine : 0u;  // fewer groups than k: every piece counts
+        if (before == k - 1) atomicMax(&s_tau, mine);
       }
+    }
+    if (n_groups < 2 * k) {
+      // the k-th of few groups is a loose bound or none: the k-th largest of the lanes' own maxima
+      // bounds the k-th logit as well (the first warp's 32 lanes have logits in any row that comes here)
+      uint32_t* const s_lane = reinterpret_cast<uint32_t*>(s_list);
+      const uint32_t mine = order_key(m);
+      s_lane[threadIdx.x] = mine;
+      __syncthreads();
+      int before = 0;
+      for (int j = 0; j < (int)blockDim.x; ++j)
+        before += s_lane[j] > mine || (s_lane[j] == mine && j < (int)threadIdx.x);
+      if (before == k - 1) atomicMax(&s_tau, mine);
     }
   }
   // the row's sums
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
         for (int j = 0; j < count; ++j) before += s_list[j] > mine;
         if (before < kp) {
           s_piece[before] = (int)(0xFFFFFFFFu - (uint32_t)mine);
-          if (before == kp - 1) s_tau2 = kp == k ? (uint32_t)(mine >> 32) : 0u;
+          if (before == kp - 1) s_tau2 = kp == k ? (uint32_t)(mine >> 32) : tau;
         }
       }
       __syncthreads();
@@ -591,7 +604,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
 
 // Rows of up to 32 kE logits: a warp each, element j 32 + lane in its lane's j-th register.
 template <typename T, int kE>
-__global__ void __launch_bounds__(kLpThreads) logprob_small_kernel(LogprobJob job) {
+__global__ void __launch_bounds__(kLpThreads, kE > 16 ? 3 : 4) logprob_small_kernel(LogprobJob job) {
+  __shared__ uint64_t s_in[kLpWarps][kE == 1 ? 1 : kLpSmallCand];
   const int lane = threadIdx.x & 31;
   const int64_t r64 = (int64_t)blockIdx.x * kLpWarps + (threadIdx.x >> 5);
   if (r64 >= job.R) return;
@@ -642,28 +656,70 @@ __global__ void __launch_bounds__(kLpThreads) logprob_small_kernel(LogprobJob jo
     if (job.out_entropy) job.out_entropy[r] = part_entropy(p, log_s);
     if (job.out_status) job.out_status[r] = SPEC_TREE_OK;
   }
-  // the k largest one after another: the lane's best key, then the warp's
-  uint32_t key[kE];
+  if (k > (kE == 1 ? 8 : 3)) {
+    // The k-th largest of the lanes' maxima bounds the k-th logit (a lane without a logit has key 0):
+    // what is at or above it goes to a buffer and is sorted, 32 keys at a time.  A few are found
+    // sooner one after another: 40000 bf16 rows of 1000 take 61 us with one, 101 with five sorted, 264
+    // with twenty one after another and 118 with twenty sorted.
+    uint64_t L = 0ull;
+    int n_in = 0;
+    if constexpr (kE == 1) {
+      L = warp_sort_desc(lane < V ? key_of(z[0], lane) : 0ull, lane);
+    } else {
+      uint32_t top[2] = {0u, 0u};  // of two halves of the lane's logits: for a large k one is too loose
 #pragma unroll
-  for (int j = 0; j < kE; ++j) key[j] = j * 32 + lane < V ? order_key(z[j]) : 0u;
+      for (int j = 0; j < kE; ++j)
+        if (j * 32 + lane < V) top[j & 1] = max(top[j & 1], order_key(z[j]));
+      uint64_t sorted = (uint64_t)(k > 16 ? top[0] : max(top[0], top[1])) << 32;
+      sorted = warp_sort_desc(sorted, lane);
+      if (k > 16) sorted = list_merge(sorted, warp_sort_desc((uint64_t)top[1] << 32, lane), lane);
+      const uint32_t tau = (uint32_t)(__shfl_sync(kFull, sorted, k - 1) >> 32);
+      uint64_t* const in = s_in[threadIdx.x >> 5];
+#pragma unroll
+      for (int j = 0; j < kE; ++j) {
+        const int i = j * 32 + lane;
+        const bool take = i < V && order_key(z[j]) >= tau;
+        const uint32_t who = __ballot_sync(kFull, take);
+        const int at = n_in + __popc(who & ((1u << lane) - 1u));
+        if (take && at < kLpSmallCand) in[at] = key_of(z[j], i);
+        n_in += __popc(who);
+      }
+      __syncwarp();
+      for (int c = 0; c < min(n_in, kLpSmallCand); c += 32) {
+        const uint64_t x = warp_sort_desc(c + lane < n_in ? in[c + lane] : 0ull, lane);
+        L = c == 0 ? x : list_merge(L, x, lane);
+      }
+    }
+    if (n_in <= kLpSmallCand) {
+      if (lane < k) {
+        const float v = key_value((uint32_t)(L >> 32));
+        job.out_top[(int64_t)r * k + lane] = (int32_t)(0xFFFFFFFFu - (uint32_t)L);
+        job.out_top_lp[(int64_t)r * k + lane] = (v - M) * job.inv_t - log_s;
+      }
+      return;
+    }
+  }
+  // the k largest one after another: the lane's best key, then the warp's
+  uint32_t left = 0u;  // this lane's logits that are not listed yet
+#pragma unroll
+  for (int j = 0; j < kE; ++j)
+    if (j * 32 + lane < V) left |= 1u << j;
   int mine = -1;
   float mine_lp = 0.f;
   for (int t = 0; t < k; ++t) {
-    uint32_t best = key[0];
-    int at = lane;
+    uint32_t best = 0u;
+    int at = INT_MAX;
 #pragma unroll
-    for (int j = 1; j < kE; ++j)
-      if (key[j] > best) {
-        best = key[j];
+    for (int j = 0; j < kE; ++j) {
+      const uint32_t key = (left >> j) & 1u ? order_key(z[j]) : 0u;
+      if (key > best) {
+        best = key;
         at = j * 32 + lane;
       }
+    }
     const uint32_t top = __reduce_max_sync(kFull, best);
     const int i = __reduce_min_sync(kFull, best == top ? at : INT_MAX);
-    if (at == i) {
-#pragma unroll
-      for (int j = 0; j < kE; ++j)
-        if (j * 32 + lane == i) key[j] = 0u;
-    }
+    if (at == i) left &= ~(1u << (i >> 5));
     if (lane == t) {
       mine = i;
       mine_lp = (key_value(top) - M) * job.inv_t - log_s;
@@ -681,6 +737,7 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
     const unsigned blocks = ((unsigned)job.R + kLpWarps - 1) / kLpWarps;
     if (job.V <= 32) logprob_small_kernel<T, 1><<<blocks, kLpThreads, 0, s>>>(job);
     else if (job.V <= 256) logprob_small_kernel<T, 8><<<blocks, kLpThreads, 0, s>>>(job);
+    else if (job.V <= 512) logprob_small_kernel<T, 16><<<blocks, kLpThreads, 0, s>>>(job);
     else logprob_small_kernel<T, 32><<<blocks, kLpThreads, 0, s>>>(job);
     return cudaGetLastError();
   }
@@ -711,6 +768,7 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
       C = w / cta;
     }
   }
+  if (W == 1 && job.k > 16 && job.n_pieces < 2 * job.k && job.n_loads > 1) W = 2;  // more lanes' maxima
   job.cluster = C;
   // Groups: counting takes the square of their number, ranking the pieces in them little, so the
   // largest that leave 48 of them (k is at most 32).  1664 fp32 rows of 152064, k = 20: 156 us with

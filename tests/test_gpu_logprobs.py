@@ -82,6 +82,19 @@ def test_numbers_of_rows(R):
     _check(_gauss(R, 20000, R), BF, g.integers(0, 20000, R), 10)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,V", [(4000, 33), (4000, 300), (3000, 1000), (5000, 1100), (5000, 2000), (2000, 5000)])
+def test_many_short_rows(R, V, dtype):
+    """Rows by the thousand, a warp or two each: the alternatives against a stable sort."""
+    d = _rows(_gauss(R, V, R + V), dtype)
+    order = torch.sort(d.float(), dim=1, descending=True, stable=True)[1]
+    for k in (1, 3, 4, 17, 32):
+        got = binding.token_logprobs(d, order[:, :2].to(torch.int32).contiguous(), k)
+        assert torch.equal(got["top_tokens"], order[:, :k].to(torch.int32)) and not got["status"].any()
+        n = min(k, 2)
+        assert torch.equal(got["top_logprobs"][:, :n], got["logprobs"][:, :n])
+
+
 @pytest.mark.parametrize("T", [1e-3, 0.25, 0.7, 2.0, 100.0])
 @pytest.mark.parametrize("V", [500, 20000])
 def test_temperatures(T, V):
