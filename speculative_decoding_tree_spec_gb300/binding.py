@@ -814,11 +814,13 @@ def _fp4_check(m: Fp4Matrix, dev: int, what: str):
 
 
 def _padded(rows: int, cols: int, dtype, device):
-    """An empty [rows, cols] whose rows start on 16-byte boundaries."""
+    """An empty [rows, cols] whose rows start on 16-byte boundaries.  (The last row's padding is not part
+    of it: the allocator's blocks end on such boundaries, too.)"""
     per = 16 // dtype.itemsize
     pitch = (cols + per - 1) // per * per
-    t = torch.empty((rows, pitch), dtype=dtype, device=device)
-    return t if pitch == cols else t[:, :cols]
+    if pitch == cols:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    return torch.empty_strided((rows, cols), (pitch, 1), dtype=dtype, device=device)
 
 
 def _matrix_out(out, rows: int, cols: int, dtype, dev: int):

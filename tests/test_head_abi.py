@@ -72,6 +72,11 @@ class Torch(FakeTorch):
         self.cuda.made[-1] = Tensor(t.shape, t.dtype, t.dev, t.made_on)
         return self.cuda.made[-1]
 
+    def empty_strided(self, shape, strides, dtype=None, device=None):
+        t = self.empty(shape, dtype, device)
+        t._strides = strides
+        return t
+
 
 class Lib(FakeLib):
     def __getattr__(self, name):
@@ -186,6 +191,11 @@ def test_the_binding_refuses(fake, name):
 
 
 def test_padded_results(fake):
-    assert binding._padded(3, 9, BF, torch.device("cuda", 0)) is fake.made[-1] and fake.made[-1].shape == (3, 16)
-    binding._padded(3, 9, F32, torch.device("cuda", 0))
-    assert fake.made[-1].shape == (3, 12)
+    cuda = torch.device("cuda", 0)
+    assert binding._padded(3, 9, BF, cuda) is fake.made[-1]
+    assert fake.made[-1].shape == (3, 9) and fake.made[-1].stride() == (16, 1)
+    assert binding._padded(3, 9, F32, cuda).stride() == (12, 1)
+    assert binding._padded(3, 8, F32, cuda).stride() == (8, 1)
+    # a result with padded rows goes to the kernel with its pitch, one row with any
+    assert binding._pitch(binding._padded(3, 9, F32, cuda), 9) == 12
+    assert binding._pitch(T((1, 9), F32, strides=(77, 1)), 9) == 12
