@@ -789,7 +789,8 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   // eight warps per SM then, so that those to come take the places of those without a row, instead
   // of three, all at once, which leaves three rows on some SMs and none on others.  448 bf16 rows
   // of 128256: 21 us instead of 27 where 253 of them are rows, 34 instead of 28 where all are.
-  if (job.rows && C == 1 && W == kLpWarps && job.R > 2 * device_sm_count() && cfg.dynamicSmemBytes < kLpTwoPerSm)
+  if (job.rows && waves_of == 1 && C == 1 && W == kLpWarps && job.R > 2 * device_sm_count() &&
+      cfg.dynamicSmemBytes < kLpTwoPerSm)
     cfg.dynamicSmemBytes = kLpTwoPerSm;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
