@@ -45,6 +45,7 @@ constexpr int kLpMaxShared = (int)(kLpWarps * kLpRing) + SPEC_MAX_VOCAB / 32;
 constexpr size_t kLpTwoPerSm = 96 * 1024;  // shared memory that leaves room for two CTAs
 constexpr int kLpCand = 256;     // candidates ranked by counting
 constexpr int kLpGroups = 128;   // groups ranked by counting
+constexpr int kLpManyK = 24;     // alternatives from which on 32 maxima are a loose bound
 constexpr int kLpSmallCand = 96; // candidates of a row of up to 1024 logits that are sorted
 
 struct LogprobJob {
@@ -439,9 +440,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
         if (before == k - 1) atomicMax(&s_tau, mine);
       }
     }
-    if (n_groups < 2 * k) {
-      // the k-th of few groups is a loose bound or none: the k-th largest of the lanes' own maxima
-      // bounds the k-th logit as well (the first warp's 32 lanes have logits in any row that comes here)
+    if (n_groups < k || (k > kLpManyK && n_groups < 2 * k)) {
+      // the k-th of few groups is no bound or, for a large k, a loose one: the k-th largest of the
+      // lanes' own maxima bounds the k-th logit as well (the first warp's 32 lanes have logits in any
+      // row that comes here)
       uint32_t* const s_lane = reinterpret_cast<uint32_t*>(s_list);
       const uint32_t mine = order_key(m);
       s_lane[threadIdx.x] = mine;
@@ -768,7 +770,8 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
       C = w / cta;
     }
   }
-  if (W == 1 && job.k > 16 && job.n_pieces < 2 * job.k && job.n_loads > 1) W = 2;  // more lanes' maxima
+  // the lanes' maxima bound a large k better when there are more of them
+  if (W == 1 && job.k > kLpManyK && job.n_pieces < 2 * job.k && job.n_loads > 1) W = 2;
   job.cluster = C;
   // Groups: counting takes the square of their number, ranking the pieces in them little, so the
   // largest that leave 48 of them (k is at most 32).  1664 fp32 rows of 152064, k = 20: 156 us with
