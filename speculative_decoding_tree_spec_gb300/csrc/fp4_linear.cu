@@ -24,7 +24,8 @@
 // products take 390), low words of descriptors computed once a stage (nv 99 -> 86 us at 3840 x
 // 16384 x 4096), the transposed epilogue (two-byte stores by lane: 1152 us instead of 983 then).
 // No gain: scales copied a stage ahead of the products (124 us instead of 99), peeking at the next
-// stage's barrier, longer suspensions in waits.
+// stage's barrier, longer suspensions in waits; in the epilogue the next columns' loads ahead of the
+// stores, four staging buffers a warp, rows of 128 bytes by two warps (85.2 us instead of 85.4).
 #include <cuda.h>
 
 #include <cuda_bf16.h>
