@@ -246,6 +246,10 @@ __device__ __forceinline__ void bulk_store(const CUtensorMap* tm, uint32_t src, 
                : "memory");
   asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
 }
+// A piece that leaves without a bulk store commits an empty group in its place.
+__device__ __forceinline__ void bulk_none() {
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void bulk_store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(N) : "memory");
@@ -479,7 +483,9 @@ __global__ void __launch_bounds__(kFlThreads, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < rows; c0 += 32, ++chunk) {
         const uint32_t buf = staging + (chunk & 1u) * kStageOut;
-        if (lane == 0) bulk_store_wait_read<1>();  // the stores from this buffer have read it
+        // every piece commits one group: with the newest alone pending, the last store from this
+        // buffer has read it
+        if (lane == 0) bulk_store_wait_read<1>();
         __syncwarp();
         uint32_t x[32];
         load_out<O>(taddr + (uint32_t)c0, x);
@@ -496,6 +502,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
           __syncwarp();
           if (lane == 0) bulk_store(&tm_out, buf, v0, n0 + c0);
         } else {  // a bulk store clips to 16 bytes, the matrix may end within them
+          if (lane == 0) bulk_none();
           __syncwarp();
           if (v0 + lane < job.V)
             for (int i = 0; i < min(32, rows - c0); ++i)
