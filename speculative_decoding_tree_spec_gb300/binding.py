@@ -768,6 +768,7 @@ def draft_topk_fused_lmhead(features: torch.Tensor, weight: torch.Tensor, k: int
 
 
 _FP4_FORMATS = {"mx": SPEC_FP4_MX, "nv": SPEC_FP4_NV}
+_F32_NORMAL = 2.0 ** -126  # smaller float32 numbers have fewer bits
 
 
 class Fp4Matrix(typing.NamedTuple):
@@ -902,8 +903,9 @@ def fp4_dequantize(m: Fp4Matrix, dtype=torch.bfloat16, *, out=None, stream=None)
 def fp4_linear(a: Fp4Matrix, w: Fp4Matrix, dtype=torch.bfloat16, *, alpha: float = 1.0, out=None,
                stream=None) -> torch.Tensor:
     """spec_fp4_linear: alpha * a w^T [a.rows, w.rows] of two matrices of one format with the same
-    number of columns, as bfloat16 or float32 (a view with padded rows where w.rows is odd).  The
-    tensor scales are taken in."""
+    number of columns, as bfloat16 or float32 (a view with padded rows where they would not start on
+    16-byte boundaries).  The tensor scales are taken in: their product with alpha is the kernel's
+    factor, a float32, and refused where it is too small for one."""
     dev = a.codes.get_device()
     if dev < 0:
         raise ValueError("the matrices must be on a CUDA device")
@@ -916,13 +918,16 @@ def fp4_linear(a: Fp4Matrix, w: Fp4Matrix, dtype=torch.bfloat16, *, alpha: float
     if a.format != w.format or a.cols != w.cols:
         raise ValueError("a and w must share the format and the number of columns")
     code = _float_dtype(dtype)
+    factor = alpha * a.tensor_scale * w.tensor_scale
+    if abs(factor) < _F32_NORMAL and alpha != 0 and (factor == 0 or ctypes.c_float(factor).value != factor):
+        raise ValueError(f"alpha times the tensor scales, {factor}, is too small for a float32")
     if out is None:
         out = _padded(a.rows, w.rows, dtype, a.codes.device)
     else:
         _matrix_out(out, a.rows, w.rows, dtype, dev)
-    rc = (_lib or lib()).spec_fp4_linear(ac, asc, wc, wsc, fmt, a.rows, w.rows, a.cols,
-                                         alpha * a.tensor_scale * w.tensor_scale, out.data_ptr(), code,
-                                         _pitch(out, w.rows), torch._C._cuda_getCurrentRawStream(dev))
+    rc = (_lib or lib()).spec_fp4_linear(ac, asc, wc, wsc, fmt, a.rows, w.rows, a.cols, factor,
+                                         out.data_ptr(), code, _pitch(out, w.rows),
+                                         torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise SpecError(rc, "spec_fp4_linear")
     return out

@@ -49,8 +49,10 @@ extern "C" int spec_draft_topk_fused_fp4(const void* features, float feature_sca
   if (!fp4_tensor_scale_ok(feature_scale) || !fp4_tensor_scale_ok(weight_scale) ||
       (format == SPEC_FP4_MX && (feature_scale != 1.0f || weight_scale != 1.0f)))
     return SPEC_ERR_INVALID_ARG;
+  // the scales' product, a power of two, has to be a float: beyond the largest all logits would be
+  // infinite, below the smallest all 0
   const double alpha = (double)feature_scale * (double)weight_scale;
-  if (!(alpha <= 3.402823466e38)) return SPEC_ERR_INVALID_ARG;
+  if ((double)(float)alpha != alpha) return SPEC_ERR_INVALID_ARG;
   if (R == 0) return SPEC_OK;
   if (!features || !w_codes || !w_scales || !out_tokens || !out_probs || !workspace)
     return SPEC_ERR_INVALID_ARG;

@@ -1,0 +1,29 @@
+"""Values at the ends of the head calls' ranges that the host has to refuse.  Run as a script in a child
+process that sees no GPU: a call that is not refused ends with the launch's error (-5), or with 0 where
+it has no rows.  Prints the return codes as JSON."""
+import json
+import sys
+
+import head_validation_cases as hv
+from speculative_decoding_tree_spec_gb300 import binding
+
+# feature scale, weight scale: their product is the logits' factor, a float32
+SCALES = [
+    (dict(feature_scale=2.0 ** -100, weight_scale=2.0 ** -50), -1),
+    (dict(feature_scale=2.0 ** -75, weight_scale=2.0 ** -75), -1),
+    (dict(feature_scale=2.0 ** -100, weight_scale=2.0 ** -100), -1),
+    (dict(feature_scale=2.0 ** 100, weight_scale=2.0 ** 28), -1),
+    (dict(feature_scale=2.0 ** -100, weight_scale=2.0 ** -49, R=0), 0),
+    (dict(feature_scale=2.0 ** -63, weight_scale=2.0 ** -63, R=0), 0),
+    (dict(feature_scale=2.0 ** 100, weight_scale=2.0 ** 27, R=0), 0),
+    (dict(feature_scale=2.0 ** 100, weight_scale=2.0 ** -100, R=0), 0),
+]
+
+
+def main():
+    L = binding.lib()
+    print(json.dumps({"scales": [hv.fused(L, format=1, **kw) for kw, _ in SCALES]}))
+
+
+if __name__ == "__main__":
+    sys.exit(main())
