@@ -42,7 +42,6 @@ constexpr int kLpMaxCluster = 8;
 constexpr int kLpSmallV = 1024;
 // the ring of eight warps and the maxima of the widest fp32 row
 constexpr int kLpMaxShared = (int)(kLpWarps * kLpRing) + SPEC_MAX_VOCAB / 32;
-constexpr size_t kLpTwoPerSm = 96 * 1024;  // shared memory that leaves room for two CTAs
 constexpr int kLpCand = 256;     // candidates ranked by counting
 constexpr int kLpGroups = 128;   // groups ranked by counting
 constexpr int kLpManyK = 24;     // alternatives from which on 32 maxima are a loose bound
@@ -788,13 +787,6 @@ cudaError_t launch_logprobs(LogprobJob job, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(job.R * C));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)W * kLpRing + (job.k > 0 ? (size_t)job.n_loads * 16 : 0);
-  // Given row numbers, some of them name no row (behind the ends of accepted paths): two CTAs of
-  // eight warps per SM then, so that those to come take the places of those without a row, instead
-  // of three, all at once, which leaves three rows on some SMs and none on others.  448 bf16 rows
-  // of 128256: 21 us instead of 27 where 253 of them are rows, 34 instead of 28 where all are.
-  if (job.rows && waves_of == 1 && C == 1 && W == kLpWarps && job.R > 2 * device_sm_count() &&
-      cfg.dynamicSmemBytes < kLpTwoPerSm)
-    cfg.dynamicSmemBytes = kLpTwoPerSm;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
