@@ -639,13 +639,14 @@ int spec_draft_topk_fused_fp4(const void* features, float feature_scale, const v
  * logits [n_rows, row_pitch] of dtype, base and row_pitch * sizeof(elem) 16-byte aligned.  rows [R]
  *   (device): the row that result r is read from, in any order, the same one any number of times;
  *   NULL: row r (R <= n_rows).  With the row numbers of an accepted path only those rows are
- *   read.  tokens is int32, G >= 0 (0: NULL).
+ *   read.  tokens is int32, 0 <= G <= SPEC_LOGPROB_MAX_GIVEN (0: NULL).
  * temperature finite and at least SPEC_LOGPROB_MIN_TEMPERATURE.  Asynchronous on `stream`;
  * allocates nothing.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED_DTYPE, SPEC_ERR_MISALIGNED,
- * SPEC_ERR_TOO_LARGE (V > SPEC_MAX_VOCAB), SPEC_ERR_CUDA.
+ * SPEC_ERR_TOO_LARGE (V > SPEC_MAX_VOCAB, G), SPEC_ERR_CUDA.
  */
 #define SPEC_LOGPROB_MIN_TEMPERATURE 1e-37f
+#define SPEC_LOGPROB_MAX_GIVEN (1 << 30)
 int spec_token_logprobs(const void* logits, spec_dtype dtype, int32_t n_rows, int32_t V,
                         int64_t row_pitch, const int32_t* rows, int32_t R, const int32_t* tokens,
                         int32_t G, int32_t k, float temperature, float* out_logprobs,

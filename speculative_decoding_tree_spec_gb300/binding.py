@@ -48,6 +48,7 @@ SPEC_FP4_MX = 0
 SPEC_FP4_NV = 1
 SPEC_FP4_MAX_DIM = 1 << 24
 SPEC_LOGPROB_MIN_TEMPERATURE = 1e-37
+SPEC_LOGPROB_MAX_GIVEN = 1 << 30
 ERRORS = {0: "SPEC_OK", -1: "SPEC_ERR_INVALID_ARG", -2: "SPEC_ERR_UNSUPPORTED_DTYPE",
           -3: "SPEC_ERR_MISALIGNED", -4: "SPEC_ERR_WORKSPACE", -5: "SPEC_ERR_CUDA",
           -6: "SPEC_ERR_TOO_LARGE"}

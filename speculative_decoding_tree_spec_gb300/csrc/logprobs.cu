@@ -823,7 +823,8 @@ extern "C" int spec_token_logprobs(const void* logits, spec_dtype dtype, int32_t
   if (n_rows < 0 || R < 0 || V < 1 || G < 0 || k < 0 || k > kLpMaxK || k > V)
     return SPEC_ERR_INVALID_ARG;
   if (!rows && R > n_rows) return SPEC_ERR_INVALID_ARG;
-  if (V > SPEC_MAX_VOCAB) return SPEC_ERR_TOO_LARGE;
+  // (the kernels' counters of given tokens go up to a block's threads past the last)
+  if (V > SPEC_MAX_VOCAB || G > SPEC_LOGPROB_MAX_GIVEN) return SPEC_ERR_TOO_LARGE;
   // log2(e) / T has to be a float
   if (!(temperature >= SPEC_LOGPROB_MIN_TEMPERATURE) || !(temperature <= 3.402823466e38f))
     return SPEC_ERR_INVALID_ARG;

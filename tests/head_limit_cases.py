@@ -19,10 +19,19 @@ SCALES = [
     (dict(feature_scale=2.0 ** 100, weight_scale=2.0 ** -100, R=0), 0),
 ]
 
+# given tokens per row: the kernels count them in 32 bits, a block's threads past the last
+GIVEN = [
+    (dict(G=2 ** 31 - 1), -6),
+    (dict(G=2 ** 31 - 200), -6),
+    (dict(G=2 ** 30 + 1), -6),
+    (dict(G=2 ** 30, R=0), 0),
+]
+
 
 def main():
     L = binding.lib()
-    print(json.dumps({"scales": [hv.fused(L, format=1, **kw) for kw, _ in SCALES]}))
+    print(json.dumps({"scales": [hv.fused(L, format=1, **kw) for kw, _ in SCALES],
+                      "given": [hv.logprobs(L, **kw) for kw, _ in GIVEN]}))
 
 
 if __name__ == "__main__":

@@ -32,6 +32,10 @@ def test_scales_whose_product_is_no_float(codes):
     assert codes["scales"] == [want for _, want in hl.SCALES]
 
 
+def test_given_tokens_beyond_the_counters(codes):
+    assert codes["given"] == [want for _, want in hl.GIVEN]
+
+
 @pytest.mark.parametrize("alpha,sa,sw", [(1.0, 2.0 ** -100, 2.0 ** -100), (1.0, 2.0 ** -75, 2.0 ** -75),
                                          (1e-20, 2.0 ** -100, 1.0), (-1e-45, 2.0 ** -4, 1.0),
                                          (3.0, 2.0 ** -100, 2.0 ** -50), (1e-300, 2.0 ** -100, 2.0 ** -100)])
