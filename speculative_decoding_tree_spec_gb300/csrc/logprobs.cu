@@ -51,8 +51,8 @@ struct LogprobJob {
   const void* base;
   int64_t pitch_bytes;
   int n_rows, R, V, G, k;
-  float c;      // log2(e) / T
-  float inv_t;  // 1 / T
+  float c;      // 16 log2(e) / T
+  float inv_t;  // 16 / T
   const int32_t* rows;
   const int32_t* tokens;
   float* out_lp;
@@ -64,6 +64,14 @@ struct LogprobJob {
   int n_pieces, group;   // pieces of a row, and of a group
   int refine;            // the pieces of the chosen groups are ranked, too, before they are read
 };
+
+// (z - m) times a sixteenth of `by` (c or inv_t).  fp32 need not hold the difference of two logits, of
+// their sixteenths it does; unless it is subnormal, it is the same number otherwise.  (And 16 / T is
+// normal for every T.)
+constexpr float kSixteenth = 0.0625f;
+__device__ __forceinline__ float apart(float z, float m, float by) {
+  return fmaf(z, kSixteenth, -kSixteenth * m) * by;
+}
 
 // Sums of 2^a and a 2^a over some elements, referred to their maximum m (in logits).
 struct Part {
@@ -82,7 +90,7 @@ __device__ __forceinline__ void part_raise(Part& p, float M, float c) {
   if (p.m == -CUDART_INF_F) {
     p.s_hi = p.s_lo = p.a = 0.f;
   } else if (p.m != M) {
-    const float d = (p.m - M) * c;
+    const float d = apart(p.m, M, c);
     const float f = ex2_approx(d);
     // a p whose weights vanish must not turn an infinite d into NaN
     p.a = f > 0.f ? f * fmaf(d, p.s_hi, p.a) : 0.f;
@@ -139,7 +147,7 @@ __device__ __forceinline__ int row_of(const LogprobJob& job, int r) {
 template <typename T>
 __device__ __forceinline__ float given_logprob(const LogprobJob& job, const void* row, int tok, float M,
                                                float log_s) {
-  return (unsigned)tok < (unsigned)job.V ? (Elt<T>::at(row, tok) - M) * job.inv_t - log_s : -CUDART_INF_F;
+  return (unsigned)tok < (unsigned)job.V ? apart(Elt<T>::at(row, tok), M, job.inv_t) - log_s : -CUDART_INF_F;
 }
 // Those of the tokens from t on, `step` apart.
 template <typename T>
@@ -243,13 +251,14 @@ __device__ __forceinline__ float unit_max(const uint4& u) {
   }
 }
 
-// Sums of 2^a and a 2^a over the lane's units, a = (z - m) c.  Weights that vanish (z = -inf)
+// Sums of 2^a and a 2^a over the lane's units, a = apart(z, m, c).  Weights that vanish (z = -inf)
 // would make the second sum NaN: kMasked bounds a from below, which leaves those weights 0.
 template <typename T, bool kMasked>
 __device__ __forceinline__ void units_sums(const uint4 (&raw)[kLpUnits], float m, float c, float& s,
                                            float& aw) {
   constexpr int E = Elt<T>::kPerUnit;
-  const float2 nm = make_float2(-m, -m), c2 = make_float2(c, c);
+  const float nm16 = -kSixteenth * m;
+  const float2 nm = make_float2(nm16, nm16), c2 = make_float2(c, c), part = make_float2(kSixteenth, kSixteenth);
   float2 s0 = make_float2(0.f, 0.f), s1 = s0, a0 = s0, a1 = s0;
 #pragma unroll
   for (int j = 0; j < kLpUnits; ++j) {
@@ -257,7 +266,7 @@ __device__ __forceinline__ void units_sums(const uint4 (&raw)[kLpUnits], float m
     Elt<T>::unpack(raw[j], f);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-      float2 a = __fmul2_rn(__fadd2_rn(make_float2(f[e], f[e + 1]), nm), c2);
+      float2 a = __fmul2_rn(__ffma2_rn(make_float2(f[e], f[e + 1]), part, nm), c2);
       if (kMasked) a = make_float2(fmaxf(a.x, -1000.f), fmaxf(a.y, -1000.f));
       const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
       if ((e >> 1) & 1) {
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     }
     if (um > m) {
       if (m != -CUDART_INF_F) {
-        const float d = (m - um) * c;
+        const float d = apart(m, um, c);
         const float f = ex2_approx(d);
         const float s = S.s - S.c;
         A.s = f > 0.f ? f * fmaf(d, s, A.s - A.c) : 0.f;
@@ -555,7 +564,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
         if (before < k) {
           const float z = key_value((uint32_t)(mine >> 32));
           job.out_top[(int64_t)r * k + before] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
-          job.out_top_lp[(int64_t)r * k + before] = (z - M) * job.inv_t - log_s;
+          job.out_top_lp[(int64_t)r * k + before] = apart(z, M, job.inv_t) - log_s;
         }
       }
       return;
@@ -598,7 +607,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprob_rows_kernel(Logp
     if (lane < k) {
       const float z = key_value((uint32_t)(L >> 32));
       job.out_top[(int64_t)r * k + lane] = (int32_t)(0xFFFFFFFFu - (uint32_t)L);
-      job.out_top_lp[(int64_t)r * k + lane] = (z - M) * job.inv_t - log_s;
+      job.out_top_lp[(int64_t)r * k + lane] = apart(z, M, job.inv_t) - log_s;
     }
   }
 }
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kLpThreads, kE > 16 ? 3 : 4) logprob_small_ker
   p.a = 0.f;
 #pragma unroll
   for (int j = 0; j < kE; ++j) {
-    const float a = fmaxf((z[j] - M) * job.c, -1000.f);
+    const float a = fmaxf(apart(z[j], M, job.c), -1000.f);
     const float w = ex2_approx(a);
     s.add(w);
     p.a = fmaf(a, w, p.a);
@@ -695,7 +704,7 @@ __global__ void __launch_bounds__(kLpThreads, kE > 16 ? 3 : 4) logprob_small_ker
       if (lane < k) {
         const float v = key_value((uint32_t)(L >> 32));
         job.out_top[(int64_t)r * k + lane] = (int32_t)(0xFFFFFFFFu - (uint32_t)L);
-        job.out_top_lp[(int64_t)r * k + lane] = (v - M) * job.inv_t - log_s;
+        job.out_top_lp[(int64_t)r * k + lane] = apart(v, M, job.inv_t) - log_s;
       }
       return;
     }
@@ -723,7 +732,7 @@ __global__ void __launch_bounds__(kLpThreads, kE > 16 ? 3 : 4) logprob_small_ker
     if (at == i) left &= ~(1u << (i >> 5));
     if (lane == t) {
       mine = i;
-      mine_lp = (key_value(top) - M) * job.inv_t - log_s;
+      mine_lp = apart(key_value(top), M, job.inv_t) - log_s;
     }
   }
   if (lane < k) {
@@ -825,7 +834,7 @@ extern "C" int spec_token_logprobs(const void* logits, spec_dtype dtype, int32_t
   if (!rows && R > n_rows) return SPEC_ERR_INVALID_ARG;
   // (the kernels' counters of given tokens go up to a block's threads past the last)
   if (V > SPEC_MAX_VOCAB || G > SPEC_LOGPROB_MAX_GIVEN) return SPEC_ERR_TOO_LARGE;
-  // log2(e) / T has to be a float
+  // 16 log2(e) / T has to be a float
   if (!(temperature >= SPEC_LOGPROB_MIN_TEMPERATURE) || !(temperature <= 3.402823466e38f))
     return SPEC_ERR_INVALID_ARG;
   if (row_pitch < V) return SPEC_ERR_INVALID_ARG;
@@ -845,8 +854,8 @@ extern "C" int spec_token_logprobs(const void* logits, spec_dtype dtype, int32_t
   job.V = V;
   job.G = G;
   job.k = k;
-  job.c = (float)(1.4426950408889634 / (double)temperature);
-  job.inv_t = (float)(1.0 / (double)temperature);
+  job.c = (float)(16.0 * 1.4426950408889634 / (double)temperature);
+  job.inv_t = (float)(16.0 / (double)temperature);
   job.rows = rows;
   job.tokens = tokens;
   job.out_lp = out_logprobs;
