@@ -603,6 +603,14 @@ int spec_fp4_linear(const void* a_codes, const void* a_scales, const void* w_cod
                     const void* w_scales, spec_fp4_format format, int32_t R, int32_t V, int32_t K,
                     float alpha, void* out, spec_dtype dtype, int64_t row_pitch,
                     spec_stream_t stream);
+/* Self-test of those waits (for tests only): spec_fp4_linear with a limit of 20 ms, in which the last
+ * operands of one tile are not fetched.  The call completes, and the results of that tile, and of the
+ * tiles that the same CTA would take after it, are NaN.  Tiles are counted along the activations' rows
+ * first. */
+int spec_fp4_linear_test_stall(const void* a_codes, const void* a_scales, const void* w_codes,
+                               const void* w_scales, spec_fp4_format format, int32_t R, int32_t V,
+                               int32_t K, float alpha, void* out, spec_dtype dtype, int64_t row_pitch,
+                               int32_t tile, spec_stream_t stream);
 
 /*
  * spec_draft_topk_fused_lmhead with a draft LM head kept in 4 bits: the features F [R, d] (bf16,

@@ -167,6 +167,8 @@ def lib():
             L.spec_fp4_linear.argtypes = [P, P, P, P, ctypes.c_int, i32, i32, i32, F, P, ctypes.c_int,
                                           i64, P]
             L.spec_fp4_linear.restype = ctypes.c_int
+            L.spec_fp4_linear_test_stall.argtypes = L.spec_fp4_linear.argtypes[:-1] + [i32, P]
+            L.spec_fp4_linear_test_stall.restype = ctypes.c_int
             L.spec_draft_fused_fp4_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.c_int]
             L.spec_draft_fused_fp4_workspace_size.restype = ctypes.c_size_t
             L.spec_draft_topk_fused_fp4.argtypes = [P, F, P, P, ctypes.c_int, F, i32, i32, i32, i32, F, P,

@@ -53,6 +53,7 @@ cudaError_t launch_fp4_quantize(const void* x, spec_dtype dtype, int rows, int c
                                 void* codes, void* scales, cudaStream_t s);
 cudaError_t launch_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
                               const void* w_scales, spec_fp4_format format, int R, int V, int K,
-                              float alpha, void* out, spec_dtype dtype, int64_t pitch, cudaStream_t s);
+                              float alpha, void* out, spec_dtype dtype, int64_t pitch, int stall,
+                              cudaStream_t s);
 
 }  // namespace svk

@@ -15,7 +15,8 @@
 //   warps 2-5   epilogue: 32 weight rows a warp, 32 activation rows at a time, transposed in shared memory
 //               (stmatrix) and stored in bulk
 // Where weight rows are few, clusters share a tile's K instead and join in shared memory (kSplit).
-// Every wait is bounded; a tile whose accumulator does not come is written as NaN.
+// Every wait on a barrier in shared memory is bounded; a tile whose accumulator does not come is
+// written as NaN.
 //
 // What bounds it (GB300, 128256 x 4096): up to 128 rows the weight's bytes (one row nv, 295 MB: 48
 // us, 6.1 TB/s, 90 % of the copy bandwidth; 128 rows mx 51 us), from there the tensor cores: 3840
@@ -259,7 +260,7 @@ __device__ __forceinline__ void bulk_store_wait() {
 }
 
 // A bounded wait that reads the timer, which takes longer than a stage, only once the barrier has
-// been tried often.
+// been tried often (4096 attempts take 15 ms when nothing comes, and the limit starts after them).
 __device__ __forceinline__ bool fp4_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
 #pragma unroll 1
   for (int i = 0; i < 4096; ++i)
@@ -290,6 +291,11 @@ __device__ __forceinline__ void put_four(uint32_t addr, uint32_t cta, const uint
                "r"(x[3])
                : "memory");
 }
+__device__ __forceinline__ void put_word(const void* p, uint32_t cta, uint32_t x) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(a), "r"(x) : "memory");
+}
 __device__ __forceinline__ float4 get_four(uint32_t addr) {
   float4 x;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
@@ -312,11 +318,12 @@ struct LinearJob {
   void* out;
   int64_t pitch;
   uint64_t wait_limit_ns;
+  int stall;              // the tile whose last stage does not come (-1: none; the wait limits' self-test)
 };
 
 struct LinearShared {
   uint64_t full[kFlMaxStages], empty[kFlMaxStages], tfull[2], tempty[2];
-  uint32_t tmem;
+  uint32_t tmem, lost;  // lost: a part of the tile did not come (kSplit)
 };
 
 template <int CG, spec_fp4_format F, typename O, bool kSplit>
@@ -357,6 +364,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
       mbar_init(&sh.tfull[a], 1);
       mbar_init(&sh.tempty[a], 4 * CG);
     }
+    sh.lost = 0u;
     fence_barrier_init();
   }
   if (warp == 1) fp4_alloc<CG>(&sh.tmem);
@@ -379,7 +387,10 @@ __global__ void __launch_bounds__(kFlThreads, 1)
       const int n = min(job.tile_n, (job.R - n0 + 15) & ~15);
       const int row_w = ((t / job.n_tiles) * CG + rank) * kFlM, row_a = n0 + rank * (n / CG);
       const int tile_w = (row_w >> 7) * job.groups, tile_a = (n0 >> 7) * job.groups;
-      for (int kb = k0; kb < k1; ++kb, ring.next(stages)) {
+      const bool stall = t == job.stall && (!kSplit || part + 1 == job.split);
+      const int k_end = k1 - (stall ? 1 : 0);
+      stop = stall;
+      for (int kb = k0; kb < k_end; ++kb, ring.next(stages)) {
         if (!__all_sync(kFull, fp4_wait(&sh.empty[ring.s], ring.phase ^ 1u, limit))) {
           stop = true;
           break;
@@ -516,13 +527,16 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   if constexpr (kSplit) {
     // The parts of a tile along K are joined in shared memory, which the stages no longer need:
     // every CTA of the cluster owns an equal run of the activations' rows, in fours, and gets the
-    // others' parts of them. One tile per cluster.
+    // others' parts of them. One tile per cluster.  A CTA whose products did not come tells all: its
+    // copies may still be on their way to the memory where the parts are joined.
     const int quarter = warp & 3, n = job.R, own = (n + 4 * job.split - 1) / (4 * job.split);  // fours
     const int lane_v = quarter * 32 + lane, v = group * kFlM + lane_v;
     bool lost = false;
     __syncwarp();
     if (warp >= 2) lost = !__all_sync(kFull, fp4_wait(&sh.tfull[0], 0u, limit));
     cluster_sync();  // all products of the tile are done
+    if (lost && lane == 0)
+      for (int q = 0; q < job.split; ++q) put_word(&sh.lost, (uint32_t)q, 1u);
     if (warp >= 2) {
       tc05_fence_after();
 #pragma unroll 1
@@ -535,7 +549,6 @@ __global__ void __launch_bounds__(kFlThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (c0 + 4 * i < n) {
-            if (lost) x[4 * i] = x[4 * i + 1] = x[4 * i + 2] = x[4 * i + 3] = 0x7fffffffu;
             put_four(base + (uint32_t)((part * own + four) * kFlM + lane_v) * 16, (uint32_t)owner, x + 4 * i);
             if (++four == own) {
               four = 0;
@@ -550,6 +563,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
     cluster_sync();  // the parts are there
     if (warp >= 2 && v < job.V) {
       const int row0 = part * own * 4;
+      const float alpha = *reinterpret_cast<volatile uint32_t*>(&sh.lost) ? CUDART_NAN_F : job.alpha;
       for (int four = 0; four < own && row0 + four * 4 < n; ++four) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int q = 0; q < job.split; ++q) {
@@ -565,9 +579,9 @@ __global__ void __launch_bounds__(kFlThreads, 1)
         for (int i = 0; i < 4; ++i) {
           if (row0 + four * 4 + i < n) {
             if constexpr (sizeof(O) == 2)
-              reinterpret_cast<__nv_bfloat16*>(out)[i * job.pitch] = __float2bfloat16_rn(z[i] * job.alpha);
+              reinterpret_cast<__nv_bfloat16*>(out)[i * job.pitch] = __float2bfloat16_rn(z[i] * alpha);
             else
-              out[i * job.pitch] = z[i] * job.alpha;
+              out[i * job.pitch] = z[i] * alpha;
           }
         }
       }
@@ -716,14 +730,16 @@ cudaError_t launch_linear_group(const void* a, const void* a_scales, const void*
 
 cudaError_t launch_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
                               const void* w_scales, spec_fp4_format format, int R, int V, int K,
-                              float alpha, void* out, spec_dtype dtype, int64_t pitch, cudaStream_t s) {
+                              float alpha, void* out, spec_dtype dtype, int64_t pitch, int stall,
+                              cudaStream_t s) {
   LinearJob job{};
   job.R = R;
   job.V = V;
   job.alpha = alpha;
   job.out = out;
   job.pitch = pitch;
-  job.wait_limit_ns = 2000000000ull;
+  job.wait_limit_ns = stall >= 0 ? 20000000ull : 2000000000ull;
+  job.stall = stall;
   // tiles of equal numbers of rows; more than one start at multiples of 64 rows, where the scales'
   // columns in tensor memory are aligned
   job.n_tiles = (R + kFlMaxN - 1) / kFlMaxN;
@@ -744,10 +760,11 @@ cudaError_t launch_fp4_linear(const void* a_codes, const void* a_scales, const v
 
 using namespace svk;
 
-extern "C" int spec_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
-                               const void* w_scales, spec_fp4_format format, int32_t R, int32_t V,
-                               int32_t K, float alpha, void* out, spec_dtype dtype, int64_t row_pitch,
-                               spec_stream_t stream) {
+namespace {
+
+int linear_call(const void* a_codes, const void* a_scales, const void* w_codes, const void* w_scales,
+                spec_fp4_format format, int32_t R, int32_t V, int32_t K, float alpha, void* out,
+                spec_dtype dtype, int64_t row_pitch, int32_t stall, spec_stream_t stream) {
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED_DTYPE;
   if (format != SPEC_FP4_MX && format != SPEC_FP4_NV) return SPEC_ERR_UNSUPPORTED_DTYPE;
   if (R < 0 || V < 1 || K < 1 || row_pitch < V) return SPEC_ERR_INVALID_ARG;
@@ -763,7 +780,26 @@ extern "C" int spec_fp4_linear(const void* a_codes, const void* a_scales, const 
                         reinterpret_cast<uintptr_t>(out);
   if ((all & 15u) || row_pitch * (dtype == SPEC_BF16 ? 2 : 4) % 16 != 0) return SPEC_ERR_MISALIGNED;
   return launch_fp4_linear(a_codes, a_scales, w_codes, w_scales, format, R, V, K, alpha, out, dtype,
-                           row_pitch, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                           row_pitch, stall, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SPEC_OK
              : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int spec_fp4_linear(const void* a_codes, const void* a_scales, const void* w_codes,
+                               const void* w_scales, spec_fp4_format format, int32_t R, int32_t V,
+                               int32_t K, float alpha, void* out, spec_dtype dtype, int64_t row_pitch,
+                               spec_stream_t stream) {
+  return linear_call(a_codes, a_scales, w_codes, w_scales, format, R, V, K, alpha, out, dtype, row_pitch,
+                     -1, stream);
+}
+
+extern "C" int spec_fp4_linear_test_stall(const void* a_codes, const void* a_scales, const void* w_codes,
+                                          const void* w_scales, spec_fp4_format format, int32_t R,
+                                          int32_t V, int32_t K, float alpha, void* out, spec_dtype dtype,
+                                          int64_t row_pitch, int32_t tile, spec_stream_t stream) {
+  if (tile < 0) return SPEC_ERR_INVALID_ARG;
+  return linear_call(a_codes, a_scales, w_codes, w_scales, format, R, V, K, alpha, out, dtype, row_pitch,
+                     tile, stream);
 }
