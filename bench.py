@@ -904,6 +904,25 @@ def run_draft(args):
         print(json.dumps(line), flush=True)
 
 
+def fp4_head_roofline(R, V, d, k, fmt, ms, peaks, peak_kind):
+    """The draft call on a 4-bit head against the later of two floors: the bytes that its kernels
+    exchange with memory (features, codes and scales, the bf16 logits written and read back, the
+    children) at the measured copy bandwidth, and its operations at four times the measured bf16 rate
+    (no 4-bit rate is measured; the instructions' nominal ratio at K = 64 is four)."""
+    packed = V * d * (0.5 + 1.0 / (32 if fmt == "mx" else 16))
+    n_bytes = R * d * 2.0 + packed + 2.0 * R * V * 2 + R * (8.0 * k + 4)
+    flops = 2.0 * R * V * d
+    gbs, tf = n_bytes / (ms * 1e6), flops / (ms * 1e9)
+    hbm, tensor = float(peaks["hbm_gbs"]), 4.0 * float(peaks["bf16_tflops"])
+    by_bytes = gbs / hbm >= tf / tensor
+    return {"bound": "hbm" if by_bytes else "tensor", "achieved": gbs if by_bytes else tf,
+            "peak": hbm if by_bytes else tensor, "unit": "GB/s" if by_bytes else "TFLOP/s",
+            "frac": max(gbs / hbm, tf / tensor), "frac_hbm": gbs / hbm, "frac_tensor": tf / tensor, "traffic": None,
+            "kernel": "quantize_kernel + fp4_linear_kernel + draft_topk_kernel (whole call)",
+            "peak_source": f"{peak_kind} hbm_gbs" if by_bytes else f"4 x {peak_kind} bf16_tflops",
+            "algorithmic_bytes_per_launch": n_bytes, "algorithmic_flops_per_launch": flops, "avg_launch_ms": ms}
+
+
 def run_draft_fused(args):
     """Draft LM head + top-k in one call: the features of the nodes one EAGLE-2 layer
     expands (the workload's batch x 10, d = 4096, N(0, 1)) times a draft LM-head weight
@@ -996,7 +1015,7 @@ def run_draft_fused(args):
             "gpu_launches": args.steps * 2}
     if args.head != "bf16":
         line["config"]["head"] = f"4 bits ({args.head}), features quantised in the call"
-        line["roofline"].update(kernel="quantize_kernel + fp4_linear_kernel + draft_topk_kernel (whole call)")
+        line["roofline"] = fp4_head_roofline(R, V, d, k, args.head, ms, peaks, peak_kind)
         line["gpu_launches"] = args.steps * 3
     if rank == 0:
         print(json.dumps(line), flush=True)
