@@ -284,6 +284,7 @@ WALK_SOURCES = ["speculative_decoding_tree_spec_gb300/csrc/walk.cu",
                 "speculative_decoding_tree_spec_gb300/csrc/common.cuh",
                 "speculative_decoding_tree_spec_gb300/csrc/internal.h"]
 DRAFT_SOURCES = ["speculative_decoding_tree_spec_gb300/csrc/draft.cu",
+                 "speculative_decoding_tree_spec_gb300/csrc/toplist.cuh",
                  "speculative_decoding_tree_spec_gb300/csrc/common.cuh",
                  "speculative_decoding_tree_spec_gb300/csrc/internal.h"]
 

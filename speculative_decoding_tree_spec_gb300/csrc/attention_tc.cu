@@ -32,6 +32,7 @@
 // control flow runs to its end and the CTA's results become NaN.
 #include "attention.cuh"
 #include "tcgen05.cuh"
+#include "tensormap.cuh"
 
 namespace svk {
 
@@ -779,24 +780,6 @@ __global__ void __launch_bounds__(TcCfg<DP, H>::kThreads, 3 - H)
   __syncthreads();
   tc05_fence_after();
   if (warp == 1) tc05_dealloc(tmem, Cfg::kTmemCols);
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
 }
 
 // Rows of a box: the largest power of two that divides the page length, at most a block.

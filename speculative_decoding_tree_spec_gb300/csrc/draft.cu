@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "toplist.cuh"
 
 namespace svk {
 
@@ -135,50 +136,16 @@ __device__ __forceinline__ uint32_t candidate_bits(const uint4 (&raw)[kDraftUnro
   return bits;
 }
 
-// 64-bit keys held one per lane, sorted descending by a bitonic network (blocks of
-// size s alternate direction so that each pair forms a bitonic sequence; size 32 is
-// descending).
-__device__ __forceinline__ uint64_t warp_sort_desc(uint64_t x, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      const uint64_t y = __shfl_xor_sync(kFull, x, stride);
-      const bool desc = (lane & size) == 0, low = (lane & stride) == 0;
-      x = (low == desc) ? (x > y ? x : y) : (x < y ? x : y);
-    }
-  }
-  return x;
-}
-
 // The row's list (32 keys, descending, lane j holding the j-th) merged with n keys of a
-// candidate buffer by one whole warp.  A chunk of up to 32 keys is sorted, reversed
-// against the list (the lane-wise larger of the list and the reversed chunk holds the
-// 32 largest of both, as a bitonic sequence) and merged; a chunk of a few keys is
-// inserted one key at a time instead.  Returns the merged list.
+// candidate buffer by one whole warp.  A chunk of up to 32 keys is sorted and merged; a chunk
+// of a few keys is inserted one key at a time instead.  Returns the merged list.
 __device__ uint64_t merge_into_list(uint64_t L, const uint64_t* buf, int n, int k_out, int lane) {
   for (int c = 0; c < n; c += 32) {
     const int m = min(32, n - c);
     if (m <= 6) {
-      for (int i = 0; i < m; ++i) {
-        const uint64_t x = buf[c + i];
-        const int pos = __popc(__ballot_sync(kFull, L > x));
-        if (pos < k_out) {
-          const uint64_t up = __shfl_up_sync(kFull, L, 1);
-          if (lane > pos) L = up;
-          if (lane == pos) L = x;
-        }
-      }
+      for (int i = 0; i < m; ++i) L = list_insert(L, buf[c + i], k_out, lane);
     } else {
-      uint64_t x = lane < m ? buf[c + lane] : 0ull;
-      x = warp_sort_desc(x, lane);
-      const uint64_t y = __shfl_sync(kFull, x, 31 - lane);
-      L = L > y ? L : y;
-#pragma unroll
-      for (int stride = 16; stride > 0; stride >>= 1) {
-        const uint64_t o = __shfl_xor_sync(kFull, L, stride);
-        L = ((lane & stride) == 0) == (L > o) ? L : o;
-      }
+      L = list_merge(L, warp_sort_desc(lane < m ? buf[c + lane] : 0ull, lane), lane);
     }
   }
   return L;

@@ -33,6 +33,7 @@
 
 #include "fp4.cuh"
 #include "tcgen05.cuh"
+#include "tensormap.cuh"
 
 namespace svk {
 
@@ -166,13 +167,8 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(first_cta(bar))
                  : "memory");
 }
-template <int CG>
-__device__ __forceinline__ void group_sync() {
-  if constexpr (CG == 1)
-    __syncthreads();
-  else
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
-                     : "memory");
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 // The epilogue takes 32 columns (activation rows) of its 32 lanes (weight rows) at a time, leaves
@@ -280,9 +276,6 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
 // Four floats at a shared-memory address of CTA `cta` of the cluster, and of this one.
 __device__ __forceinline__ void put_four(uint32_t addr, uint32_t cta, const uint32_t* x) {
   uint32_t a;
@@ -370,7 +363,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   if (warp == 1) fp4_alloc<CG>(&sh.tmem);
   tc05_fence_before();
   __syncthreads();
-  if (CG > 1) group_sync<CG>();
+  if (CG > 1) cluster_sync();
   tc05_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
   // up to here the launch may overlap the end of the one before it, whose results are read from
@@ -590,27 +583,9 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   __syncwarp();
   tc05_fence_before();
   __syncthreads();
-  if (CG > 1) group_sync<CG>();
+  if (CG > 1) cluster_sync();
   tc05_fence_after();
   if (warp == 1) fp4_dealloc<CG>(tmem);
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
 }
 
 // Rows of codes, boxes of 128 bytes by box_rows.

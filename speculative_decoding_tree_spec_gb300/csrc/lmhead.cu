@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "tensormap.cuh"
 
 namespace svk {
 
@@ -381,24 +382,6 @@ __global__ void lmhead_combine_kernel(const TilePart* part, int M, int n_tiles, 
     stats[warp] = r;
     if (counters) atomicAdd(&counters[0], 1ull);
   }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
 }
 
 // 2-D tensor map of a row-major [rows, K] bf16 matrix, box [box_rows, 64], 128-byte swizzle.
