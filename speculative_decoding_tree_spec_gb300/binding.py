@@ -940,7 +940,8 @@ def draft_topk_fused_fp4(features: torch.Tensor, weight: Fp4Matrix, k: int, temp
                          feature_scale: float = 1.0, want_logits: bool = False, workspace=None,
                          stream=None) -> dict:
     """spec_draft_topk_fused_fp4: draft_topk_fused_lmhead with a head [V, d] kept in 4 bits; features
-    [R, d] bf16 (device, contiguous), quantised with the tensor scale feature_scale.  Returns tokens
+    [R, d] bf16 (device, contiguous), quantised with the tensor scale feature_scale (a power of two; the
+    weight's own may be any positive number in the "nv" format).  Returns tokens
     [R, k], probs [R, k], status [R] and, if asked, the bf16 logits [R, V] (a padded-pitch view)."""
     dev = features.get_device()
     if dev < 0:

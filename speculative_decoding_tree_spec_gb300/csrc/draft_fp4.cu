@@ -46,13 +46,13 @@ extern "C" int spec_draft_topk_fused_fp4(const void* features, float feature_sca
   if (R < 0 || V < 1 || d < 1 || k < 1 || k > 32 || k > V) return SPEC_ERR_INVALID_ARG;
   if (V > SPEC_MAX_VOCAB || R > SPEC_FP4_MAX_DIM || d > SPEC_FP4_MAX_DIM) return SPEC_ERR_TOO_LARGE;
   if (!(temperature > 0.0f) || !(temperature <= 3.402823466e38f)) return SPEC_ERR_INVALID_ARG;
-  if (!fp4_tensor_scale_ok(feature_scale) || !fp4_tensor_scale_ok(weight_scale) ||
+  if (!fp4_tensor_scale_ok(feature_scale) || !(weight_scale > 0.0f) ||
       (format == SPEC_FP4_MX && (feature_scale != 1.0f || weight_scale != 1.0f)))
     return SPEC_ERR_INVALID_ARG;
-  // the scales' product, a power of two, has to be a float: beyond the largest all logits would be
-  // infinite, below the smallest all 0
+  // the scales' product, 24 bits times a power of two, has to be a float: beyond the largest all
+  // logits would be infinite, below the smallest all 0
   const double alpha = (double)feature_scale * (double)weight_scale;
-  if ((double)(float)alpha != alpha) return SPEC_ERR_INVALID_ARG;
+  if (!(alpha <= 3.402823466e38) || (double)(float)alpha != alpha) return SPEC_ERR_INVALID_ARG;
   if (R == 0) return SPEC_OK;
   if (!features || !w_codes || !w_scales || !out_tokens || !out_probs || !workspace)
     return SPEC_ERR_INVALID_ARG;

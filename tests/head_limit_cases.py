@@ -17,6 +17,15 @@ SCALES = [
     (dict(feature_scale=2.0 ** -63, weight_scale=2.0 ** -63, R=0), 0),
     (dict(feature_scale=2.0 ** 100, weight_scale=2.0 ** 27, R=0), 0),
     (dict(feature_scale=2.0 ** 100, weight_scale=2.0 ** -100, R=0), 0),
+    # a weight's scale is a factor of the logits, and need not be a power of two
+    (dict(feature_scale=2.0 ** -4, weight_scale=0.0123, R=0), 0),
+    (dict(weight_scale=3e-38, R=0), 0),
+    (dict(weight_scale=1e38, R=0), 0),
+    (dict(feature_scale=4.0, weight_scale=1e38), -1),
+    (dict(feature_scale=2.0 ** -30, weight_scale=0.3e-37), -1),
+    (dict(weight_scale=-0.5), -1),
+    (dict(weight_scale=float("nan")), -1),
+    (dict(weight_scale=float("inf")), -1),
 ]
 
 # given tokens per row: the kernels count them in 32 bits, a block's threads past the last
