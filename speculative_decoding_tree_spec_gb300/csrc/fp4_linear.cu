@@ -19,8 +19,9 @@
 // written as NaN.
 //
 // What bounds it (GB300, 128256 x 4096): up to 128 rows the weight's bytes (one row nv, 295 MB: 48
-// us, 6.1 TB/s, 90 % of the copy bandwidth; 128 rows mx 51 us), from there the tensor cores: 3840
-// rows mx 576 us, 7.0 PFLOP/s, the tensor pipe 67 % active on 16384 weight rows.  What it took: the
+// us, 6.1 TB/s, 90 % of the copy bandwidth; 128 rows mx 50 us), from there the tensor cores: 3840
+// rows mx 575 to 600 us, 6.7 to 7.0 PFLOP/s; on 16384 weight rows the tensor pipe is 71 % active in mx
+// and 67 % in nv.  With K = 64 to 256 the epilogue does (3840 x 32000: bf16 76 us, f32 93).  What it took: the
 // issuing warp whole and its descriptors in uniform registers (issuing a stage took 500 cycles, its
 // products take 390), low words of descriptors computed once a stage (nv 99 -> 86 us at 3840 x
 // 16384 x 4096), the transposed epilogue (two-byte stores by lane: 1152 us instead of 983 then).

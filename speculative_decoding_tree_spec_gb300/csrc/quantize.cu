@@ -11,8 +11,10 @@
 // a midpoint between two codes that rounding it to fp32 first would take it there: the midpoints
 // times S are fp32 numbers themselves.
 //
-// Memory-bound: 8 elements per thread, 16-byte loads and 4-byte stores side by side, rows in groups
-// of four loads in flight.  Blocks share their maximum over 4 (nv: 2) lanes; the scales of four
+// 8 elements per thread, 16-byte loads and 4-byte stores side by side, rows in groups of four loads in
+// flight.  128256 x 4096 (GB300): mx bf16 202 us, memory-bound (96 % of the copy bandwidth), f32 350; nv
+// bf16 353 us, bound by issue slots (86 % active: twice mx's instructions), f32 459; back 190, 446 (f32's
+// two stores a lane), 193, 469 us.  Blocks share their maximum over 4 (nv: 2) lanes; the scales of four
 // blocks in four rows are transposed over lanes and go out as four words.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
