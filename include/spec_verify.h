@@ -619,8 +619,8 @@ int spec_fp4_linear_test_stall(const void* a_codes, const void* a_scales, const 
  * children as spec_fp4_quantize, spec_fp4_linear and spec_draft_topk give one after the other.
  * workspace: device, 256-byte aligned, spec_draft_fused_fp4_workspace_size bytes (the features in 4
  * bits and, unless out_logits is given, the logits; about 2 R V bytes; 0 for invalid sizes).
- * feature_scale as in spec_fp4_quantize; weight_scale any positive number (1 for MX: a head quantised
- * elsewhere has its own), with a product that float32 holds (else SPEC_ERR_INVALID_ARG); d a multiple of 8, bases 16-byte aligned.  Other arguments, outputs and errors
+ * feature_scale as in spec_fp4_quantize; weight_scale 1 (MX) or any positive number (NV: a factor of
+ * the logits); their product a float32 number (else SPEC_ERR_INVALID_ARG); d a multiple of 8, bases 16-byte aligned.  Other arguments, outputs and errors
  * as spec_draft_topk_fused_lmhead; SPEC_ERR_UNSUPPORTED_DTYPE for another format.  A device
  * wait that gave up makes the logits it concerns NaN, and their rows SPEC_ROW_NONFINITE.
  */
